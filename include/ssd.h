@@ -359,6 +359,145 @@ ssd_status ssd_chunk_scan_varlen_fwd_inplace_noalloc(
 ssd_status ssd_validate_inputs(const ssd_problem *prob, const int32_t *query_start_loc,
                                const uint32_t *cache_indices, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a fixed decay per head.
+ *
+ * For each head h, with group g = h / (nheads / ngroups) and lambda =
+ * exp(log_decay[h]):
+ *     S_t = lambda S_{t-1} + v[t,h,:] k[t,g,:]^T      (value_dim x key_dim)
+ *     o[t,h,:] = scale * S_t q[t,g,:]
+ * with the state reset at every query_start_loc boundary, as in the scan.
+ * The conventions at the top of this file hold here too, with these
+ * differences:
+ *   - query_start_loc[batch] may be less than total_len: the rows behind the
+ *     last sequence belong to nobody, are not read and keep their outputs.
+ *     Boundaries are clamped to 0 .. total_len on the device, so a wrong
+ *     table gives wrong results, never an access outside the tensors.
+ *   - in the in-place entry points a sequence whose cache_indices entry is
+ *     max_slots or more is padding: none of its rows, and no slot, is read
+ *     or written.  The other entries must be pairwise distinct.
+ *   - q, k and v may have a stride between tokens (slices of one projection);
+ *     everything else is dense.
+ * log_decay is a constant of the layer, normally negative; 0 is a plain sum
+ * and -infinity forgets everything but the token itself.  Activations are
+ * bf16; the states, all sums and the chain between chunks are fp32.
+ * Results are deterministic (bitwise run to run).  A NaN or infinity in one
+ * token reaches every later token of its sequence and head, and may reach
+ * the earlier ones of the same 64-token chunk; never another sequence.     */
+#define SSD_LINEAR_ATTN_MAX_DIM 256 /* largest key_dim and value_dim */
+typedef struct ssd_linear_attn_problem {
+    int64_t total_len;  /* rows of q, k, v, o; >= 0, fits int32                 */
+    int32_t batch;      /* number of sequences; >= 1                            */
+    int32_t nheads;     /* H: heads of v, o and the states; multiple of ngroups */
+    int32_t ngroups;    /* G: heads of q and k                                  */
+    int32_t key_dim;    /* K: multiple of 8, 8 .. SSD_LINEAR_ATTN_MAX_DIM       */
+    int32_t value_dim;  /* V: the same                                          */
+    int32_t max_slots;  /* leading dimension of the pool; >= 1 (in-place only)  */
+    int32_t state_dtype; /* SSD_STATE_F32 or SSD_STATE_BF16                     */
+    float scale;        /* finite                                               */
+    /* elements from one token of q, k, v to the next: a multiple of 8, at
+     * least the row itself (ngroups key_dim, or nheads value_dim), or 0 for
+     * dense tensors                                                           */
+    int64_t q_stride, k_stride, v_stride;
+} ssd_linear_attn_problem;
+
+/* Workspace of the prompt forms (backward 0) or of the backward pass
+ * (backward not 0), 256-byte aligned; 0 bytes need none.  Host only.      */
+ssd_status ssd_linear_attn_workspace_size(const ssd_linear_attn_problem *prob, int backward, size_t *bytes);
+
+/* Prompts: the chunked form over a ragged batch, pool updated in place.
+ *   o                 OUT  bf16 [T,H,V]
+ *   q, k              IN   bf16 [T,G,K]
+ *   v                 IN   bf16 [T,H,V]
+ *   log_decay         IN   fp32 [H]
+ *   pool              IN/OUT fp32 or bf16 (state_dtype) [max_slots,H,V,K]:
+ *                     the layout of ssm_pool with head_dim = V, dstate = K
+ *   query_start_loc, has_initial_state (or NULL), cache_indices: as for
+ *                     ssd_chunk_scan_varlen_fwd_inplace
+ * Errors as there (all before any launch).                                */
+ssd_status ssd_linear_attn_varlen_fwd_inplace(
+    const ssd_linear_attn_problem *prob, void *o, const void *q, const void *k, const void *v,
+    const float *log_decay, void *pool, const int32_t *query_start_loc,
+    const uint8_t *has_initial_state, const uint32_t *cache_indices,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with separate states [batch,H,V,K], as ssd_chunk_scan_varlen_fwd:
+ * initial_states may be NULL (zero) or the same buffer as final_states.   */
+ssd_status ssd_linear_attn_varlen_fwd(
+    const ssd_linear_attn_problem *prob, void *o, const void *q, const void *k, const void *v,
+    const float *log_decay, const void *initial_states, void *final_states,
+    const int32_t *query_start_loc, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of ssd_linear_attn_varlen_fwd.  With U the gradient of S:
+ *     U_T = d_final + scale d_o_T q_T^T,   U_t = lambda U_{t+1} + scale d_o_t q_t^T
+ *     dq_t = scale S_t^T d_o_t,  dk_t = U_t^T v_t,  dv_t = U_t k_t,  d_initial = lambda U_1
+ * (dq and dk summed over the heads of their group; d_initial = d_final for a
+ * sequence without tokens).
+ *   dq, dk            OUT  bf16 [T,G,K] (dense)
+ *   dv                OUT  bf16 [T,H,V] (dense)
+ *   d_initial         OUT  fp32 or bf16 (state_dtype) [batch,H,V,K], or NULL
+ *   q, k, v, log_decay, initial_states, query_start_loc: as in the forward
+ *   d_o               IN   bf16 [T,H,V] (dense)
+ *   d_final           IN   state_dtype [batch,H,V,K], or NULL (zero); may be
+ *                     the same buffer as d_initial
+ * log_decay gets no gradient.                                             */
+ssd_status ssd_linear_attn_varlen_bwd(
+    const ssd_linear_attn_problem *prob, void *dq, void *dk, void *dv, void *d_initial,
+    const void *q, const void *k, const void *v, const void *d_o, const float *log_decay,
+    const void *initial_states, const void *d_final, const int32_t *query_start_loc,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Single tokens: sequence b is the one token in row b (total_len == batch),
+ * by the recurrence, pool updated in place.  One kernel, no workspace.
+ * Arguments as for ssd_linear_attn_varlen_fwd_inplace.                    */
+ssd_status ssd_linear_attn_step_inplace(
+    const ssd_linear_attn_problem *prob, void *o, const void *q, const void *k, const void *v,
+    const float *log_decay, void *pool, const uint8_t *has_initial_state,
+    const uint32_t *cache_indices, void *stream);
+
+/* ------------------------------------------------------------------------
+ * States of a pool parked in 8 bits and read back (preempted sequences,
+ * prefixes).  Any pool [max_slots,H,P,N] of this library; each row (slot, h,
+ * p) of N elements gets one fp32 scale, and x is stored as the code nearest
+ * to x / scale:
+ *   SSD_CODE_I8    scale = max|x| / 127 rounded to fp32, whole codes -127 ..
+ *                  127, ties to even; a row whose scale would be below the
+ *                  smallest normal number is stored as zeros with scale 0
+ *   SSD_CODE_E4M3  scale = the least power of two (at least 2^-126) with
+ *                  max|x| / scale <= 448, codes in the 8-bit float format of
+ *                  4 exponent and 3 mantissa bits, ties to even; scale 0 for
+ *                  a row of zeros
+ * A row that holds an infinity or NaN reads back as NaN throughout.
+ * Element i of the call moves pool slot pool_indices[i] and cache entry
+ * entry_indices[i]; a pair with either index out of range is padding and
+ * moves nothing.  Destinations must be pairwise distinct; sources may
+ * repeat.  Other slots and entries keep their bits.                        */
+#define SSD_CODE_I8 0
+#define SSD_CODE_E4M3 1
+typedef struct ssd_state_cache_problem {
+    int32_t count;       /* pairs to move; >= 0                               */
+    int32_t nheads, head_dim; /* H, P; >= 1                                    */
+    int32_t dstate;      /* N: multiple of 8, 8 .. SSD_MAX_DSTATE             */
+    int32_t max_slots;   /* leading dimension of the pool; >= 1               */
+    int32_t max_entries; /* leading dimension of codes and scales; >= 1       */
+    int32_t state_dtype; /* SSD_STATE_F32 or SSD_STATE_BF16                   */
+    int32_t code_format; /* SSD_CODE_I8 or SSD_CODE_E4M3                      */
+} ssd_state_cache_problem;
+
+/*   codes    OUT  8-bit [max_entries,H,P,N]  (8-byte aligned)
+ *   scales   OUT  fp32 [max_entries,H,P]
+ *   pool     IN   [max_slots,H,P,N]
+ *   pool_indices, entry_indices  IN  uint32 [count]                       */
+ssd_status ssd_state_quantize(const ssd_state_cache_problem *prob, void *codes, float *scales,
+                              const void *pool, const uint32_t *pool_indices,
+                              const uint32_t *entry_indices, void *stream);
+
+/* Reads back: pool slot pool_indices[i] = codes * scale of entry
+ * entry_indices[i], rounded once to the pool's type.                      */
+ssd_status ssd_state_dequantize(const ssd_state_cache_problem *prob, void *pool, const void *codes,
+                                const float *scales, const uint32_t *pool_indices,
+                                const uint32_t *entry_indices, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

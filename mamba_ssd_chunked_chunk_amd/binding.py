@@ -26,7 +26,10 @@ EXPORTED = ("ssd_abi_version", "ssd_status_string", "ssd_workspace_size",
             "ssd_workspace_get_layout", "ssd_chunk_scan_varlen_fwd_inplace",
             "ssd_kernel_count", "ssd_kernel_name", "ssd_chunk_scan_varlen_fwd_inplace_profiled",
             "ssd_chunk_scan_varlen_fwd", "ssd_chunk_scan_varlen_fwd_profiled", "ssd_validate_inputs",
-            "ssd_chunk_scan_varlen_fwd_inplace_noalloc")
+            "ssd_chunk_scan_varlen_fwd_inplace_noalloc",
+            "ssd_linear_attn_workspace_size", "ssd_linear_attn_varlen_fwd_inplace", "ssd_linear_attn_varlen_fwd",
+            "ssd_linear_attn_varlen_bwd", "ssd_linear_attn_step_inplace", "ssd_state_quantize",
+            "ssd_state_dequantize")
 
 
 class SsdError(RuntimeError):
@@ -42,6 +45,19 @@ class ssd_problem(ctypes.Structure):
                 ("max_slots", ctypes.c_int32), ("chunk_size", ctypes.c_int32),
                 ("dt_softplus", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
                 ("short_path_max", ctypes.c_int32)]
+
+
+class ssd_linear_attn_problem(ctypes.Structure):
+    _fields_ = [("total_len", ctypes.c_int64), ("batch", ctypes.c_int32), ("nheads", ctypes.c_int32),
+                ("ngroups", ctypes.c_int32), ("key_dim", ctypes.c_int32), ("value_dim", ctypes.c_int32),
+                ("max_slots", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class ssd_state_cache_problem(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("nheads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dstate", ctypes.c_int32), ("max_slots", ctypes.c_int32), ("max_entries", ctypes.c_int32),
+                ("state_dtype", ctypes.c_int32), ("code_format", ctypes.c_int32)]
 
 
 class ssd_workspace_layout(ctypes.Structure):
@@ -66,6 +82,8 @@ NOALLOC_SCRATCH_BYTES = 64 << 20  # SSD_NOALLOC_SCRATCH_BYTES
 STATE_F32, STATE_BF16 = 0, 1  # SSD_STATE_F32, SSD_STATE_BF16
 SHORT_PATH_LIMIT = 128  # SSD_SHORT_PATH_LIMIT
 MAX_DSTATE, MAX_HEAD_DIM = 256, 1024  # SSD_MAX_DSTATE, SSD_MAX_HEAD_DIM
+LINEAR_ATTN_MAX_DIM = 256  # SSD_LINEAR_ATTN_MAX_DIM
+CODE_I8, CODE_E4M3 = 0, 1  # SSD_CODE_I8, SSD_CODE_E4M3
 SHORT_PATH_DEFAULT = -1  # ssd_problem.short_path_max: any negative value selects SHORT_PATH_LIMIT
 
 
@@ -110,6 +128,18 @@ def load_library():
             lib.ssd_chunk_scan_varlen_fwd_inplace_noalloc.argtypes = [PP] + [V] * 12 + [V]
             lib.ssd_validate_inputs.restype = ctypes.c_int
             lib.ssd_validate_inputs.argtypes = [PP, V, V, V]
+            PL = ctypes.POINTER(ssd_linear_attn_problem)
+            PC = ctypes.POINTER(ssd_state_cache_problem)
+            for name, args in (
+                    ("ssd_linear_attn_workspace_size", [PL, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+                    ("ssd_linear_attn_varlen_fwd_inplace", [PL] + [V] * 10 + [ctypes.c_size_t, V]),
+                    ("ssd_linear_attn_varlen_fwd", [PL] + [V] * 9 + [ctypes.c_size_t, V]),
+                    ("ssd_linear_attn_varlen_bwd", [PL] + [V] * 13 + [ctypes.c_size_t, V]),
+                    ("ssd_linear_attn_step_inplace", [PL] + [V] * 9),
+                    ("ssd_state_quantize", [PC] + [V] * 6),
+                    ("ssd_state_dequantize", [PC] + [V] * 6)):
+                getattr(lib, name).restype = ctypes.c_int
+                getattr(lib, name).argtypes = args
             _lib = lib
     return _lib
 
@@ -357,3 +387,265 @@ def ssd_validate_inputs(prob: ssd_problem, query_start_loc, cache_indices, strea
     st = stream if stream is not None else torch.cuda.current_stream(query_start_loc.device)
     return load_library().ssd_validate_inputs(ctypes.byref(prob), _ptr(query_start_loc),
                                               _ptr(cache_indices), ctypes.c_void_p(st.cuda_stream))
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a fixed decay per head, and the 8-bit state cache
+
+def make_linear_attn_problem(total_len, batch, nheads, ngroups, key_dim, value_dim, max_slots=1,
+                             state_dtype=STATE_F32, scale=1.0, q_stride=0, k_stride=0,
+                             v_stride=0) -> ssd_linear_attn_problem:
+    return ssd_linear_attn_problem(int(total_len), int(batch), int(nheads), int(ngroups), int(key_dim),
+                                   int(value_dim), int(max_slots), int(state_dtype), float(scale), int(q_stride),
+                                   int(k_stride), int(v_stride))
+
+
+def ssd_linear_attn_workspace_size(prob: ssd_linear_attn_problem, backward=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().ssd_linear_attn_workspace_size(ctypes.byref(prob), 1 if backward else 0, ctypes.byref(n)),
+           "ssd_linear_attn_workspace_size")
+    return n.value
+
+
+def _token_stride(t, name, shape, device):
+    """Elements between tokens of a bf16 [T, n, D] tensor whose tokens are dense rows (a slice of a wider
+    projection is one); 0 for a dense tensor."""
+    import torch
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return 0
+    T, n, D = shape
+    if (D > 1 and t.stride(2) != 1) or (n > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if T > 1 and (t.stride(0) < n * D or t.stride(0) % 8 != 0):
+        raise ValueError(f"{name}: the stride between tokens must be a multiple of 8 elements, at least {n * D}")
+    return t.stride(0) if T > 1 else 0
+
+
+def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
+    """Problem of a linear-attention call, its tensors checked."""
+    import torch
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is None or t.dim() != 3:
+            raise ValueError(f"{name} must be [T, heads, dim]")
+    dev = v.device
+    if dev.type != "cuda":
+        raise ValueError("libssd runs on a HIP device; got tensors on " + str(dev))
+    T, H, V = v.shape
+    G, K = q.shape[1], q.shape[2]
+    strides = [_token_stride(q, "q", (T, G, K), dev), _token_stride(k, "k", (T, G, K), dev),
+               _token_stride(v, "v", (T, H, V), dev)]
+    _need(log_decay, "log_decay", torch.float32, (H,), dev)
+    return make_linear_attn_problem(T, batch, H, G, K, V, max_slots, state_dtype,
+                                    K ** -0.5 if scale is None else scale, *strides), dev
+
+
+def _slots(cache_indices, has_initial_state, batch, dev):
+    import torch
+    if cache_indices.dtype not in (torch.int32, torch.uint32):
+        raise TypeError("cache_indices must be int32 or uint32")
+    if tuple(cache_indices.shape) != (batch,) or not cache_indices.is_contiguous() or cache_indices.device != dev:
+        raise ValueError("cache_indices must be a contiguous [batch] tensor on the same device")
+    if has_initial_state is None or has_initial_state.numel() == 0:
+        return None
+    if has_initial_state.dtype == torch.bool:
+        has_initial_state = has_initial_state.view(torch.uint8)
+    _need(has_initial_state, "has_initial_state", torch.uint8, (batch,), dev)
+    return has_initial_state
+
+
+class _On:
+    """The device of a call made current, and the stream it runs on."""
+
+    def __init__(self, dev, stream):
+        import torch
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        self.guard = torch.cuda.stream(self.stream)  # makes the stream's device current too
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *a):
+        return self.guard.__exit__(*a)
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, checked, or a new one (allocated on the call's stream)."""
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev:
+        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+    return workspace
+
+
+def ssd_linear_attn_varlen_fwd_inplace(o, q, k, v, log_decay, pool, query_start_loc, has_initial_state,
+                                       cache_indices, *, scale=None, workspace=None, stream=None):
+    """Linear attention with a fixed decay per head over a ragged batch, pool
+    updated in place (see include/ssd.h).
+
+    Tensors (torch, on one HIP device): o, v bf16 [T,H,V]; q, k bf16 [T,G,K]
+    (q, k and v may be slices of one projection: dense heads, a stride between
+    tokens that is a multiple of 8); log_decay fp32 [H]; pool fp32 or bf16
+    [S,H,V,K] (updated in place); query_start_loc int32 [batch+1] (rows behind
+    the last sequence are left alone); has_initial_state uint8/bool [batch] or
+    None; cache_indices int32/uint32 [batch], S or more (or negative) for a
+    padding entry.  ``scale``: None for K ** -0.5.  Runs on ``stream`` or the
+    current stream; asynchronous.  Returns the workspace tensor.
+    """
+    import torch
+    batch = query_start_loc.numel() - 1
+    sd = _state_dtype(pool, "pool")
+    prob, dev = _linear_attn(q, k, v, log_decay, batch, pool.shape[0], sd, scale)
+    _need(o, "o", torch.bfloat16, v.shape, dev)
+    _need(pool, "pool", pool.dtype, (pool.shape[0], prob.nheads, prob.value_dim, prob.key_dim), dev)
+    _need(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    has_initial_state = _slots(cache_indices, has_initial_state, batch, dev)
+    need = ssd_linear_attn_workspace_size(prob)
+    with _On(dev, stream) as st:
+        workspace = _workspace(workspace, need, dev)
+        status = load_library().ssd_linear_attn_varlen_fwd_inplace(
+            ctypes.byref(prob), _ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(pool),
+            _ptr(query_start_loc), _ptr(has_initial_state), _ptr(cache_indices), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel()), st)
+    _check(status, "ssd_linear_attn_varlen_fwd_inplace")
+    return workspace
+
+
+def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_states, query_start_loc, *, scale=None,
+                               workspace=None, stream=None):
+    """The same with separate states: sequence b starts from
+    ``initial_states[b]`` ([batch,H,V,K], or None for zero) and leaves
+    ``final_states[b]``; both fp32 or both bf16.  Returns the workspace tensor.
+    """
+    import torch
+    batch = query_start_loc.numel() - 1
+    if final_states is None:
+        raise ValueError("final_states is required")
+    sd = _state_dtype(final_states, "final_states")
+    prob, dev = _linear_attn(q, k, v, log_decay, batch, max(batch, 1), sd, scale)
+    shape = (batch, prob.nheads, prob.value_dim, prob.key_dim)
+    _need(o, "o", torch.bfloat16, v.shape, dev)
+    initial_states = _opt(initial_states, "initial_states", final_states.dtype, shape, dev)
+    _need(final_states, "final_states", final_states.dtype, shape, dev)
+    _need(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    need = ssd_linear_attn_workspace_size(prob)
+    with _On(dev, stream) as st:
+        workspace = _workspace(workspace, need, dev)
+        status = load_library().ssd_linear_attn_varlen_fwd(
+            ctypes.byref(prob), _ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_states),
+            _ptr(final_states), _ptr(query_start_loc), _ptr(workspace), ctypes.c_size_t(workspace.numel()), st)
+    _check(status, "ssd_linear_attn_varlen_fwd")
+    return workspace
+
+
+def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_decay, initial_states,
+                               d_final_states, query_start_loc, *, scale=None, workspace=None, stream=None):
+    """Backward pass of ssd_linear_attn_varlen_fwd (see include/ssd.h): dq, dk
+    bf16 [T,G,K] and dv bf16 [T,H,V] are written, and ``d_initial_states``
+    where it is not None; ``initial_states`` and ``d_final_states`` may be None
+    (zero).  State tensors [batch,H,V,K], all fp32 or all bf16.  Returns the
+    workspace tensor.
+    """
+    import torch
+    batch = query_start_loc.numel() - 1
+    states = [(t, n) for t, n in ((d_initial_states, "d_initial_states"), (initial_states, "initial_states"),
+                                  (d_final_states, "d_final_states")) if t is not None]
+    sd = _state_dtype(*states[0]) if states else STATE_F32
+    prob, dev = _linear_attn(q, k, v, log_decay, batch, max(batch, 1), sd, scale)
+    shape = (batch, prob.nheads, prob.value_dim, prob.key_dim)
+    for t, n in states:
+        _need(t, n, states[0][0].dtype, shape, dev)
+    _need(dq, "dq", torch.bfloat16, q.shape, dev)
+    _need(dk, "dk", torch.bfloat16, k.shape, dev)
+    _need(dv, "dv", torch.bfloat16, v.shape, dev)
+    _need(d_o, "d_o", torch.bfloat16, v.shape, dev)
+    _need(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    need = ssd_linear_attn_workspace_size(prob, backward=True)
+    with _On(dev, stream) as st:
+        workspace = _workspace(workspace, need, dev)
+        status = load_library().ssd_linear_attn_varlen_bwd(
+            ctypes.byref(prob), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(d_initial_states), _ptr(q), _ptr(k), _ptr(v),
+            _ptr(d_o), _ptr(log_decay), _ptr(initial_states), _ptr(d_final_states), _ptr(query_start_loc),
+            _ptr(workspace), ctypes.c_size_t(workspace.numel()), st)
+    _check(status, "ssd_linear_attn_varlen_bwd")
+    return workspace
+
+
+def ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, has_initial_state, cache_indices, *, scale=None,
+                                 stream=None):
+    """One token per sequence by the recurrence, pool updated in place (see
+    include/ssd.h): row b of o, q, k, v is sequence b's token; other arguments
+    as for ssd_linear_attn_varlen_fwd_inplace.  One kernel, no workspace.
+    """
+    import torch
+    batch = v.shape[0]
+    sd = _state_dtype(pool, "pool")
+    prob, dev = _linear_attn(q, k, v, log_decay, batch, pool.shape[0], sd, scale)
+    _need(o, "o", torch.bfloat16, v.shape, dev)
+    _need(pool, "pool", pool.dtype, (pool.shape[0], prob.nheads, prob.value_dim, prob.key_dim), dev)
+    has_initial_state = _slots(cache_indices, has_initial_state, batch, dev)
+    with _On(dev, stream) as st:
+        status = load_library().ssd_linear_attn_step_inplace(
+            ctypes.byref(prob), _ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(pool),
+            _ptr(has_initial_state), _ptr(cache_indices), st)
+    _check(status, "ssd_linear_attn_step_inplace")
+
+
+def _state_cache(pool, codes, scales, pool_indices, entry_indices):
+    """Problem of a state-cache call, its tensors checked."""
+    import torch
+    dev = pool.device
+    if dev.type != "cuda":
+        raise ValueError("libssd runs on a HIP device; got tensors on " + str(dev))
+    if pool.dim() != 4:
+        raise ValueError("pool must be [slots, H, P, N]")
+    S, H, P, N = pool.shape
+    sd = _state_dtype(pool, "pool")
+    _need(pool, "pool", pool.dtype, (S, H, P, N), dev)
+    formats = {torch.int8: CODE_I8, torch.float8_e4m3fn: CODE_E4M3}
+    if codes.dtype not in formats:
+        raise TypeError(f"codes: expected int8 or float8_e4m3fn, got {codes.dtype}")
+    E = codes.shape[0]
+    _need(codes, "codes", codes.dtype, (E, H, P, N), dev)
+    _need(scales, "scales", torch.float32, (E, H, P), dev)
+    n = pool_indices.numel()
+    for t, name in ((pool_indices, "pool_indices"), (entry_indices, "entry_indices")):
+        if t.dtype not in (torch.int32, torch.uint32):
+            raise TypeError(f"{name} must be int32 or uint32")
+        if tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous [{n}] tensor on {dev}")
+    return ssd_state_cache_problem(n, H, P, N, S, E, sd, formats[codes.dtype]), dev
+
+
+def ssd_state_quantize(codes, scales, pool, pool_indices, entry_indices, *, stream=None):
+    """Park pool slots in 8 bits: slot pool_indices[i] of ``pool`` (fp32 or
+    bf16 [S,H,P,N], of the scan or of linear attention) becomes entry
+    entry_indices[i] of ``codes`` (int8 or float8_e4m3fn [E,H,P,N]) and
+    ``scales`` (fp32 [E,H,P]).  A pair with an index out of range is skipped.
+    """
+    prob, dev = _state_cache(pool, codes, scales, pool_indices, entry_indices)
+    with _On(dev, stream) as st:
+        status = load_library().ssd_state_quantize(ctypes.byref(prob), _ptr(codes), _ptr(scales), _ptr(pool),
+                                                   _ptr(pool_indices), _ptr(entry_indices), st)
+    _check(status, "ssd_state_quantize")
+
+
+def ssd_state_dequantize(pool, codes, scales, pool_indices, entry_indices, *, stream=None):
+    """Read parked states back: slot pool_indices[i] of ``pool`` becomes entry
+    entry_indices[i] of ``codes`` times its scales."""
+    prob, dev = _state_cache(pool, codes, scales, pool_indices, entry_indices)
+    with _On(dev, stream) as st:
+        status = load_library().ssd_state_dequantize(ctypes.byref(prob), _ptr(pool), _ptr(codes), _ptr(scales),
+                                                     _ptr(pool_indices), _ptr(entry_indices), st)
+    _check(status, "ssd_state_dequantize")

@@ -1,0 +1,415 @@
+"""Linear attention with a fixed decay per head on the GPU: prompts, single
+tokens and the backward pass against the recurrence in 64 bits, within bounds
+counted from the roundings (linear_attn_testlib), and the ways of calling them."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import linear_attn_testlib as L  # noqa: E402
+from mamba_ssd_chunked_chunk_amd import binding  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def cuda(d):
+    return {k: v.cuda() for k, v in d.items()}
+
+
+def rounding(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def prompt(d, c, scale, dtype=F32, init="all", **kw):
+    """In-place prompts on the device copy `c` of `d`: o, pool, and which sequences resumed."""
+    B = d["query_start_loc"].numel() - 1
+    pool = c["pool"].to(dtype, copy=True)
+    flags = torch.tensor([init == "all" or (init == "half" and b % 2 == 0) for b in range(B)], dtype=torch.uint8)
+    o = torch.full_like(c["v"], 7.0)
+    binding.ssd_linear_attn_varlen_fwd_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool,
+                                               c["query_start_loc"], flags.cuda() if init != "none" else None,
+                                               c["cache_indices"], scale=scale, **kw)
+    return o, pool, flags
+
+
+def check_prompt(lens, H, G, K, V, seed, dtype=F32, init="all", tail=0, log_decay=None):
+    d = L.draw(lens, H, G, K, V, seed, slots=len(lens) + 2, tail=tail)
+    if log_decay is not None:
+        d["log_decay"] = log_decay
+    scale = K ** -0.5
+    c = cuda(d)
+    before = c["pool"].to(dtype).clone()
+    o, pool, flags = prompt(d, c, scale, dtype, init)
+    slots = d["cache_indices"].long()
+    initial = before.cpu()[slots].float() * flags[:, None, None, None]
+    want, final = L.reference(d, lens, scale, initial)
+    bo, bf = L.forward_bounds(d, lens, scale, initial)
+    T = sum(lens)
+    assert L.worst(o[:T], want, bo, rounding(BF16)) <= 1
+    assert bool((o[T:] == 7.0).all())  # rows behind the last sequence
+    after = pool.cpu()
+    assert L.worst(after[slots], final, bf, rounding(dtype)) <= 1
+    rest = [s for s in range(len(lens) + 2) if s not in slots.tolist()]
+    assert torch.equal(after[rest], before.cpu()[rest])
+
+
+@pytest.mark.parametrize("K,V", [(8, 8), (64, 64), (32, 128), (72, 40), (128, 64), (128, 128), (96, 200), (256, 128),
+                                 (200, 256), (256, 64)])
+def test_prompt_sizes(K, V):
+    check_prompt([70, 1, 0, 133], 3, 1, K, V, 100 + K + V)
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 500])
+def test_prompt_lengths(n):
+    check_prompt([n], 2, 2, 64, 64, 200 + n)
+
+
+@pytest.mark.parametrize("H,G", [(1, 1), (4, 4), (6, 2), (5, 1), (16, 8)])
+def test_prompt_heads(H, G):
+    check_prompt([65, 64, 3], H, G, 64, 128, 300 + H + G)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("init", ["none", "half", "all"])
+def test_prompt_states(dtype, init):
+    check_prompt([100, 0, 64, 0, 1], 2, 1, 128, 64, 400, dtype=dtype, init=init, tail=9)
+
+
+def test_prompt_many_sequences():
+    lens = [int(x) for x in torch.randint(0, 90, (150,), generator=torch.Generator().manual_seed(5))]
+    check_prompt(lens, 2, 1, 64, 64, 500, tail=3)
+
+
+@pytest.mark.parametrize("lens", [[3000], [1700, 5, 900, 2100], [64 * 40], [64 * 40 + 1, 64 * 40 - 1]])
+def test_prompt_long(lens):
+    check_prompt(lens, 2, 1, 64, 128, 600, init="half", tail=5)
+
+
+def test_decay_limits():
+    """No decay at all, a decay that forgets at once (-infinity), a state that grows, and a very strong one."""
+    ld = torch.tensor([0.0, float("-inf"), 0.01, -60.0, -1e-6, -3.0])
+    check_prompt([100, 64, 7], 6, 2, 64, 64, 700, log_decay=ld)
+
+
+def test_decay_that_forgets_is_the_token_alone():
+    d = L.draw([130], 1, 1, 64, 64, 701, slots=1)
+    d["log_decay"][:] = float("-inf")
+    o, pool, _ = prompt(d, cuda(d), 1.0)
+    q, k, v = (d[n].double() for n in "qkv")
+    want = (q * k).sum(-1, keepdim=True) * v
+    bound = (q * k).sum(-1, keepdim=True).abs() * v.abs() * (L.BF16 + L.FP32) + (q * k).abs().sum(-1, keepdim=True) * v.abs() * L.FP32
+    assert L.worst(o, want, bound, rounding(BF16)) <= 1
+    last = v[-1][:, :, None] * k[-1][:, None, :]
+    assert L.worst(pool[d["cache_indices"].long().cuda()], last[None], last.abs()[None] * L.FP32, 0.0) <= 1
+
+
+@pytest.mark.parametrize("lens", [[100, 37, 64], [700, 1300]])
+def test_padding_entries_and_unread_slots(lens):
+    """Entries of max_slots or more move nothing; a slot that no flag marks is not read (NaN there stays out)."""
+    d = L.draw(lens, 2, 1, 64, 64, 800, slots=4)
+    d["pool"][:] = float("nan")
+    c = cuda(d)
+    c["cache_indices"][1] = -1 if len(lens) == 3 else 4
+    o, pool, _ = prompt(d, c, 0.125, init="none")
+    want, final = L.reference(d, lens, 0.125)
+    bo, bf = L.forward_bounds(d, lens, 0.125)
+    keep = torch.ones(sum(lens), dtype=torch.bool)
+    keep[lens[0]:lens[0] + lens[1]] = False
+    assert L.worst(o.cpu()[keep], want[keep], bo[keep], rounding(BF16)) <= 1
+    assert bool((o.cpu()[~keep] == 7.0).all())
+    live = [b for b in range(len(lens)) if b != 1]
+    slots = d["cache_indices"].long()
+    assert L.worst(pool[slots[live].cuda()], final[live], bf[live], rounding(F32)) <= 1
+    others = [s for s in range(4) if s not in slots[live].tolist()]
+    assert bool(torch.isnan(pool[others]).all())
+
+
+def test_no_rows_at_all():
+    d = L.draw([0, 0], 2, 1, 64, 64, 810, slots=2)
+    c = cuda(d)
+    o, pool, _ = prompt(d, c, 1.0)
+    assert o.numel() == 0 and torch.equal(pool, c["pool"])
+
+
+def test_nan_stays_in_its_sequence_and_head():
+    lens = [70, 70, 70]
+    d = L.draw(lens, 2, 2, 64, 64, 820, slots=3)
+    clean, _, _ = prompt(d, cuda(d), 1.0)
+    d["v"][70 + 30, 1] = float("nan")
+    d["k"][70 + 66, 1] = float("inf")
+    o, pool, _ = prompt(d, cuda(d), 1.0)
+    same = torch.ones(210, 2, dtype=torch.bool)
+    same[70:140, 1] = False
+    assert torch.equal(o.cpu()[same], clean.cpu()[same])
+    assert bool(torch.isnan(o[100:140, 1]).all())
+
+
+def test_slices_of_one_projection():
+    lens, H, G, K, V = [90, 150], 4, 2, 64, 64
+    d = L.draw(lens, H, G, K, V, 830, slots=2)
+    c = cuda(d)
+    T = sum(lens)
+    fused = torch.cat([c["q"].reshape(T, -1), c["k"].reshape(T, -1), c["v"].reshape(T, -1),
+                       torch.zeros(T, 8, dtype=BF16, device="cuda")], 1)
+    q, k, v = fused[:, :G * K], fused[:, G * K:2 * G * K], fused[:, 2 * G * K:2 * G * K + H * V]
+    e = dict(c, q=q.view(T, G, K), k=k.view(T, G, K), v=v.view(T, H, V))
+    a, pa, _ = prompt(d, c, 0.3)
+    o = torch.empty(T, H, V, dtype=BF16, device="cuda")
+    pb = c["pool"].clone()
+    binding.ssd_linear_attn_varlen_fwd_inplace(o, e["q"], e["k"], e["v"], c["log_decay"], pb, c["query_start_loc"],
+                                               torch.ones(2, dtype=torch.bool, device="cuda"), c["cache_indices"],
+                                               scale=0.3)
+    assert torch.equal(a, o) and torch.equal(pa, pb)
+    grads = [[torch.empty_like(c["q"]), torch.empty_like(c["k"]), torch.empty_like(c["v"])] for _ in range(2)]
+    for g, x in zip(grads, (c, e)):
+        binding.ssd_linear_attn_varlen_bwd(*g, None, x["q"], x["k"], x["v"], c["d_o"], c["log_decay"], None, None,
+                                           c["query_start_loc"])
+    assert all(torch.equal(x, y) for x, y in zip(*grads))
+    g = [torch.empty(2, H, V, dtype=BF16, device="cuda") for _ in range(2)]
+    pools = [c["pool"].clone() for _ in range(2)]
+    for x, o2, p2 in zip((c, e), g, pools):
+        binding.ssd_linear_attn_step_inplace(o2, x["q"][:2], x["k"][:2], x["v"][:2], c["log_decay"], p2, None,
+                                             c["cache_indices"])
+    assert torch.equal(*g) and torch.equal(*pools)
+
+
+def test_separate_states_equal_the_pool():
+    lens = [200, 0, 65]
+    d = L.draw(lens, 4, 2, 128, 64, 840, slots=3)
+    c = cuda(d)
+    a, pool, _ = prompt(d, c, 0.1)
+    slots = c["cache_indices"].long()
+    initial = c["pool"][slots].contiguous()
+    o, final = torch.empty_like(a), torch.empty_like(initial)
+    binding.ssd_linear_attn_varlen_fwd(o, c["q"], c["k"], c["v"], c["log_decay"], initial, final,
+                                       c["query_start_loc"], scale=0.1)
+    assert torch.equal(o, a) and torch.equal(final, pool[slots])
+    # the same buffer for both, and no initial states
+    binding.ssd_linear_attn_varlen_fwd(o, c["q"], c["k"], c["v"], c["log_decay"], initial, initial,
+                                       c["query_start_loc"], scale=0.1)
+    assert torch.equal(initial, final)
+    binding.ssd_linear_attn_varlen_fwd(o, c["q"], c["k"], c["v"], c["log_decay"], None, final, c["query_start_loc"],
+                                       scale=0.1)
+    want, f = L.reference(d, lens, 0.1)
+    bo, bf = L.forward_bounds(d, lens, 0.1)
+    assert L.worst(o, want, bo, rounding(BF16)) <= 1 and L.worst(final, f, bf, rounding(F32)) <= 1
+
+
+# ------------------------------------------------------------------ single tokens
+
+@pytest.mark.parametrize("K,V", [(8, 8), (64, 64), (128, 128), (72, 40), (256, 200), (96, 256)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step(K, V, dtype):
+    B, H, G = 5, 6, 2
+    d = L.draw([1] * B, H, G, K, V, 900 + K + V, slots=B + 2)
+    c = cuda(d)
+    pool = c["pool"].to(dtype)
+    before = pool.cpu()
+    flags = torch.tensor([1, 0, 1, 1, 0], dtype=torch.uint8)
+    o = torch.full_like(c["v"], 7.0)
+    idx = c["cache_indices"].clone()
+    idx[3] = B + 2  # padding
+    binding.ssd_linear_attn_step_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool, flags.cuda(), idx, scale=0.2)
+    slots = d["cache_indices"].long()
+    initial = before[slots].float() * flags[:, None, None, None]
+    want, final = L.reference(d, [1] * B, 0.2, initial)
+    _, A = zip(*(L.magnitudes(L.spread(d["q"][b:b + 1].double(), H), L.spread(d["k"][b:b + 1].double(), H),
+                              d["v"][b:b + 1].double(), torch.exp(d["log_decay"].double()), 1.0, 1.0, 1.0,
+                              initial[b].double()) for b in range(B)))
+    A = torch.stack(A)
+    # fp32 throughout: decay, product and sum of an element, then K products and their sum
+    bs = A * 2.0 ** -24 * 4
+    bo = 0.2 * (A * L.spread(d["q"].double(), H).abs()[:, :, None, :]).sum(-1) * 2.0 ** -24 * (K + 8)
+    live = [0, 1, 2, 4]
+    assert L.worst(o[live], want[live], bo[live], rounding(BF16)) <= 1
+    assert L.worst(pool.cpu()[slots[live]], final[live], bs[live], rounding(dtype)) <= 1
+    assert bool((o[3] == 7.0).all())
+    rest = [s for s in range(B + 2) if s not in slots[live].tolist()]
+    assert torch.equal(pool.cpu()[rest], before[rest])
+
+
+def test_step_continues_a_prompt():
+    """A prompt of n tokens and m single steps are the prompt of n + m tokens."""
+    n, m, H, G, K, V = 77, 5, 4, 2, 128, 128
+    d = L.draw([n + m], H, G, K, V, 950, slots=3)
+    c = cuda(d)
+    slots, scale = c["cache_indices"], K ** -0.5
+    pool = c["pool"].clone()
+    o = torch.empty_like(c["v"])
+    qsl = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    binding.ssd_linear_attn_varlen_fwd_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool, qsl, None, slots)
+    one = torch.ones(1, dtype=torch.uint8, device="cuda")
+    for t in range(n, n + m):
+        binding.ssd_linear_attn_step_inplace(o[t:t + 1], c["q"][t:t + 1], c["k"][t:t + 1], c["v"][t:t + 1],
+                                             c["log_decay"], pool, one, slots)
+    want, final = L.reference(d, [n + m], scale)
+    bo, bf = L.forward_bounds(d, [n + m], scale)
+    assert L.worst(o, want, bo, rounding(BF16)) <= 1
+    assert L.worst(pool[slots.long()], final, 2 * bf, rounding(F32)) <= 1
+
+
+# ------------------------------------------------------------------ backward
+
+def check_backward(lens, H, G, K, V, seed, dtype=F32, initial=True, final=True, tail=0, log_decay=None):
+    d = L.draw(lens, H, G, K, V, seed, tail=tail)
+    if log_decay is not None:
+        d["log_decay"] = log_decay
+    scale = K ** -0.5
+    d["initial"], d["d_final"] = d["initial"].to(dtype), d["d_final"].to(dtype)
+    c = cuda(d)
+    dq, dk, dv = (torch.full_like(c[n], 7.0) for n in "qkv")
+    di = torch.full_like(c["initial"], 7.0)
+    binding.ssd_linear_attn_varlen_bwd(dq, dk, dv, di, c["q"], c["k"], c["v"], c["d_o"], c["log_decay"],
+                                       c["initial"] if initial else None, c["d_final"] if final else None,
+                                       c["query_start_loc"], scale=scale)
+    i, f = d["initial"].float() if initial else None, d["d_final"].float() if final else None
+    want = L.gradients(d, lens, scale, i, f)
+    bounds = L.backward_bounds(d, lens, scale, i, f)
+    T = sum(lens)
+    for name, got, w, b, t in zip(("dq", "dk", "dv", "d_initial"), (dq[:T], dk[:T], dv[:T], di), want, bounds,
+                                  (BF16, BF16, BF16, dtype)):
+        assert L.worst(got, w, b, rounding(t)) <= 1, name
+    assert all(bool((x[T:] == 7.0).all()) for x in (dq, dk, dv))  # rows behind the last sequence
+
+
+@pytest.mark.parametrize("K,V", [(8, 8), (64, 64), (128, 128), (96, 200), (64, 256), (256, 72)])
+def test_backward_sizes(K, V):
+    check_backward([70, 1, 0, 129], 3, 3, K, V, 1000 + K + V)
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 33, 63, 64, 65, 128, 200, 900])
+def test_backward_lengths(n):
+    check_backward([n], 2, 2, 64, 64, 1100 + n)
+
+
+@pytest.mark.parametrize("H,G", [(6, 2), (4, 1), (5, 5)])
+def test_backward_shared_heads(H, G):
+    check_backward([65, 64, 3], H, G, 64, 128, 1200 + H, tail=4)
+
+
+@pytest.mark.parametrize("initial,final,dtype", [(False, False, F32), (True, False, F32), (False, True, F32),
+                                                 (True, True, BF16)])
+def test_backward_states(initial, final, dtype):
+    check_backward([100, 0, 65], 2, 1, 128, 64, 1300, dtype=dtype, initial=initial, final=final)
+
+
+@pytest.mark.parametrize("lens", [[2500], [1500, 3, 900, 1800]])
+def test_backward_long(lens):
+    check_backward(lens, 2, 1, 64, 128, 1350)
+
+
+def test_backward_decay_limits():
+    ld = torch.tensor([0.0, float("-inf"), 0.01, -60.0])
+    check_backward([100, 64, 7], 4, 2, 64, 64, 1400, log_decay=ld)
+
+
+def test_backward_states_in_one_buffer():
+    d = L.draw([80, 130], 2, 2, 64, 64, 1410)
+    c = cuda(d)
+    out = []
+    for shared in (False, True):
+        g = [torch.empty_like(c[n]) for n in "qkv"]
+        df = c["d_final"].clone()
+        di = df if shared else torch.empty_like(df)
+        binding.ssd_linear_attn_varlen_bwd(*g, di, c["q"], c["k"], c["v"], c["d_o"], c["log_decay"], None, df,
+                                           c["query_start_loc"])
+        out.append(g + [di])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_backward_against_differences():
+    """Central differences of the device's own forward pass along random directions: its loss is linear in v and in
+    the initial states, and linear in q and in k one at a time, so a difference is exact but for the outputs' bf16."""
+    lens, scale = [150, 70], 0.1
+    d = L.draw(lens, 2, 1, 64, 64, 1420)
+    c = cuda(d)
+    dq, dk, dv = (torch.empty_like(c[n]) for n in "qkv")
+    binding.ssd_linear_attn_varlen_bwd(dq, dk, dv, None, c["q"], c["k"], c["v"], c["d_o"], c["log_decay"], None, None,
+                                       c["query_start_loc"], scale=scale)
+
+    def run(x):
+        o = torch.empty_like(c["v"])
+        f = torch.empty_like(c["initial"])
+        binding.ssd_linear_attn_varlen_fwd(o, x["q"], x["k"], x["v"], c["log_decay"], None, f, c["query_start_loc"],
+                                           scale=scale)
+        return o.double()
+
+    g = torch.Generator().manual_seed(3)
+    for name, grad in (("q", dq), ("k", dk), ("v", dv)):
+        step = torch.randn(c[name].shape, generator=g).bfloat16().cuda()
+        # linear: the change along `step` is the output with `step` in the input's place
+        change = run(dict(c, **{name: step}))
+        want = (change * c["d_o"].double()).sum().item()
+        got = (grad.double() * step.double()).sum().item()
+        # each side's values carry at most two roundings of 2^-8 (operand and result), of random sign: the sums of
+        # n of them differ by a normal deviate of at most 2 * 2^-8 sqrt(sum of squares); five of those
+        noise = (change * c["d_o"].double()).square().sum().sqrt() + (grad.double() * step.double()).square().sum().sqrt()
+        assert abs(got - want) <= 5 * 2 * L.BF16 * noise.item(), name
+
+
+# ------------------------------------------------------------------ ways of calling
+
+def _all_calls(c, lens):
+    """Every operator once on fresh outputs: a list of tensors."""
+    B = len(lens)
+    o, pool, _ = prompt(c, c, 0.2, init="none")
+    dq, dk, dv = (torch.empty_like(c[n]) for n in "qkv")
+    di = torch.empty_like(c["initial"])
+    binding.ssd_linear_attn_varlen_bwd(dq, dk, dv, di, c["q"], c["k"], c["v"], c["d_o"], c["log_decay"], c["initial"],
+                                       c["d_final"], c["query_start_loc"], scale=0.2)
+    so = torch.empty(B, *c["v"].shape[1:], dtype=BF16, device="cuda")
+    binding.ssd_linear_attn_step_inplace(so, c["q"][:B], c["k"][:B], c["v"][:B], c["log_decay"], pool, None,
+                                         c["cache_indices"], scale=0.2)
+    return [o, pool, dq, dk, dv, di, so]
+
+
+def test_runs_are_deterministic_and_other_streams_agree():
+    lens = [900, 64, 1, 300]
+    c = cuda(L.draw(lens, 4, 2, 64, 64, 1500, slots=6))
+    a = _all_calls(c, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = _all_calls(c, lens)
+    e = _all_calls(c, lens)  # may overlap with the side stream's
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, e))
+
+
+def test_stream_argument():
+    lens = [700, 20]
+    d = L.draw(lens, 2, 1, 64, 64, 1510, slots=2)
+    c = cuda(d)
+    a, pa, _ = prompt(d, c, 0.5)
+    o, pool = torch.empty_like(a), c["pool"].clone()
+    flags = torch.ones(2, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ws = binding.ssd_linear_attn_varlen_fwd_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool,
+                                                    c["query_start_loc"], flags, c["cache_indices"], scale=0.5,
+                                                    stream=side)
+    assert ws.device == o.device
+    side.synchronize()
+    assert torch.equal(a, o) and torch.equal(pa, pool)
+
+
+def test_captured_and_replayed():
+    lens = [1000, 40, 130]
+    c = cuda(L.draw(lens, 2, 1, 64, 64, 1520, slots=4))
+    want = _all_calls(c, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _all_calls(c, lens)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _all_calls(c, lens)
+    for _ in range(4):
+        for t in got:
+            t.fill_(3.0)
+        graph.replay()
+        eager = _all_calls(c, lens)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(want, got, eager))
