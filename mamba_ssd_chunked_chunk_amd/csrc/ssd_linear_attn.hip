@@ -1,23 +1,25 @@
 // Linear attention with a fixed decay per head: the chunked form, forward
 // and (as three recurrences with exchanged roles) backward.
 //
-// A workgroup walks one sequence for one head and 32 * NW value channels, in
-// chunks of 64 tokens.  With i, j the places in a chunk, S the state that
-// enters it and lambda the head's decay,
+// A workgroup walks one segment of a sequence for one head and 16 * NW value
+// channels, in chunks of 64 tokens.  With i, j the places in a chunk, S the
+// state that enters it and lambda the head's decay,
 //     out_i = lambda^(i+1) S q_i + sum_{j <= i} lambda^(i-j) (q_i . k_j) v_j
 //     S    <- lambda^len S + sum_j lambda^(len-1-j) v_j k_j^T
-// Each wavefront owns 32 value channels and keeps S of them (32 x kd, fp32)
+// Each wavefront owns 16 value channels and keeps S of them (16 x kd, fp32)
 // in registers for the whole walk, so the state never moves; the wavefronts
 // share only the chunk's q, k, v rows and its 64 x 64 matrix of weighted
 // scores, in LDS.  Every product is computed transposed (channels x tokens):
-// a lane then holds one token and 8 consecutive channels, so its decay is a
-// scalar and its result is written 16 bytes at a time, and the state
-// registers are, as they are, the operand of the next product.
+// a lane then holds one token and consecutive channels, so its decay is a
+// scalar, and the state registers are, as they are, the operand of the next
+// product.
 //
 // Operands that run along tokens (v and k of the state update) come from LDS
-// with the transposing read, whose lanes take columns in groups of four; the
-// groups are ordered so that the accumulator's 8 registers of a lane are 8
-// consecutive channels (channel() below).
+// with the transposing read, whose lanes take columns in groups of four.  For
+// k (and for the rows of k in the scores) two tiles of 16 channels are taken
+// from 32, channels 8 g + 0..3 to the one and 8 g + 4..7 to the other, so
+// that the two accumulators of a lane together are 8 consecutive channels:
+// one 16-byte operand of the next product.
 //
 // Rounding: scores and the state are rounded to bf16 once as operands of the
 // output, which is bf16 itself.  The weighted v of the state update is split
@@ -32,15 +34,6 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
-
-__device__ __forceinline__ f32x16 mfma32_bf16(const bf16x8 &a, const bf16x8 &b, const f32x16 &c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
-// Channel (or token) that operand lane l % 32 stands for, so that accumulator
-// register e of lane half hh belongs to channel 16 (e / 8) + 8 hh + e % 8:
-// bits 2 and 3 exchanged.
-__device__ __forceinline__ int channel(int l) { return (l & 19) | ((l & 4) << 1) | ((l & 8) >> 1); }
 
 // LDS place (in 16-byte units) of unit c of row r, rows of U units: the units
 // of a row are permuted so that both a column of 16-byte reads down
@@ -59,15 +52,14 @@ __device__ __forceinline__ bf16x8 row_read(const uint16_t *s, int r, int c) {
     return *reinterpret_cast<const bf16x8 *>(s + place<U>(r, c) * 8);
 }
 
-// 8 tokens (t0 + 8 (lane / 32) ..) of the column c0 + channel(lane % 32)
+// For lane l: 8 tokens t0 + 8 (l / 16) .. of one of 16 columns.  The lanes
+// take the columns of four groups of four; group l % 4 starts at column
+// unit * 8 + half (both may depend on l % 4).
 template <int U>
-__device__ __forceinline__ bf16x8 column_read(const uint16_t *s, int t0, int c0, int lane) {
-    const int x = lane & 15;
-    const int r = t0 + 8 * (lane >> 5) + (x >> 2);
-    const int col = c0 + (lane & 16) + 4 * (((x & 1) << 1) | ((x >> 1) & 1));
-    const int c = col >> 3, half = col & 4;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + place<U>(r, c) * 8 + half));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + place<U>(r + 4, c) * 8 + half));
+__device__ __forceinline__ bf16x8 column_read(const uint16_t *s, int t0, int unit, int half, int lane) {
+    const int r = t0 + 8 * (lane >> 4) + ((lane & 15) >> 2);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + place<U>(r, unit) * 8 + half));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + place<U>(r + 4, unit) * 8 + half));
     const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     return __builtin_bit_cast(bf16x8, v);
 }
@@ -116,147 +108,270 @@ __device__ __forceinline__ void write_state(void *base, int64_t at, int64_t sk, 
     }
 }
 
-// KD: channels of k and q the kernel holds (kd rounded up; the rest is zero)
-template <int KD, int NW, bool SB>
-__global__ __launch_bounds__(64 * NW) void la_walk(Params p) {
+__device__ __forceinline__ int clamp_row(const Params &p, int t) { return min(max(t, 0), (int)p.T); }
+
+// whether sequence b of an operation starts from a stored state
+__device__ __forceinline__ bool resumes(const Params &p, const Op &op, int b) {
+    return op.state_in != nullptr && (p.init_all != 0 || (p.has_init != nullptr && p.has_init[b] != 0));
+}
+
+// The segment a workgroup takes.  Sequences are cut into segments of `seg`
+// tokens counted in walking order; slot w of the launch is segment w - first
+// of the last sequence whose first slot, qsl / seg + b, is at most w.  (A
+// sequence of n tokens has at most n / seg + 1 segments, so their slots never
+// meet the next sequence's; slots in between are empty.)  Every lane tests one
+// sequence at a time, so 64-ary search finds it in one or two steps.
+struct Segment {
+    int b, index, count;  // sequence, segment of it, its number of segments (0: an empty slot)
+    int begin, len;       // the sequence's first token and length
+};
+__device__ __forceinline__ Segment find_segment(const Params &p, int w) {
+    const int lane = threadIdx.x & 63;
+    Segment g;
+    int lo = 0, first = 0;
+    if (p.seg == 0) {  // one segment per sequence
+        lo = w;
+        first = w;
+    } else {
+        int n = p.batch;
+        while (true) {
+            const int step = (n + 63) / 64;
+            const int i = lane * step;
+            bool at = false;
+            if (i < n) at = clamp_row(p, p.qsl[lo + i]) / p.seg + lo + i <= w;
+            const int k = __popcll(__ballot(at)) - 1;
+            if (k < 0) return Segment{0, 0, 0, 0, 0};
+            lo += k * step;
+            n = min(step, n - k * step);
+            if (n <= 1) break;
+        }
+    }
+    g.b = __builtin_amdgcn_readfirstlane(lo);
+    g.begin = __builtin_amdgcn_readfirstlane(clamp_row(p, p.qsl[g.b]));
+    g.len = max(__builtin_amdgcn_readfirstlane(clamp_row(p, p.qsl[g.b + 1])) - g.begin, 0);
+    if (p.seg == 0) {
+        g.index = 0;
+        g.count = 1;
+    } else {
+        g.index = w - (g.begin / p.seg + g.b);
+        g.count = max((g.len + p.seg - 1) / p.seg, 1);
+        if (g.index >= g.count) g.count = 0;
+    }
+    return g;
+}
+
+// Raw buffer over the rows of one chunk: rows past it read as zero and are
+// not stored.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, kBufferFormat32);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every such buffer
+
+// Wavefronts per SIMD that the registers of a variant allow.
+constexpr int waves_of(int KD, int NW) { return 2; }
+
+// KD: channels of k and q the kernel holds (kd rounded up; the rest is zero).
+// LOCAL: only the state a segment leaves when it starts from zero.
+template <int KD, int NW, bool SB, bool LOCAL>
+__global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     constexpr int NTH = 64 * NW;
     constexpr int UK = KD / 8;       // 16-byte units of a q or k row
-    constexpr int VT = 32 * NW;      // value channels of the workgroup
+    constexpr int VT = 16 * NW;      // value channels of the workgroup
     constexpr int UV = VT / 8;
-    constexpr int NT = KD / 32;      // 32 x 32 tiles of a wavefront's state
+    constexpr int NT = KD / 32;      // blocks of 32 k channels of a wavefront's state
     constexpr int LK = kTok * UK / NTH, LV = kTok * UV / NTH;  // 16-byte loads of a thread
-    __shared__ __attribute__((aligned(16))) uint16_t s_q[kTok * KD];
+    constexpr int RK = NTH / UK, RV = NTH / UV;                // rows between them
+    __shared__ __attribute__((aligned(16))) uint16_t s_q[LOCAL ? 8 : kTok * KD];
     __shared__ __attribute__((aligned(16))) uint16_t s_k[kTok * KD];
     __shared__ __attribute__((aligned(16))) uint16_t s_v[kTok * VT];
-    __shared__ __attribute__((aligned(16))) uint16_t s_p[kTok * kTok];
+    __shared__ __attribute__((aligned(16))) uint16_t s_p[LOCAL ? 8 : kTok * kTok];
 
-    const Op &op = p.op[blockIdx.z];
-    const int v0 = blockIdx.y * VT;
+    // Consecutive workgroups go to the 8 XCDs in turn.  The workgroups that
+    // read the same rows (a group's heads, their blocks of channels, the
+    // recurrences) stay on one XCD, and its L2.
+    const int together = p.share * p.tiles * p.nops;
+    const int run = (int)blockIdx.x / 8;
+    int id = (run / together * 8 + (int)(blockIdx.x % 8)) * together + run % together;
+    if (id >= p.slots * p.H * p.tiles * p.nops) return;
+    const int which = id % p.nops;
+    id /= p.nops;
+    const int v0 = (id % p.tiles) * VT;
+    id /= p.tiles;
+    const int h = id % p.H, w = id / p.H;
+    const Op &op = p.op[which];
     if (v0 >= op.vd) return;
-    const int h = blockIdx.x % p.H, b = blockIdx.x / p.H;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hh = lane >> 5, l32 = lane & 31;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[b] : (int64_t)b;
+    const Segment g = find_segment(p, w);
+    if (g.count == 0 || (LOCAL && g.index == g.count - 1)) return;
+    const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[g.b] : (int64_t)g.b;
     if (slot >= p.max_slots) return;  // padding
-    const int64_t begin = min(max((int64_t)p.qsl[b], (int64_t)0), p.T);
-    const int64_t end = max(min((int64_t)p.qsl[b + 1], p.T), begin);
+    // the segment's tokens: n of them, from t0 upwards
+    const int skip = p.seg == 0 ? 0 : g.index * p.seg;
+    const int n = p.seg == 0 ? g.len : min(p.seg, g.len - skip);
     const bool rev = op.reverse != 0;
+    const int64_t t0 = rev ? g.begin + g.len - skip - n : g.begin + skip;
     // log2 of the decay; -infinity as a finite number, so that times 0 it is 0
     const float ld = p.log_decay[h] * kLog2e;
     const float l2 = ld < -1e30f ? -1e30f : ld;
     const float shift = rev ? 1.f : 0.f;
 
-    // ---- the state: registers e of tile t hold (v channel sv_i, k channel
-    // 32 t + 16 (e / 8) + 8 hh + e % 8)
-    const int vch = v0 + 32 * wave + channel(l32);
+    // ---- the state: register 4 y + e (y 0, 1) of block t holds v channel vch
+    // and k channel 32 t + 8 q4 + 4 y + e
+    const int vch = v0 + 16 * wave + l16;
     const bool vch_in = vch < op.vd;
     const int64_t state_at = (slot * p.H + h) * p.state_size + (int64_t)vch * op.sv;
-    f32x16 S[NT];
-    const bool init = op.state_in != nullptr && (p.init_all != 0 || (p.has_init != nullptr && p.has_init[b] != 0));
+    // the wavefront's part of the segment's slot in the workspace
+    f32x4 *const part = reinterpret_cast<f32x4 *>(
+        p.parts + ((((int64_t)which * p.slots + w) * p.H + h) * p.tiles * VT + v0 + 16 * wave) * KD) + lane;
+    f32x4 S[NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) S[t][0] = S[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (!LOCAL) {
+        if (g.count > 1) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int kc = 32 * t + 16 * x + 8 * hh;
-            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (init && vch_in && kc < op.kd) read_state<SB>(op.state_in, state_at + kc * op.sk, op.sk, f);
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) S[t][8 * x + e] = f[e];
+                for (int y = 0; y < 2; ++y) S[t][y] = part[(t * 2 + y) * 64];
+        } else if (resumes(p, op, g.b) && vch_in) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int kc = 32 * t + 8 * q4;
+                if (kc >= op.kd) continue;
+                float f[8];
+                read_state<SB>(op.state_in, state_at + kc * op.sk, op.sk, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) S[t][e / 4][e % 4] = f[e];
+            }
         }
+    }
 
+    // ---- constants of the walk.  Place r of a chunk of len tokens is its
+    // token r - pad (pad = 64 - len), or in reverse 63 - r: a short chunk ends
+    // at the last place, where the weights of the state update are the full
+    // chunk's, and starts with rows of zeros.
+    float pair[8], lead[8];
+    const int below = 16 * (wave & 3);  // of the wavefront's blocks of scores: see there
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int d = below + l16 - (8 * q4 + e);
+        pair[e] = d >= 0 ? op.scale_pair * fast_exp2(l2 * (float)d) : 0.f;
+        lead[e] = op.scale_update * fast_exp2(l2 * ((float)(31 - 8 * q4 - e) + shift));
+    }
+    const float by32 = fast_exp2(l2 * 32.f);
+
+    const int64_t qs = op.q.stride, ks = op.k.stride, vs = op.v.stride, os = (int64_t)p.H * op.vd;
     const uint16_t *gq = op.q.p + (int64_t)(h / op.q.div) * op.kd;
     const uint16_t *gk = op.k.p + (int64_t)(h / op.k.div) * op.kd;
-    const uint16_t *gv = op.v.p + (int64_t)(h / op.v.div) * op.vd + v0;
+    const uint16_t *gv = op.v.p + (int64_t)(h / op.v.div) * op.vd;
+    const int rk = tid / UK, ck = tid % UK, rv = tid / UV, cv = tid % UV;
+    const uint32_t oq = 8 * ck < op.kd ? (uint32_t)(rk * qs + 8 * ck) * 2 : kNowhere;
+    const uint32_t ok = 8 * ck < op.kd ? (uint32_t)(rk * ks + 8 * ck) * 2 : kNowhere;
+    const uint32_t ov = v0 + 8 * cv < op.vd ? (uint32_t)(rv * vs + v0 + 8 * cv) * 2 : kNowhere;
+
+    u32x4 fq[LOCAL ? 1 : LK], fk[LK], fv[LV];
+    auto fetch = [&](int c0) {  // the chunk's rows, lowest token first, into registers
+        const int len = min(kTok, n - c0);
+        const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
+        const auto bk = rows_buffer(gk + first * ks, (uint32_t)((len - 1) * ks + op.kd) * 2);
+        const auto bv = rows_buffer(gv + first * vs, (uint32_t)((len - 1) * vs + op.vd) * 2);
+#pragma unroll
+        for (int i = 0; i < LK; ++i)
+            fk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, ok + i * RK * (uint32_t)ks * 2, 0, 0);
+#pragma unroll
+        for (int i = 0; i < LV; ++i)
+            fv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, ov + i * RV * (uint32_t)vs * 2, 0, 0);
+        if constexpr (!LOCAL) {
+            const auto bq = rows_buffer(gq + first * qs, (uint32_t)((len - 1) * qs + op.kd) * 2);
+#pragma unroll
+            for (int i = 0; i < LK; ++i)
+                fq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, oq + i * RK * (uint32_t)qs * 2, 0, 0);
+        }
+    };
+    if (n > 0) fetch(0);
 
 #pragma unroll 1
-    for (int64_t c0 = 0; c0 < end - begin; c0 += kTok) {
-        const int len = (int)min((int64_t)kTok, end - begin - c0);
-        // place r of the chunk is token first + r * dir
-        const int64_t first = rev ? end - 1 - c0 : begin + c0;
-        const int dir = rev ? -1 : 1;
+    for (int c0 = 0; c0 < n; c0 += kTok) {
+        const int len = min(kTok, n - c0), pad = kTok - len;
+        const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
         __syncthreads();  // the previous chunk's rows are no longer read
+        // token i of the chunk to its place; tokens past it (zeros) wrap to the places before it
 #pragma unroll
-        for (int n = 0; n < LK; ++n) {
-            const int r = (tid + n * NTH) / UK, c = (tid + n * NTH) % UK;
-            u32x4 wq = {0, 0, 0, 0}, wk = {0, 0, 0, 0};
-            if (r < len && 8 * c < op.kd) {
-                const int64_t t = first + r * dir;
-                wq = *reinterpret_cast<const u32x4 *>(gq + t * op.q.stride + 8 * c);
-                wk = *reinterpret_cast<const u32x4 *>(gk + t * op.k.stride + 8 * c);
-            }
-            *reinterpret_cast<u32x4 *>(s_q + place<UK>(r, c) * 8) = wq;
-            *reinterpret_cast<u32x4 *>(s_k + place<UK>(r, c) * 8) = wk;
+        for (int i = 0; i < LK; ++i) {
+            const int r = rev ? 63 - (rk + i * RK) : (rk + i * RK + pad) & 63;
+            *reinterpret_cast<u32x4 *>(s_k + place<UK>(r, ck) * 8) = fk[i];
+            if constexpr (!LOCAL) *reinterpret_cast<u32x4 *>(s_q + place<UK>(r, ck) * 8) = fq[i];
         }
 #pragma unroll
-        for (int n = 0; n < LV; ++n) {
-            const int r = (tid + n * NTH) / UV, c = (tid + n * NTH) % UV;
-            u32x4 wv = {0, 0, 0, 0};
-            if (r < len && v0 + 8 * c < op.vd)
-                wv = *reinterpret_cast<const u32x4 *>(gv + (first + r * dir) * op.v.stride + 8 * c);
-            *reinterpret_cast<u32x4 *>(s_v + place<UV>(r, c) * 8) = wv;
+        for (int i = 0; i < LV; ++i) {
+            const int r = rev ? 63 - (rv + i * RV) : (rv + i * RV + pad) & 63;
+            *reinterpret_cast<u32x4 *>(s_v + place<UV>(r, cv) * 8) = fv[i];
         }
         __syncthreads();
+        if (c0 + kTok < n) fetch(c0 + kTok);
 
-        // ---- weighted scores, 32 x 32 tiles (rt, ct) with ct <= rt: lane =
-        // token i, registers = tokens j (as channels of the state)
+        f32x4 O[4] = {};
+        if constexpr (!LOCAL) {
+            // ---- weighted scores in blocks of 16 tokens i (lanes) x 32 tokens
+            // j (8 consecutive ones a lane): blocks (rt, c) = (0,0) (1,0) (2,0)
+            // (3,0) (2,1) (3,1).  Wavefront m takes block m, and with four
+            // of them 0 and 1 also 4 and 5, which lie as far below the diagonal
 #pragma unroll
-        for (int tile = 0; tile < 3; ++tile) {
-            if (tile % NW != wave) continue;
-            const int rt = tile == 0 ? 0 : 1, ct = tile == 2 ? 1 : 0;
-            f32x16 a = {};
+            for (int m = 0; m < 6; ++m) {
+                if (m % NW != wave) continue;
+                const int rt = m < 4 ? m : m - 2, c = m < 4 ? 0 : 1;
+                f32x4 a[2] = {};
 #pragma unroll
-            for (int u = 0; u < KD / 16; ++u)
-                a = mfma32_bf16(row_read<UK>(s_k, 32 * ct + channel(l32), 2 * u + hh),
-                                row_read<UK>(s_q, 32 * rt + l32, 2 * u + hh), a);
-            const int i = 32 * rt + l32;
+                for (int u = 0; u < KD / 32; ++u) {
+                    const bf16x8 q = row_read<UK>(s_q, 16 * rt + l16, 4 * u + q4);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float f[8];
-                const int j0 = 32 * ct + 16 * x + 8 * hh;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int d = i - (j0 + e);
-                    f[e] = d >= 0 ? a[8 * x + e] * (op.scale_pair * fast_exp2(l2 * (float)d)) : 0.f;
+                    for (int y = 0; y < 2; ++y)
+                        a[y] = mfma_bf16(row_read<UK>(s_k, 32 * c + 8 * (l16 >> 2) + 4 * y + (l16 & 3), 4 * u + q4), q,
+                                         a[y]);
                 }
-                *reinterpret_cast<bf16x8 *>(s_p + place<8>(i, j0 / 8) * 8) = pack8(f);
-            }
-        }
-
-        // ---- output from the state, out^T = S q^T (channels x tokens)
-        f32x16 O[2] = {};
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
                 float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = S[t][8 * x + e];
+                for (int e = 0; e < 8; ++e) f[e] = a[e / 4][e % 4] * pair[e];
+                *reinterpret_cast<bf16x8 *>(s_p + place<8>(16 * rt + l16, 4 * c + q4) * 8) = pack8(f);
+            }
+            // ---- output from the state, out^T = S q^T (channels x tokens)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][e % 4];
                 const bf16x8 a = pack8(f);
 #pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
-                    O[rt] = mfma32_bf16(a, row_read<UK>(s_q, 32 * rt + l32, 4 * t + 2 * x + hh), O[rt]);
+                for (int rt = 0; rt < 4; ++rt)
+                    O[rt] = mfma_bf16(a, row_read<UK>(s_q, 16 * rt + l16, 4 * t + q4), O[rt]);
             }
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt)
-            O[rt] *= op.scale_state * fast_exp2(l2 * ((float)(32 * rt + l32) + 1.f - shift));
-        __syncthreads();  // scores complete
+            for (int rt = 0; rt < 4; ++rt)
+                O[rt] *= op.scale_state * fast_exp2(l2 * ((float)(16 * rt + l16 - pad + 1) - shift));
+            __syncthreads();  // scores complete
+        }
 
-        // ---- output from the chunk, and the state update, 16 tokens at a time
+        // ---- output from the chunk, and the state update, 32 tokens at a time
         const float keep = fast_exp2(l2 * (float)len);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S[t] *= keep;
+        for (int t = 0; t < NT; ++t) {
+            S[t][0] *= keep;
+            S[t][1] *= keep;
+        }
 #pragma unroll
-        for (int u = 0; u < kTok / 16; ++u) {
-            const bf16x8 v = column_read<UV>(s_v, 16 * u, 32 * wave, lane);
-            if (u < 2) O[0] = mfma32_bf16(v, row_read<8>(s_p, l32, 2 * u + hh), O[0]);
-            O[1] = mfma32_bf16(v, row_read<8>(s_p, 32 + l32, 2 * u + hh), O[1]);
+        for (int u = 0; u < kTok / 32; ++u) {
+            const int x4 = lane & 3;
+            const bf16x8 v = column_read<UV>(s_v, 32 * u, 2 * wave + (x4 >> 1), 4 * (x4 & 1), lane);
+            if constexpr (!LOCAL) {
+#pragma unroll
+                for (int rt = 2 * u; rt < 4; ++rt)
+                    O[rt] = mfma_bf16(v, row_read<8>(s_p, 16 * rt + l16, 4 * u + q4), O[rt]);
+            }
             float f[8], r[8];
             unpack8(v, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = max(len - 1 - (16 * u + 8 * hh + e), 0);
-                f[e] *= op.scale_update * fast_exp2(l2 * ((float)d + shift));
-            }
+            for (int e = 0; e < 8; ++e) f[e] *= u == 0 ? lead[e] * by32 : lead[e];
             const bf16x8 w1 = pack8(f);
             unpack8(w1, r);
 #pragma unroll
@@ -268,46 +383,101 @@ __global__ __launch_bounds__(64 * NW) void la_walk(Params p) {
             const bf16x8 w3 = pack8(f);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const bf16x8 k = column_read<UK>(s_k, 16 * u, 32 * t, lane);
-                S[t] = mfma32_bf16(k, w3, S[t]);
-                S[t] = mfma32_bf16(k, w2, S[t]);
-                S[t] = mfma32_bf16(k, w1, S[t]);
+                const bf16x8 k0 = column_read<UK>(s_k, 32 * u, 4 * t + x4, 0, lane);
+                const bf16x8 k1 = column_read<UK>(s_k, 32 * u, 4 * t + x4, 4, lane);
+                S[t][0] = mfma_bf16(k0, w3, S[t][0]);
+                S[t][1] = mfma_bf16(k1, w3, S[t][1]);
+                S[t][0] = mfma_bf16(k0, w2, S[t][0]);
+                S[t][1] = mfma_bf16(k1, w2, S[t][1]);
+                S[t][0] = mfma_bf16(k0, w1, S[t][0]);
+                S[t][1] = mfma_bf16(k1, w1, S[t][1]);
             }
         }
 
-        // ---- 16-byte stores: token 32 rt + l32, channels 16 x + 8 hh ..
+        // ---- stores: place 16 rt + l16, 4 channels from 4 q4
+        if constexpr (!LOCAL) {
+            const int eb = op.out_f32 ? 4 : 2;
+            const auto bo = rows_buffer(static_cast<char *>(op.out) + (first * os + (int64_t)h * op.vd) * eb,
+                                        (uint32_t)((len - 1) * os + op.vd) * eb);
+            const int vc = v0 + 16 * wave + 4 * q4;
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-            const int r = 32 * rt + l32;
-            if (r >= len) continue;
-            const int64_t row = ((first + r * dir) * p.H + h) * op.vd;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int vc = v0 + 32 * wave + 16 * x + 8 * hh;
-                if (vc >= op.vd) continue;
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = O[rt][8 * x + e];
+            for (int rt = 0; rt < 4; ++rt) {
+                const int r = 16 * rt + l16;
+                const int tok = rev ? 63 - r : r - pad;
+                const uint32_t at =
+                    vc < op.vd && (uint32_t)tok < (uint32_t)len ? (uint32_t)(tok * os + vc) * eb : kNowhere;
                 if (op.out_f32)
-                    store_state8<false>(op.out, row + vc, f);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[rt]), bo, at, 0, 0);
                 else
-                    store_state8<true>(op.out, row + vc, f);
+                    __builtin_amdgcn_raw_buffer_store_b64(
+                        u32x2{pack_bf16x2(O[rt][0], O[rt][1]), pack_bf16x2(O[rt][2], O[rt][3])}, bo, at, 0, 0);
             }
         }
     }
 
-    if (op.state_out == nullptr || !vch_in) return;
+    if constexpr (LOCAL) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int kc = 32 * t + 16 * x + 8 * hh;
+            for (int y = 0; y < 2; ++y) part[(t * 2 + y) * 64] = S[t][y];
+    } else {
+        if (g.index != g.count - 1 || op.state_out == nullptr || !vch_in) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int kc = 32 * t + 8 * q4;
             if (kc >= op.kd) continue;
             float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = S[t][8 * x + e];
+            for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][e % 4];
             write_state<SB>(op.state_out, state_at + kc * op.sk, op.sk, f);
         }
+    }
+}
+
+// The segments' own states into the states that enter them, in place: one
+// thread per 4 state elements of a (sequence, head), in the order of the
+// walk's registers.  Sequences of one segment are left to the walk.
+template <bool SB>
+__global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
+    const int per_head = p.tiles * VT * KD / 4;  // groups of 4
+    const int blocks = (per_head + 255) / 256;
+    int id = blockIdx.x;
+    const int i = (id % blocks) * 256 + (int)threadIdx.x;
+    id /= blocks;
+    const int h = id % p.H, b = id / p.H;
+    const int which = blockIdx.y;
+    const Op &op = p.op[which];
+    if (i >= per_head) return;
+    const int begin = clamp_row(p, p.qsl[b]), len = max(clamp_row(p, p.qsl[b + 1]) - begin, 0);
+    const int count = (len + p.seg - 1) / p.seg;
+    const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[b] : (int64_t)b;
+    if (count <= 1 || slot >= p.max_slots) return;
+    const int lane = i & 63, y = (i >> 6) & 1, t = (i >> 7) % (KD / 32), wave = (i >> 7) / (KD / 32);
+    const int vch = 16 * wave + (lane & 15), kc = 32 * t + 8 * (lane >> 4) + 4 * y;
+    const bool in = vch < op.vd && kc < op.kd;
+    f32x4 S = {0.f, 0.f, 0.f, 0.f};
+    if (in && resumes(p, op, b)) {
+        const int64_t at = (slot * p.H + h) * p.state_size + (int64_t)vch * op.sv + kc * op.sk;
+        if (op.sk == 1) {
+            S = load_state4<SB>(op.state_in, at);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[e] = SB ? bf16_bits_to_float(static_cast<const uint16_t *>(op.state_in)[at + e * op.sk])
+                          : static_cast<const float *>(op.state_in)[at + e * op.sk];
+        }
+    }
+    const float ld = p.log_decay[h] * kLog2e;
+    const float keep = fast_exp2((ld < -1e30f ? -1e30f : ld) * (float)p.seg);
+    const int64_t step = (int64_t)p.H * per_head;
+    f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) +
+                  ((int64_t)which * p.slots + begin / p.seg + b) * step + (int64_t)h * per_head + i;
+    for (int s = 0; s < count - 1; ++s, part += step) {
+        const f32x4 own = *part;
+        *part = S;
+        S = S * keep + own;
+    }
+    *part = S;
 }
 
 // One thread per 8 channels of a (token, group); the sequences' rows only.
@@ -328,31 +498,52 @@ __global__ __launch_bounds__(256) void la_group_sum(const float *src, uint16_t *
     store_state8<true>(dst, i * 8, s);
 }
 
-template <int KD, int NW>
-hipError_t launch_kd(const Params &p, int nops, int tiles, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)p.batch * p.H), (unsigned)tiles, (unsigned)nops), block(64 * NW);
-    if (p.state_bf16)
-        la_walk<KD, NW, true><<<grid, block, 0, s>>>(p);
-    else
-        la_walk<KD, NW, false><<<grid, block, 0, s>>>(p);
+template <int KD, int NW, bool SB>
+hipError_t launch_kd(const Params &p, hipStream_t s) {
+    const int64_t n = (int64_t)p.slots * p.H * p.tiles * p.nops;
+    const int64_t run = (int64_t)8 * p.share * p.tiles * p.nops;
+    const dim3 grid((unsigned)((n + run - 1) / run * run)), block(64 * NW);
+    if (p.seg != 0) {
+        la_walk<KD, NW, SB, true><<<grid, block, 0, s>>>(p);
+        const int blocks = (p.tiles * 16 * NW * KD / 4 + 255) / 256;
+        const dim3 cg((unsigned)(p.batch * p.H * blocks), (unsigned)p.nops);
+        la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, 16 * NW);
+    }
+    la_walk<KD, NW, SB, false><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
 template <int KD>
-hipError_t launch_nw(const Params &p, int nops, int vd, hipStream_t s) {
-    if (vd <= 64) return launch_kd<KD, 2>(p, nops, 1, s);
-    return launch_kd<KD, 4>(p, nops, (vd + 127) / 128, s);
+hipError_t launch_nw(const Params &p, const Shape &h, hipStream_t s) {
+    if (h.nw == 4) return p.state_bf16 ? launch_kd<KD, 4, true>(p, s) : launch_kd<KD, 4, false>(p, s);
+    return p.state_bf16 ? launch_kd<KD, 8, true>(p, s) : launch_kd<KD, 8, false>(p, s);
 }
 }  // namespace
 
-hipError_t launch_walk(const Params &p, int nops, hipStream_t s) {
-    int kd = 0, vd = 0;
-    for (int i = 0; i < nops; ++i) {
-        kd = std::max(kd, p.op[i].kd);
-        vd = std::max(vd, p.op[i].vd);
-    }
-    if (kd <= 64) return launch_nw<64>(p, nops, vd, s);
-    if (kd <= 128) return launch_nw<128>(p, nops, vd, s);
-    return launch_nw<256>(p, nops, vd, s);
+// Segments: a walk is a chain of chunks, so a launch needs enough of them
+// side by side: kTarget workgroups, two per compute unit, each of at least
+// kLeast tokens.  Sequences no longer than a segment are not cut.
+Shape shape_of(int64_t T, int batch, int H, int kd, int vd, int nops) {
+    constexpr int64_t kTarget = 512, kLeast = 256;
+    Shape h;
+    h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
+    h.nw = vd <= 64 ? 4 : 8;
+    h.tiles = (vd + 16 * h.nw - 1) / (16 * h.nw);
+    const int64_t want = T * H * h.tiles * nops / kTarget;  // tokens
+    const int64_t seg = std::max((want + kTok - 1) / kTok * kTok, kLeast);
+    h.seg = T > seg ? (int)seg : 0;
+    h.slots = h.seg != 0 ? (int)(T / seg) + batch : batch;
+    h.bytes = h.seg != 0 ? (size_t)nops * h.slots * H * h.tiles * 16 * h.nw * h.kd * sizeof(float) : 0;
+    return h;
+}
+
+hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s) {
+    p.nops = nops;
+    p.tiles = h.tiles;
+    p.seg = h.seg;
+    p.slots = h.slots;
+    if (h.kd == 64) return launch_nw<64>(p, h, s);
+    if (h.kd == 128) return launch_nw<128>(p, h, s);
+    return launch_nw<256>(p, h, s);
 }
 
 hipError_t launch_group_sum(const float *src, uint16_t *dst, const Params &p, int div, int width, hipStream_t s) {

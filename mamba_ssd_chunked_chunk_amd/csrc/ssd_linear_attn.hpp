@@ -47,6 +47,7 @@ struct Params {
     Op op[kMaxOps];
     int64_t T;
     int batch, H;
+    int share;            // heads of a group
     int state_size;       // V * K
     int state_bf16;
     const float *log_decay;
@@ -55,9 +56,20 @@ struct Params {
     const uint32_t *cache_idx;  // null: slot b
     int init_all;
     uint32_t max_slots;
+    // the launch (set by launch_walk)
+    int nops, tiles;  // tiles: workgroups along the value channels
+    int seg, slots;   // tokens of a segment (0: whole sequences) and slots of segments
+    float *parts;     // [nops][slots][H][tiles * VT][KD] states of the segments, in register order
 };
 
-hipError_t launch_walk(const Params &p, int nops, hipStream_t s);
+// What a launch takes of kd x vd channels (the largest of its operations').
+struct Shape {
+    int kd, nw, tiles;  // kd rounded up; wavefronts (of 16 value channels) and workgroups along vd
+    int seg, slots;
+    size_t bytes;       // of `parts`
+};
+Shape shape_of(int64_t T, int batch, int H, int kd, int vd, int nops);
+hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s);
 
 // sums the heads of each group: dst[t][g][w] = sum_i src[t][g * div + i][w]
 hipError_t launch_group_sum(const float *src, uint16_t *dst, const Params &p, int div, int width, hipStream_t s);

@@ -13,6 +13,7 @@ using ssd::la::Params;
 using ssd::la::Rows;
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxRow = 1 << 22;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void *ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 
@@ -25,28 +26,40 @@ ssd_status check(const ssd_linear_attn_problem *p) {
         return SSD_ERR_BAD_SHAPE;
     if (p->state_dtype != SSD_STATE_F32 && p->state_dtype != SSD_STATE_BF16) return SSD_ERR_UNSUPPORTED;
     if (!dim_ok(p->key_dim) || !dim_ok(p->value_dim)) return SSD_ERR_UNSUPPORTED;
-    if ((int64_t)p->batch * p->nheads > INT32_MAX) return SSD_ERR_UNSUPPORTED;
+    // the kernels' grids: up to 4 blocks of channels, 3 recurrences, 8 blocks of 256 threads per head of states
+    if (((int64_t)p->batch + p->total_len / 256) * p->nheads > INT32_MAX / 64) return SSD_ERR_UNSUPPORTED;
     if (!isfinite(p->scale)) return SSD_ERR_UNSUPPORTED;
     const int64_t qk = (int64_t)p->ngroups * p->key_dim, vv = (int64_t)p->nheads * p->value_dim;
     const int64_t strides[3] = {p->q_stride, p->k_stride, p->v_stride}, rows[3] = {qk, qk, vv};
     for (int i = 0; i < 3; ++i)
         if (strides[i] != 0 && (strides[i] < rows[i] || strides[i] % 8 != 0)) return SSD_ERR_BAD_SHAPE;
+    for (int i = 0; i < 3; ++i)  // 64 rows are addressed with 31 bits
+        if ((strides[i] != 0 ? strides[i] : rows[i]) > kMaxRow) return SSD_ERR_UNSUPPORTED;
+    if ((int64_t)p->nheads * p->key_dim > kMaxRow) return SSD_ERR_UNSUPPORTED;  // gradients before heads are summed
     return SSD_OK;
 }
 
 int64_t stride_or(int64_t s, int64_t dense) { return s != 0 ? s : dense; }
 
-// Workspace of the backward pass: fp32 dq and dk per head, where several
-// heads share a row of q and k.
+// Workspace: the segments' states of a launch, and in the backward pass fp32
+// dq and dk per head, where several heads share a row of q and k.
 struct Layout {
-    size_t dq, dk, bytes;
+    ssd::la::Shape shape;
+    bool shared;
+    size_t dq, dk, bytes;  // the segments' states come first
 };
 Layout layout_of(const ssd_linear_attn_problem *p, bool backward) {
-    Layout L = {0, 0, 0};
-    if (backward && p->nheads != p->ngroups) {
-        const size_t n = (size_t)p->total_len * p->nheads * p->key_dim * sizeof(float);
-        L.dk = align_up(n);
-        L.bytes = L.dk + align_up(n);
+    Layout L = {};
+    const int K = p->key_dim, V = p->value_dim, m = K > V ? K : V;
+    L.shape = ssd::la::shape_of(p->total_len, p->batch, p->nheads, backward ? m : K, backward ? m : V,
+                                backward ? 3 : 1);
+    L.bytes = align_up(L.shape.bytes);
+    L.shared = backward && p->nheads != p->ngroups;
+    if (L.shared) {
+        const size_t n = align_up((size_t)p->total_len * p->nheads * p->key_dim * sizeof(float));
+        L.dq = L.bytes;
+        L.dk = L.dq + n;
+        L.bytes = L.dk + n;
     }
     return L;
 }
@@ -62,6 +75,7 @@ Params common(const ssd_linear_attn_problem *p, const float *log_decay, const in
     q.T = p->total_len;
     q.batch = p->batch;
     q.H = p->nheads;
+    q.share = p->nheads / p->ngroups;
     q.state_size = p->key_dim * p->value_dim;
     q.state_bf16 = p->state_dtype == SSD_STATE_BF16;
     q.log_decay = log_decay;
@@ -89,10 +103,12 @@ ssd_status forward(const ssd_linear_attn_problem *p, void *o, const void *q, con
     if (!aligned(o, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(state_in, 16) ||
         !aligned(state_out, 16) || !aligned(log_decay, 4) || !aligned(qsl, 4) || !aligned(cache_idx, 4))
         return SSD_ERR_MISALIGNED;
-    const ssd_status sw = check_workspace(layout_of(p, false), ws, ws_bytes);
+    const Layout L = layout_of(p, false);
+    const ssd_status sw = check_workspace(L, ws, ws_bytes);
     if (sw != SSD_OK) return sw;
 
     Params a = common(p, log_decay, qsl);
+    a.parts = static_cast<float *>(ws);
     a.has_init = has_init;
     a.cache_idx = cache_idx;
     a.init_all = init_all;
@@ -110,7 +126,7 @@ ssd_status forward(const ssd_linear_attn_problem *p, void *o, const void *q, con
     op.state_out = state_out;
     op.sv = p->key_dim;
     op.sk = 1;
-    return ssd::la::launch_walk(a, 1, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    return ssd::la::launch_walk(a, L.shape, 1, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 ssd_status check_cache(const ssd_state_cache_problem *p, const void *codes, const void *scales, const void *pool,
@@ -187,12 +203,13 @@ ssd_status ssd_linear_attn_varlen_bwd(
 
     const ssd_linear_attn_problem *p = prob;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const bool shared = L.bytes != 0;
+    const bool shared = L.shared;
     char *ws = static_cast<char *>(workspace);
     const Rows rq = group_rows(p, q, p->q_stride), rk = group_rows(p, k, p->k_stride);
     const Rows rv = head_rows(p, v, p->v_stride), rg = head_rows(p, d_o, 0);
     Params a = common(p, log_decay, query_start_loc);
     a.init_all = 1;
+    a.parts = reinterpret_cast<float *>(ws);
     Op &oq = a.op[0], &ok = a.op[1], &ov = a.op[2];
     // dq: the forward chain, with the state transposed
     oq.q = rg;
@@ -232,9 +249,9 @@ ssd_status ssd_linear_attn_varlen_bwd(
         // dv overwrites d_final with d_initial: dk, which reads it too, runs first
         Params b = a;
         b.op[0] = a.op[2];
-        if (ssd::la::launch_walk(a, 2, s) != hipSuccess || ssd::la::launch_walk(b, 1, s) != hipSuccess)
+        if (ssd::la::launch_walk(a, L.shape, 2, s) != hipSuccess || ssd::la::launch_walk(b, L.shape, 1, s) != hipSuccess)
             return SSD_ERR_HIP;
-    } else if (ssd::la::launch_walk(a, 3, s) != hipSuccess) {
+    } else if (ssd::la::launch_walk(a, L.shape, 3, s) != hipSuccess) {
         return SSD_ERR_HIP;
     }
     if (shared && p->total_len > 0) {
