@@ -23,8 +23,9 @@
 //
 // Rounding: scores and the state are rounded to bf16 once as operands of the
 // output, which is bf16 itself.  The weighted v of the state update is split
-// into three bf16 parts that carry its 24 bits, so states are those of fp32
-// sums.
+// into three bf16 parts that carry its 24 bits where the state is returned in
+// fp32, so it is that of fp32 sums; into two, 2.4e-6 off in norm, where it
+// only enters bf16 values (outputs, bf16 states).
 #include "ssd_linear_attn.hpp"
 
 namespace ssd {
@@ -35,31 +36,24 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 
-// LDS place (in 16-byte units) of unit c of row r, rows of U units: the units
-// of a row are permuted so that both a column of 16-byte reads down
-// consecutive rows and the transposing reads (4 rows x 4 units) touch every
-// bank once.
-template <int U>
-__device__ __forceinline__ int place(int r, int c) {
-    if constexpr (U == 8)
-        return r * U + (c ^ ((((r >> 1) & 1) << 2) | ((r >> 2) & 3)));
-    else
-        return r * U + (c ^ (((r & 3) << 2) | ((r >> 2) & 3)));
+// LDS layout of a chunk's rows: unit c (16 bytes, 8 channels) of row r at
+// byte c kUnit + 16 r.  16 consecutive rows of a unit are 256 bytes (every
+// bank once), and units lie 16 banks apart (kUnit = 1024 + 64), so 4 rows x 4
+// units, which the transposing reads and the stores touch at a time, do not
+// meet either.  Every place is a lane's base plus a constant, which is the
+// offset field of the instruction: one register serves a whole phase.
+constexpr int kUnit = kTok * 16 + 64;
+
+__device__ __forceinline__ bf16x8 read_unit(const char *s, int at) {
+    return *reinterpret_cast<const bf16x8 *>(s + at);
 }
 
-template <int U>
-__device__ __forceinline__ bf16x8 row_read(const uint16_t *s, int r, int c) {
-    return *reinterpret_cast<const bf16x8 *>(s + place<U>(r, c) * 8);
-}
-
-// For lane l: 8 tokens t0 + 8 (l / 16) .. of one of 16 columns.  The lanes
-// take the columns of four groups of four; group l % 4 starts at column
-// unit * 8 + half (both may depend on l % 4).
-template <int U>
-__device__ __forceinline__ bf16x8 column_read(const uint16_t *s, int t0, int unit, int half, int lane) {
-    const int r = t0 + 8 * (lane >> 4) + ((lane & 15) >> 2);
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + place<U>(r, unit) * 8 + half));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + place<U>(r + 4, unit) * 8 + half));
+// Transposing read: lane l gets 8 tokens (`at` of lane l is 4 channels of token
+// 8 (l / 16) + l % 16 / 4; the lanes' 16 columns are those 4 of lanes 0 .. 3 of
+// its 16 in turn).
+__device__ __forceinline__ bf16x8 read_columns(const char *s, int at) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + at));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + at + 4 * 16));
     const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     return __builtin_bit_cast(bf16x8, v);
 }
@@ -168,7 +162,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void *base, 
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every such buffer
 
 // Wavefronts per SIMD that the registers of a variant allow.
-constexpr int waves_of(int KD, int NW) { return 2; }
+constexpr int waves_of(int KD, int NW) { return KD > 128 ? 2 : NW == 8 ? 4 : 3; }
 
 // KD: channels of k and q the kernel holds (kd rounded up; the rest is zero).
 // LOCAL: only the state a segment leaves when it starts from zero.
@@ -181,10 +175,11 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     constexpr int NT = KD / 32;      // blocks of 32 k channels of a wavefront's state
     constexpr int LK = kTok * UK / NTH, LV = kTok * UV / NTH;  // 16-byte loads of a thread
     constexpr int RK = NTH / UK, RV = NTH / UV;                // rows between them
-    __shared__ __attribute__((aligned(16))) uint16_t s_q[LOCAL ? 8 : kTok * KD];
-    __shared__ __attribute__((aligned(16))) uint16_t s_k[kTok * KD];
-    __shared__ __attribute__((aligned(16))) uint16_t s_v[kTok * VT];
-    __shared__ __attribute__((aligned(16))) uint16_t s_p[LOCAL ? 8 : kTok * kTok];
+    __shared__ __attribute__((aligned(16))) char s_q[LOCAL ? 16 : UK * kUnit];
+    __shared__ __attribute__((aligned(16))) char s_k[UK * kUnit];
+    __shared__ __attribute__((aligned(16))) char s_v[UV * kUnit];
+    __shared__ __attribute__((aligned(16))) char s_p[LOCAL ? 16 : kTok / 8 * kUnit];
+    __shared__ float s_pair[96], s_lead[32];
 
     // Consecutive workgroups go to the 8 XCDs in turn.  The workgroups that
     // read the same rows (a group's heads, their blocks of channels, the
@@ -200,7 +195,8 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     const int h = id % p.H, w = id / p.H;
     const Op &op = p.op[which];
     if (v0 >= op.vd) return;
-    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     const Segment g = find_segment(p, w);
@@ -251,24 +247,29 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     // token r - pad (pad = 64 - len), or in reverse 63 - r: a short chunk ends
     // at the last place, where the weights of the state update are the full
     // chunk's, and starts with rows of zeros.
-    float pair[8], lead[8];
-    const int below = 16 * (wave & 3);  // of the wavefront's blocks of scores: see there
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int d = below + l16 - (8 * q4 + e);
-        pair[e] = d >= 0 ? op.scale_pair * fast_exp2(l2 * (float)d) : 0.f;
-        lead[e] = op.scale_update * fast_exp2(l2 * ((float)(31 - 8 * q4 - e) + shift));
+    // In LDS: weights of the scores by distance i - j (0 above the diagonal),
+    // from distance -31 on, and of the last 32 tokens in the state update.
+    if (tid < 64 + 31) {
+        const int d = tid - 31;
+        s_pair[tid] = d >= 0 ? op.scale_pair * fast_exp2(l2 * (float)d) : 0.f;
+        if (tid < 32) s_lead[tid] = op.scale_update * fast_exp2(l2 * ((float)tid + shift));
     }
+    const bool fine = !SB && op.state_out != nullptr;  // three parts of the weighted v, or two
     const float by32 = fast_exp2(l2 * 32.f);
 
     const int64_t qs = op.q.stride, ks = op.k.stride, vs = op.v.stride, os = (int64_t)p.H * op.vd;
     const uint16_t *gq = op.q.p + (int64_t)(h / op.q.div) * op.kd;
     const uint16_t *gk = op.k.p + (int64_t)(h / op.k.div) * op.kd;
     const uint16_t *gv = op.v.p + (int64_t)(h / op.v.div) * op.vd;
-    const int rk = tid / UK, ck = tid % UK, rv = tid / UV, cv = tid % UV;
-    const uint32_t oq = 8 * ck < op.kd ? (uint32_t)(rk * qs + 8 * ck) * 2 : kNowhere;
-    const uint32_t ok = 8 * ck < op.kd ? (uint32_t)(rk * ks + 8 * ck) * 2 : kNowhere;
-    const uint32_t ov = v0 + 8 * cv < op.vd ? (uint32_t)(rv * vs + v0 + 8 * cv) * 2 : kNowhere;
+    // A thread's unit and row of the loads: 16 lanes take 4 rows of 4 units.
+    // The thread number is made opaque wherever they are used, so that they are
+    // formed again instead of held in some ten registers across the chunk.
+    auto unit_of = [](int t, int U) { return (t >> 4) % (U / 4) * 4 + (t & 3); };
+    auto row_of = [](int t, int U) { return (t >> 4) / (U / 4) * 4 + (t >> 2) % 4; };
+    auto opaque = [](int t) {
+        asm volatile("" : "+v"(t));
+        return t;
+    };
 
     u32x4 fq[LOCAL ? 1 : LK], fk[LK], fv[LV];
     auto fetch = [&](int c0) {  // the chunk's rows, lowest token first, into registers
@@ -276,6 +277,9 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
         const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
         const auto bk = rows_buffer(gk + first * ks, (uint32_t)((len - 1) * ks + op.kd) * 2);
         const auto bv = rows_buffer(gv + first * vs, (uint32_t)((len - 1) * vs + op.vd) * 2);
+        const int t = opaque(tid), ck = unit_of(t, UK), rk = row_of(t, UK), cv = unit_of(t, UV), rv = row_of(t, UV);
+        const uint32_t ok = 8 * ck < op.kd ? (uint32_t)(rk * (int)ks + 8 * ck) * 2 : kNowhere;
+        const uint32_t ov = v0 + 8 * cv < op.vd ? (uint32_t)(rv * (int)vs + v0 + 8 * cv) * 2 : kNowhere;
 #pragma unroll
         for (int i = 0; i < LK; ++i)
             fk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, ok + i * RK * (uint32_t)ks * 2, 0, 0);
@@ -284,6 +288,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
             fv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, ov + i * RV * (uint32_t)vs * 2, 0, 0);
         if constexpr (!LOCAL) {
             const auto bq = rows_buffer(gq + first * qs, (uint32_t)((len - 1) * qs + op.kd) * 2);
+            const uint32_t oq = 8 * ck < op.kd ? (uint32_t)(rk * (int)qs + 8 * ck) * 2 : kNowhere;
 #pragma unroll
             for (int i = 0; i < LK; ++i)
                 fq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, oq + i * RK * (uint32_t)qs * 2, 0, 0);
@@ -291,28 +296,64 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     };
     if (n > 0) fetch(0);
 
+    f32x4 O[4] = {};
+    // Stores the outputs of the chunk at c0: place 16 rt + l16, 4 channels from
+    // 4 q4.  A chunk's outputs leave behind the barriers of the next one, ahead
+    // of its loads: waiting for loads then never waits for younger stores.
+    auto emit = [&](int c0) {
+        const int len = min(kTok, n - c0), pad = kTok - len;
+        const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
+        const int eb = op.out_f32 ? 4 : 2;
+        const auto bo = rows_buffer(static_cast<char *>(op.out) + (first * os + (int64_t)h * op.vd) * eb,
+                                    (uint32_t)((len - 1) * os + op.vd) * eb);
+        const int vc = v0 + 16 * wave + 4 * q4;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const int r = 16 * rt + l16;
+            const int tok = rev ? 63 - r : r - pad;
+            const uint32_t at =
+                vc < op.vd && (uint32_t)tok < (uint32_t)len ? (uint32_t)(tok * (int)os + vc) * eb : kNowhere;
+            if (op.out_f32)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[rt]), bo, at, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2{pack_bf16x2(O[rt][0], O[rt][1]), pack_bf16x2(O[rt][2], O[rt][3])}, bo, at, 0, 0);
+        }
+    };
+
+    // a lane's places: rows l16 of unit q4; rows of k as two tiles; columns
+    const int at_row = q4 * kUnit + l16 * 16;
+    const int at_key = q4 * kUnit + (8 * (l16 >> 2) + (l16 & 3)) * 16;
+    const int at_col = (8 * q4 + (l16 >> 2)) * 16;
+    const int at_kcol = at_col + (l16 & 3) * kUnit;
+    const int at_vcol = at_col + (2 * wave + ((l16 & 3) >> 1)) * kUnit + (l16 & 1) * 8;
+    const float *const w_pair = s_pair + 31 + 16 * (wave & 3) + l16 - 8 * q4, *const w_lead = s_lead + 31 - 8 * q4;
+
 #pragma unroll 1
     for (int c0 = 0; c0 < n; c0 += kTok) {
         const int len = min(kTok, n - c0), pad = kTok - len;
-        const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
         __syncthreads();  // the previous chunk's rows are no longer read
         // token i of the chunk to its place; tokens past it (zeros) wrap to the places before it
+        const int ft = opaque(tid), ck = unit_of(ft, UK), rk = row_of(ft, UK), cv = unit_of(ft, UV),
+                  rv = row_of(ft, UV);
 #pragma unroll
         for (int i = 0; i < LK; ++i) {
             const int r = rev ? 63 - (rk + i * RK) : (rk + i * RK + pad) & 63;
-            *reinterpret_cast<u32x4 *>(s_k + place<UK>(r, ck) * 8) = fk[i];
-            if constexpr (!LOCAL) *reinterpret_cast<u32x4 *>(s_q + place<UK>(r, ck) * 8) = fq[i];
+            *reinterpret_cast<u32x4 *>(s_k + ck * kUnit + r * 16) = fk[i];
+            if constexpr (!LOCAL) *reinterpret_cast<u32x4 *>(s_q + ck * kUnit + r * 16) = fq[i];
         }
 #pragma unroll
         for (int i = 0; i < LV; ++i) {
             const int r = rev ? 63 - (rv + i * RV) : (rv + i * RV + pad) & 63;
-            *reinterpret_cast<u32x4 *>(s_v + place<UV>(r, cv) * 8) = fv[i];
+            *reinterpret_cast<u32x4 *>(s_v + cv * kUnit + r * 16) = fv[i];
         }
         __syncthreads();
+        if (!LOCAL && c0 > 0) emit(c0 - kTok);
         if (c0 + kTok < n) fetch(c0 + kTok);
 
-        f32x4 O[4] = {};
         if constexpr (!LOCAL) {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) O[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
             // ---- weighted scores in blocks of 16 tokens i (lanes) x 32 tokens
             // j (8 consecutive ones a lane): blocks (rt, c) = (0,0) (1,0) (2,0)
             // (3,0) (2,1) (3,1).  Wavefront m takes block m, and with four
@@ -324,16 +365,15 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
                 f32x4 a[2] = {};
 #pragma unroll
                 for (int u = 0; u < KD / 32; ++u) {
-                    const bf16x8 q = row_read<UK>(s_q, 16 * rt + l16, 4 * u + q4);
+                    const bf16x8 q = read_unit(s_q, at_row + 16 * rt * 16 + 4 * u * kUnit);
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        a[y] = mfma_bf16(row_read<UK>(s_k, 32 * c + 8 * (l16 >> 2) + 4 * y + (l16 & 3), 4 * u + q4), q,
-                                         a[y]);
+                        a[y] = mfma_bf16(read_unit(s_k, at_key + (32 * c + 4 * y) * 16 + 4 * u * kUnit), q, a[y]);
                 }
                 float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = a[e / 4][e % 4] * pair[e];
-                *reinterpret_cast<bf16x8 *>(s_p + place<8>(16 * rt + l16, 4 * c + q4) * 8) = pack8(f);
+                for (int e = 0; e < 8; ++e) f[e] = a[e / 4][e % 4] * w_pair[-e];
+                *reinterpret_cast<bf16x8 *>(s_p + at_row + 16 * rt * 16 + 4 * c * kUnit) = pack8(f);
             }
             // ---- output from the state, out^T = S q^T (channels x tokens)
 #pragma unroll
@@ -344,7 +384,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
                 const bf16x8 a = pack8(f);
 #pragma unroll
                 for (int rt = 0; rt < 4; ++rt)
-                    O[rt] = mfma_bf16(a, row_read<UK>(s_q, 16 * rt + l16, 4 * t + q4), O[rt]);
+                    O[rt] = mfma_bf16(a, read_unit(s_q, at_row + 16 * rt * 16 + 4 * t * kUnit), O[rt]);
             }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt)
@@ -361,59 +401,44 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
         }
 #pragma unroll
         for (int u = 0; u < kTok / 32; ++u) {
-            const int x4 = lane & 3;
-            const bf16x8 v = column_read<UV>(s_v, 32 * u, 2 * wave + (x4 >> 1), 4 * (x4 & 1), lane);
+            const bf16x8 v = read_columns(s_v, at_vcol + 32 * u * 16);
             if constexpr (!LOCAL) {
 #pragma unroll
                 for (int rt = 2 * u; rt < 4; ++rt)
-                    O[rt] = mfma_bf16(v, row_read<8>(s_p, 16 * rt + l16, 4 * u + q4), O[rt]);
+                    O[rt] = mfma_bf16(v, read_unit(s_p, at_row + 16 * rt * 16 + 4 * u * kUnit), O[rt]);
             }
             float f[8], r[8];
             unpack8(v, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= u == 0 ? lead[e] * by32 : lead[e];
+            for (int e = 0; e < 8; ++e) f[e] *= w_lead[-e] * (u == 0 ? by32 : 1.f);
             const bf16x8 w1 = pack8(f);
             unpack8(w1, r);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] -= r[e];
             const bf16x8 w2 = pack8(f);
-            unpack8(w2, r);
+            bf16x8 w3;
+            if (fine) {
+                unpack8(w2, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] -= r[e];
-            const bf16x8 w3 = pack8(f);
+                for (int e = 0; e < 8; ++e) f[e] -= r[e];
+                w3 = pack8(f);
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const bf16x8 k0 = column_read<UK>(s_k, 32 * u, 4 * t + x4, 0, lane);
-                const bf16x8 k1 = column_read<UK>(s_k, 32 * u, 4 * t + x4, 4, lane);
-                S[t][0] = mfma_bf16(k0, w3, S[t][0]);
-                S[t][1] = mfma_bf16(k1, w3, S[t][1]);
+                const bf16x8 k0 = read_columns(s_k, at_kcol + 32 * u * 16 + 4 * t * kUnit);
+                const bf16x8 k1 = read_columns(s_k, at_kcol + 32 * u * 16 + 4 * t * kUnit + 8);
+                if (fine) {
+                    S[t][0] = mfma_bf16(k0, w3, S[t][0]);
+                    S[t][1] = mfma_bf16(k1, w3, S[t][1]);
+                }
                 S[t][0] = mfma_bf16(k0, w2, S[t][0]);
                 S[t][1] = mfma_bf16(k1, w2, S[t][1]);
                 S[t][0] = mfma_bf16(k0, w1, S[t][0]);
                 S[t][1] = mfma_bf16(k1, w1, S[t][1]);
             }
         }
-
-        // ---- stores: place 16 rt + l16, 4 channels from 4 q4
-        if constexpr (!LOCAL) {
-            const int eb = op.out_f32 ? 4 : 2;
-            const auto bo = rows_buffer(static_cast<char *>(op.out) + (first * os + (int64_t)h * op.vd) * eb,
-                                        (uint32_t)((len - 1) * os + op.vd) * eb);
-            const int vc = v0 + 16 * wave + 4 * q4;
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                const int r = 16 * rt + l16;
-                const int tok = rev ? 63 - r : r - pad;
-                const uint32_t at =
-                    vc < op.vd && (uint32_t)tok < (uint32_t)len ? (uint32_t)(tok * os + vc) * eb : kNowhere;
-                if (op.out_f32)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[rt]), bo, at, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b64(
-                        u32x2{pack_bf16x2(O[rt][0], O[rt][1]), pack_bf16x2(O[rt][2], O[rt][3])}, bo, at, 0, 0);
-            }
-        }
     }
+    if (!LOCAL && n > 0) emit((n - 1) / kTok * kTok);
 
     if constexpr (LOCAL) {
 #pragma unroll
