@@ -1,31 +1,38 @@
 // Linear attention with a fixed decay per head: the chunked form, forward
 // and (as three recurrences with exchanged roles) backward.
 //
-// A workgroup walks one segment of a sequence for one head and 16 * NW value
-// channels, in chunks of 64 tokens.  With i, j the places in a chunk, S the
-// state that enters it and lambda the head's decay,
+// A workgroup walks one segment of a sequence, in chunks of 64 tokens, for one
+// head and VT value channels, or for HP heads that share q and k.  With i, j
+// the places in a chunk, S the state that enters it and lambda the head's decay,
 //     out_i = lambda^(i+1) S q_i + sum_{j <= i} lambda^(i-j) (q_i . k_j) v_j
 //     S    <- lambda^len S + sum_j lambda^(len-1-j) v_j k_j^T
-// Each wavefront owns 16 value channels and keeps S of them (16 x kd, fp32)
-// in registers for the whole walk, so the state never moves; the wavefronts
-// share only the chunk's q, k, v rows and its 64 x 64 matrix of weighted
-// scores, in LDS.  Every product is computed transposed (channels x tokens):
-// a lane then holds one token and consecutive channels, so its decay is a
-// scalar, and the state registers are, as they are, the operand of the next
-// product.
+// Each wavefront owns 16 DT value channels and keeps S of them (fp32) in
+// registers for the whole walk, so the state never moves; the wavefronts share
+// only the chunk's q, k, v rows and its 64 x 64 matrix of weighted scores, in
+// LDS.  Every product is computed transposed (channels x tokens): a lane then
+// holds one token and consecutive channels, so its decay is a scalar, and the
+// state registers are, as they are, the operand of the next product.
 //
-// Operands that run along tokens (v and k of the state update) come from LDS
-// with the transposing read, whose lanes take columns in groups of four.  For
-// k (and for the rows of k in the scores) two tiles of 16 channels are taken
-// from 32, channels 8 g + 0..3 to the one and 8 g + 4..7 to the other, so
-// that the two accumulators of a lane together are 8 consecutive channels:
-// one 16-byte operand of the next product.
+// LDS is what a wavefront of 16 channels is bound by (32 ragged prompts of 128
+// heads: 65% of the cycles, and half as many again lost to conflicts), since
+// all of them read all of q and k; 32 channels (DT 2) halve that.  The orders
+// below let every large read touch each bank once:
+//   - rows lie unit by unit (16 bytes, 8 channels), units 16 banks apart;
+//   - operands along tokens come from the transposing read, 4 rows of 4 half
+//     units at a time, two such tiles for 32 channels (the lane groups then use
+//     the same half of the banks: half rate, cheaper than exchanging halves in
+//     registers);
+//   - of the 32 tokens of a product, lane group q4 takes 4 q4 .. + 3 and 16 + 4 q4 .. + 3
+//     (k, v and the scores alike: a sum's order is free);
+//   - of 32 rows of q or scores, the first 16-row tile takes 0 .. 3, 8 .. 11,
+//     .., the second the others.
 //
 // Rounding: scores and the state are rounded to bf16 once as operands of the
 // output, which is bf16 itself.  The weighted v of the state update is split
 // into three bf16 parts that carry its 24 bits where the state is returned in
 // fp32, so it is that of fp32 sums; into two, 2.4e-6 off in norm, where it
 // only enters bf16 values (outputs, bf16 states).
+#include <stdlib.h>
 #include "ssd_linear_attn.hpp"
 
 namespace ssd {
@@ -36,27 +43,27 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 
-// LDS layout of a chunk's rows: unit c (16 bytes, 8 channels) of row r at
-// byte c kUnit + 16 r.  16 consecutive rows of a unit are 256 bytes (every
-// bank once), and units lie 16 banks apart (kUnit = 1024 + 64), so 4 rows x 4
-// units, which the transposing reads and the stores touch at a time, do not
-// meet either.  Every place is a lane's base plus a constant, which is the
-// offset field of the instruction: one register serves a whole phase.
+// LDS layout of a chunk's rows: unit c of row r at byte c kUnit + 16 r.  Every
+// place is a lane's base plus a constant, which is the offset field of the
+// instruction: one register serves a whole phase.
 constexpr int kUnit = kTok * 16 + 64;
 
 __device__ __forceinline__ bf16x8 read_unit(const char *s, int at) {
     return *reinterpret_cast<const bf16x8 *>(s + at);
 }
 
-// Transposing read: lane l gets 8 tokens (`at` of lane l is 4 channels of token
-// 8 (l / 16) + l % 16 / 4; the lanes' 16 columns are those 4 of lanes 0 .. 3 of
-// its 16 in turn).
+// Transposing read: lane l gets the tokens r .. r + 3 and r + 16 .. r + 19 of one
+// of 16 columns; `at` of lane l is row r + l % 16 / 4 of the four columns that
+// lanes 4 (l % 4) .. + 3 of its 16 get.
 __device__ __forceinline__ bf16x8 read_columns(const char *s, int at) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + at));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + at + 4 * 16));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s + at + 16 * 16));
     const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     return __builtin_bit_cast(bf16x8, v);
 }
+
+// the 32 channels of two tiles: lane l of tile y (0, 1) of 16 columns
+__device__ __forceinline__ int column(int l, int y) { return 8 * (l >> 2) + 4 * y + (l & 3); }
 
 __device__ __forceinline__ bf16x8 pack8(const float (&f)[8]) {
     const u32x4 w = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -103,6 +110,20 @@ __device__ __forceinline__ void write_state(void *base, int64_t at, int64_t sk, 
 }
 
 __device__ __forceinline__ int clamp_row(const Params &p, int t) { return min(max(t, 0), (int)p.T); }
+
+// log2 of a head's decay; -infinity as a finite number, so that times 0 it is 0
+__device__ __forceinline__ float log2_decay(const Params &p, int h) {
+    const float ld = p.log_decay[h] * kLog2e;
+    return ld < -1e30f ? -1e30f : ld;
+}
+
+// a uniform value as one the compiler has to keep
+__device__ __forceinline__ int held(int x) {
+    x = __builtin_amdgcn_readfirstlane(x);
+    asm volatile("" : "+s"(x));
+    return x;
+}
+__device__ __forceinline__ float held(float x) { return __int_as_float(held(__float_as_int(x))); }
 
 // whether sequence b of an operation starts from a stored state
 __device__ __forceinline__ bool resumes(const Params &p, const Op &op, int b) {
@@ -161,43 +182,51 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void *base, 
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every such buffer
 
-// Wavefronts per SIMD that the registers of a variant allow.
-constexpr int waves_of(int KD, int NW) { return KD > 128 ? 2 : NW == 8 ? 4 : 3; }
-
-// KD: channels of k and q the kernel holds (kd rounded up; the rest is zero).
+// KD: channels of k and q the kernel holds (kd rounded up; the rest is zero);
+// NW wavefronts of DT tiles of 16 value channels, for HP heads.
 // LOCAL: only the state a segment leaves when it starts from zero.
-template <int KD, int NW, bool SB, bool LOCAL>
-__global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
+template <int KD, int NW, int DT, int HP, bool SB, bool LOCAL>
+__global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     constexpr int NTH = 64 * NW;
-    constexpr int UK = KD / 8;       // 16-byte units of a q or k row
-    constexpr int VT = 16 * NW;      // value channels of the workgroup
-    constexpr int UV = VT / 8;
+    constexpr int WH = NW / HP;      // wavefronts of a head
+    constexpr int VT = 16 * DT * WH; // value channels of the workgroup, of each head
+    constexpr int UK = KD / 8;       // units of a q or k row
+    constexpr int UV = HP * VT / 8;  // and of the heads' v rows together
     constexpr int NT = KD / 32;      // blocks of 32 k channels of a wavefront's state
     constexpr int LK = kTok * UK / NTH, LV = kTok * UV / NTH;  // 16-byte loads of a thread
     constexpr int RK = NTH / UK, RV = NTH / UV;                // rows between them
+    constexpr int kScores = kTok / 8 * kUnit;
+    static_assert(VT % 32 == 0, "pairs of tiles");
     __shared__ __attribute__((aligned(16))) char s_q[LOCAL ? 16 : UK * kUnit];
     __shared__ __attribute__((aligned(16))) char s_k[UK * kUnit];
     __shared__ __attribute__((aligned(16))) char s_v[UV * kUnit];
-    __shared__ __attribute__((aligned(16))) char s_p[LOCAL ? 16 : kTok / 8 * kUnit];
-    __shared__ float s_pair[96], s_lead[32];
+    __shared__ __attribute__((aligned(16))) char s_p[LOCAL ? 16 : HP * kScores];
+    __shared__ float s_pair[HP][96], s_lead[HP][64];
 
     // Consecutive workgroups go to the 8 XCDs in turn.  The workgroups that
     // read the same rows (a group's heads, their blocks of channels, the
     // recurrences) stay on one XCD, and its L2.
-    const int together = p.share * p.tiles * p.nops;
+    const int together = p.share / HP * p.tiles * p.nops;
     const int run = (int)blockIdx.x / 8;
     int id = (run / together * 8 + (int)(blockIdx.x % 8)) * together + run % together;
-    if (id >= p.slots * p.H * p.tiles * p.nops) return;
+    if (id >= p.slots * (p.H / HP) * p.tiles * p.nops) return;
     const int which = id % p.nops;
     id /= p.nops;
     const int v0 = (id % p.tiles) * VT;
     id /= p.tiles;
-    const int h = id % p.H, w = id / p.H;
+    const int h0 = id % (p.H / HP) * HP, w = id / (p.H / HP);
     const Op &op = p.op[which];
-    if (v0 >= op.vd) return;
+    // what the walk needs of it, held in scalar registers (a scalar load inside
+    // the walk would wait for every LDS read before it)
+    const int kd = held(op.kd), vd = held(op.vd), out_f32 = held(op.out_f32);
+    const int qs = held((int)op.q.stride), ks = held((int)op.k.stride), vs = held((int)op.v.stride);
+    const bool rev = held(op.reverse) != 0;
+    const float scale_state = held(op.scale_state);
+    if (v0 >= vd) return;
     const int tid = threadIdx.x;
     const int lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int hw = wave / WH, h = h0 + hw;  // the wavefront's head
 
     const Segment g = find_segment(p, w);
     if (g.count == 0 || (LOCAL && g.index == g.count - 1)) return;
@@ -206,40 +235,43 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     // the segment's tokens: n of them, from t0 upwards
     const int skip = p.seg == 0 ? 0 : g.index * p.seg;
     const int n = p.seg == 0 ? g.len : min(p.seg, g.len - skip);
-    const bool rev = op.reverse != 0;
     const int64_t t0 = rev ? g.begin + g.len - skip - n : g.begin + skip;
-    // log2 of the decay; -infinity as a finite number, so that times 0 it is 0
-    const float ld = p.log_decay[h] * kLog2e;
-    const float l2 = ld < -1e30f ? -1e30f : ld;
+    const float l2 = log2_decay(p, h);
     const float shift = rev ? 1.f : 0.f;
 
-    // ---- the state: register 4 y + e (y 0, 1) of block t holds v channel vch
-    // and k channel 32 t + 8 q4 + 4 y + e
-    const int vch = v0 + 16 * wave + l16;
-    const bool vch_in = vch < op.vd;
-    const int64_t state_at = (slot * p.H + h) * p.state_size + (int64_t)vch * op.sv;
+    // ---- the state: register e of S[t][y][d] holds k channel 32 t + 8 q4 + 4 y
+    // + e and v channel vch(d)
+    const int tile0 = wave % WH * DT;  // the wavefront's first tile of the head's value channels
+    auto vch = [&](int d) { return v0 + 32 * ((tile0 + d) >> 1) + column(l16, (tile0 + d) & 1); };
+    const int64_t state_at = (slot * p.H + h) * p.state_size;
     // the wavefront's part of the segment's slot in the workspace
     f32x4 *const part = reinterpret_cast<f32x4 *>(
-        p.parts + ((((int64_t)which * p.slots + w) * p.H + h) * p.tiles * VT + v0 + 16 * wave) * KD) + lane;
-    f32x4 S[NT][2];
+        p.parts + ((((int64_t)which * p.slots + w) * p.H + h) * p.tiles * VT + v0 + 16 * tile0) * KD) + lane;
+    f32x4 S[NT][2][DT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) S[t][0] = S[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) S[t][0][d] = S[t][1][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (!LOCAL) {
         if (g.count > 1) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) S[t][y] = part[(t * 2 + y) * 64];
-        } else if (resumes(p, op, g.b) && vch_in) {
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int kc = 32 * t + 8 * q4;
-                if (kc >= op.kd) continue;
-                float f[8];
-                read_state<SB>(op.state_in, state_at + kc * op.sk, op.sk, f);
+                    for (int y = 0; y < 2; ++y) S[t][y][d] = part[((d * NT + t) * 2 + y) * 64];
+        } else if (resumes(p, op, g.b)) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) S[t][e / 4][e % 4] = f[e];
-            }
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int kc = 32 * t + 8 * q4;
+                    if (kc >= op.kd || vch(d) >= op.vd) continue;
+                    float f[8];
+                    read_state<SB>(op.state_in, state_at + vch(d) * op.sv + kc * op.sk, op.sk, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) S[t][e / 4][d][e % 4] = f[e];
+                }
         }
     }
 
@@ -248,24 +280,25 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     // at the last place, where the weights of the state update are the full
     // chunk's, and starts with rows of zeros.
     // In LDS: weights of the scores by distance i - j (0 above the diagonal),
-    // from distance -31 on, and of the last 32 tokens in the state update.
-    if (tid < 64 + 31) {
-        const int d = tid - 31;
-        s_pair[tid] = d >= 0 ? op.scale_pair * fast_exp2(l2 * (float)d) : 0.f;
-        if (tid < 32) s_lead[tid] = op.scale_update * fast_exp2(l2 * ((float)tid + shift));
+    // from distance -31 on, and of the tokens in the state update, last first.
+    if (tid < HP * 128) {
+        const int i = tid & 127, d = i - 31;
+        const float l2h = HP == 1 ? l2 : log2_decay(p, h0 + (tid >> 7));
+        if (i < 95) s_pair[tid >> 7][i] = d >= 0 ? op.scale_pair * fast_exp2(l2h * (float)d) : 0.f;
+        if (i < 64) s_lead[tid >> 7][i] = op.scale_update * fast_exp2(l2h * ((float)i + shift));
     }
     const bool fine = !SB && op.state_out != nullptr;  // three parts of the weighted v, or two
-    const float by32 = fast_exp2(l2 * 32.f);
 
-    const int64_t qs = op.q.stride, ks = op.k.stride, vs = op.v.stride, os = (int64_t)p.H * op.vd;
-    const uint16_t *gq = op.q.p + (int64_t)(h / op.q.div) * op.kd;
-    const uint16_t *gk = op.k.p + (int64_t)(h / op.k.div) * op.kd;
-    const uint16_t *gv = op.v.p + (int64_t)(h / op.v.div) * op.vd;
-    // A thread's unit and row of the loads: 16 lanes take 4 rows of 4 units.
-    // The thread number is made opaque wherever they are used, so that they are
-    // formed again instead of held in some ten registers across the chunk.
-    auto unit_of = [](int t, int U) { return (t >> 4) % (U / 4) * 4 + (t & 3); };
-    auto row_of = [](int t, int U) { return (t >> 4) / (U / 4) * 4 + (t >> 2) % 4; };
+    const int os = p.H * vd;
+    const uint16_t *gq = op.q.p + (int64_t)(h0 / op.q.div) * kd;
+    const uint16_t *gk = op.k.p + (int64_t)(h0 / op.k.div) * kd;
+    const uint16_t *gv = op.v.p + (int64_t)(h0 / op.v.div) * vd;
+    // A thread's unit and row of the loads: 8 lanes take 4 rows of 2 units (the
+    // stores to LDS use 32 banks at a time).  The thread number is made opaque
+    // wherever they are used, so that they are formed again instead of held in
+    // some ten registers across the chunk.
+    auto unit_of = [](int t, int U) { return (t >> 3) % (U / 2) * 2 + (t & 1); };
+    auto row_of = [](int t, int U) { return (t >> 3) / (U / 2) * 4 + (t >> 1) % 4; };
     auto opaque = [](int t) {
         asm volatile("" : "+v"(t));
         return t;
@@ -275,11 +308,12 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     auto fetch = [&](int c0) {  // the chunk's rows, lowest token first, into registers
         const int len = min(kTok, n - c0);
         const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
-        const auto bk = rows_buffer(gk + first * ks, (uint32_t)((len - 1) * ks + op.kd) * 2);
-        const auto bv = rows_buffer(gv + first * vs, (uint32_t)((len - 1) * vs + op.vd) * 2);
+        const auto bk = rows_buffer(gk + first * ks, (uint32_t)((len - 1) * ks + kd) * 2);
+        const auto bv = rows_buffer(gv + first * vs, (uint32_t)((len - 1) * vs + HP * vd) * 2);
         const int t = opaque(tid), ck = unit_of(t, UK), rk = row_of(t, UK), cv = unit_of(t, UV), rv = row_of(t, UV);
-        const uint32_t ok = 8 * ck < op.kd ? (uint32_t)(rk * (int)ks + 8 * ck) * 2 : kNowhere;
-        const uint32_t ov = v0 + 8 * cv < op.vd ? (uint32_t)(rv * (int)vs + v0 + 8 * cv) * 2 : kNowhere;
+        const int hv = cv / (VT / 8), vc = v0 + cv % (VT / 8) * 8;  // head and channel of the v unit
+        const uint32_t ok = 8 * ck < kd ? (uint32_t)(rk * ks + 8 * ck) * 2 : kNowhere;
+        const uint32_t ov = vc < vd ? (uint32_t)(rv * vs + hv * vd + vc) * 2 : kNowhere;
 #pragma unroll
         for (int i = 0; i < LK; ++i)
             fk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, ok + i * RK * (uint32_t)ks * 2, 0, 0);
@@ -287,8 +321,8 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
         for (int i = 0; i < LV; ++i)
             fv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, ov + i * RV * (uint32_t)vs * 2, 0, 0);
         if constexpr (!LOCAL) {
-            const auto bq = rows_buffer(gq + first * qs, (uint32_t)((len - 1) * qs + op.kd) * 2);
-            const uint32_t oq = 8 * ck < op.kd ? (uint32_t)(rk * (int)qs + 8 * ck) * 2 : kNowhere;
+            const auto bq = rows_buffer(gq + first * qs, (uint32_t)((len - 1) * qs + kd) * 2);
+            const uint32_t oq = 8 * ck < kd ? (uint32_t)(rk * qs + 8 * ck) * 2 : kNowhere;
 #pragma unroll
             for (int i = 0; i < LK; ++i)
                 fq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, oq + i * RK * (uint32_t)qs * 2, 0, 0);
@@ -296,43 +330,81 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
     };
     if (n > 0) fetch(0);
 
-    f32x4 O[4] = {};
-    // Stores the outputs of the chunk at c0: place 16 rt + l16, 4 channels from
-    // 4 q4.  A chunk's outputs leave behind the barriers of the next one, ahead
-    // of its loads: waiting for loads then never waits for younger stores.
+    // in 16-row tile rt of q, scores and outputs, lane l16 is token place0 + row_tile(rt)
+    auto row_tile = [](int rt) { return 32 * (rt >> 1) + 4 * (rt & 1); };
+    const int place0 = 8 * (l16 >> 2) + (l16 & 3);
+    f32x4 O[4][DT] = {};
+    // Stores the outputs of the chunk at c0: a token a tile, channels 8 q4 .. of
+    // a pair of tiles (half of them with one tile).  A chunk's outputs leave behind
+    // the barriers of the next one, ahead of its loads: waiting for loads then
+    // never waits for younger stores.
     auto emit = [&](int c0) {
         const int len = min(kTok, n - c0), pad = kTok - len;
         const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
-        const int eb = op.out_f32 ? 4 : 2;
-        const auto bo = rows_buffer(static_cast<char *>(op.out) + (first * os + (int64_t)h * op.vd) * eb,
-                                    (uint32_t)((len - 1) * os + op.vd) * eb);
-        const int vc = v0 + 16 * wave + 4 * q4;
+        const int eb = out_f32 ? 4 : 2;
+        const auto bo = rows_buffer(static_cast<char *>(op.out) + (first * os + (int64_t)h * vd) * eb,
+                                    (uint32_t)((len - 1) * os + vd) * eb);
+        const int vc = v0 + 32 * (tile0 >> 1) + 8 * q4 + 4 * (tile0 & 1);
+        const int tok0 = rev ? 63 - place0 : place0 - pad;
+        const uint32_t at0 = (uint32_t)((tok0 * os + vc) * eb);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const int r = 16 * rt + l16;
-            const int tok = rev ? 63 - r : r - pad;
-            const uint32_t at =
-                vc < op.vd && (uint32_t)tok < (uint32_t)len ? (uint32_t)(tok * (int)os + vc) * eb : kNowhere;
-            if (op.out_f32)
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[rt]), bo, at, 0, 0);
-            else
-                __builtin_amdgcn_raw_buffer_store_b64(
-                    u32x2{pack_bf16x2(O[rt][0], O[rt][1]), pack_bf16x2(O[rt][2], O[rt][3])}, bo, at, 0, 0);
+            const int more = row_tile(rt);
+            const int tok = rev ? tok0 - more : tok0 + more;
+            const uint32_t at = vc < vd && (uint32_t)tok < (uint32_t)len
+                                    ? at0 + (uint32_t)((rev ? -more : more) * os * eb)
+                                    : kNowhere;
+            if constexpr (DT == 2) {
+                const f32x4 lo = O[rt][0], hi = O[rt][1];
+                if (out_f32) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, lo), bo, at, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, hi), bo, at + 16, 0, 0);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                              pack_bf16x2(hi[2], hi[3])},
+                        bo, at, 0, 0);
+                }
+            } else {
+                const f32x4 x = O[rt][0];
+                if (out_f32)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), bo, at, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b64(
+                        u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, bo, at, 0, 0);
+            }
         }
     };
 
-    // a lane's places: rows l16 of unit q4; rows of k as two tiles; columns
+    // a lane's places: row l16 of unit q4; row place0; columns of k and v tiles
     const int at_row = q4 * kUnit + l16 * 16;
-    const int at_key = q4 * kUnit + (8 * (l16 >> 2) + (l16 & 3)) * 16;
-    const int at_col = (8 * q4 + (l16 >> 2)) * 16;
-    const int at_kcol = at_col + (l16 & 3) * kUnit;
-    const int at_vcol = at_col + (2 * wave + ((l16 & 3) >> 1)) * kUnit + (l16 & 1) * 8;
-    const float *const w_pair = s_pair + 31 + 16 * (wave & 3) + l16 - 8 * q4, *const w_lead = s_lead + 31 - 8 * q4;
+    const int at_place = q4 * kUnit + place0 * 16;
+    const int at_col = (4 * q4 + (l16 >> 2)) * 16 + (l16 & 3) * kUnit;
+    const int v_units = (hw * (VT / 8) + 4 * (tile0 >> 1)) * kUnit;
+    const float *const w_pair = s_pair[0] + 31 + place0 - 4 * q4;
+    const float *const w_lead = s_lead[hw] + 63 - 4 * q4;
+    const int scores = hw * kScores;
 
+    // the chunk's v columns, kept for the scores' product
+    bf16x8 vcol[kTok / 32][DT];
+    // out^T += v^T scores^T of the chunk whose scores are complete
+    auto add_scores = [&]() {
+#pragma unroll
+        for (int u = 0; u < kTok / 32; ++u)
+#pragma unroll
+            for (int rt = 2 * u; rt < 4; ++rt) {
+                const bf16x8 x = read_unit(s_p, scores + at_place + row_tile(rt) * 16 + 4 * u * kUnit);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) O[rt][d] = mfma_bf16(vcol[u][d], x, O[rt][d]);
+            }
+    };
+
+    // Two barriers a chunk: between them lie (A to B) the rows' way into LDS
+    // and the scores' product of the chunk before, and (B to A) everything else.
 #pragma unroll 1
     for (int c0 = 0; c0 < n; c0 += kTok) {
         const int len = min(kTok, n - c0), pad = kTok - len;
-        __syncthreads();  // the previous chunk's rows are no longer read
+        __syncthreads();  // A: the previous chunk's rows are read, its scores written
         // token i of the chunk to its place; tokens past it (zeros) wrap to the places before it
         const int ft = opaque(tid), ck = unit_of(ft, UK), rk = row_of(ft, UK), cv = unit_of(ft, UV),
                   rv = row_of(ft, UV);
@@ -347,115 +419,149 @@ __global__ __launch_bounds__(64 * NW, waves_of(KD, NW)) void la_walk(Params p) {
             const int r = rev ? 63 - (rv + i * RV) : (rv + i * RV + pad) & 63;
             *reinterpret_cast<u32x4 *>(s_v + cv * kUnit + r * 16) = fv[i];
         }
-        __syncthreads();
-        if (!LOCAL && c0 > 0) emit(c0 - kTok);
+        if (!LOCAL && c0 > 0) {
+            add_scores();
+            emit(c0 - kTok);
+        }
+        __syncthreads();  // B
         if (c0 + kTok < n) fetch(c0 + kTok);
 
         if constexpr (!LOCAL) {
+            // ---- weighted scores, for all heads, in blocks of 16 RB tokens i
+            // (lanes) x 32 tokens j (8 a lane): with four wavefronts 32 x 32 blocks
+            // (rt, c) = (0, 0) (2, 0) (2, 1), with eight 16 x 32 ones
+            constexpr int RB = NW == 4 ? 2 : 1;
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) O[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            // ---- weighted scores in blocks of 16 tokens i (lanes) x 32 tokens
-            // j (8 consecutive ones a lane): blocks (rt, c) = (0,0) (1,0) (2,0)
-            // (3,0) (2,1) (3,1).  Wavefront m takes block m, and with four
-            // of them 0 and 1 also 4 and 5, which lie as far below the diagonal
-#pragma unroll
-            for (int m = 0; m < 6; ++m) {
-                if (m % NW != wave) continue;
-                const int rt = m < 4 ? m : m - 2, c = m < 4 ? 0 : 1;
-                f32x4 a[2] = {};
+            for (int m = 0; m < 6 / RB; ++m) {
+                if (m != wave) continue;
+                const int c = m < 4 / RB ? 0 : 1, rt = RB * m - 2 * c;
+                f32x4 a[RB][2] = {};
 #pragma unroll
                 for (int u = 0; u < KD / 32; ++u) {
-                    const bf16x8 q = read_unit(s_q, at_row + 16 * rt * 16 + 4 * u * kUnit);
+                    bf16x8 q[RB];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        a[y] = mfma_bf16(read_unit(s_k, at_key + (32 * c + 4 * y) * 16 + 4 * u * kUnit), q, a[y]);
+                    for (int i = 0; i < RB; ++i)
+                        q[i] = read_unit(s_q, at_place + row_tile(rt + i) * 16 + 4 * u * kUnit);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const bf16x8 k = read_unit(s_k, at_row + (32 * c + 16 * y) * 16 + 4 * u * kUnit);
+#pragma unroll
+                        for (int i = 0; i < RB; ++i) a[i][y] = mfma_bf16(k, q[i], a[i][y]);
+                    }
                 }
-                float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = a[e / 4][e % 4] * w_pair[-e];
-                *reinterpret_cast<bf16x8 *>(s_p + at_row + 16 * rt * 16 + 4 * c * kUnit) = pack8(f);
+                for (int x = 0; x < HP; ++x)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = a[i][e / 4][e % 4] *
+                                   w_pair[96 * x + row_tile(rt + i) - 32 * c - 16 * (e / 4) - e % 4];
+                        *reinterpret_cast<bf16x8 *>(s_p + x * kScores + at_place + row_tile(rt + i) * 16 +
+                                                    4 * c * kUnit) = pack8(f);
+                    }
             }
             // ---- output from the state, out^T = S q^T (channels x tokens)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                float f[8];
+                bf16x8 a[DT];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][e % 4];
-                const bf16x8 a = pack8(f);
+                for (int d = 0; d < DT; ++d) {
+                    float f[8];
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt)
-                    O[rt] = mfma_bf16(a, read_unit(s_q, at_row + 16 * rt * 16 + 4 * t * kUnit), O[rt]);
-            }
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt)
-                O[rt] *= op.scale_state * fast_exp2(l2 * ((float)(16 * rt + l16 - pad + 1) - shift));
-            __syncthreads();  // scores complete
-        }
-
-        // ---- output from the chunk, and the state update, 32 tokens at a time
-        const float keep = fast_exp2(l2 * (float)len);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            S[t][0] *= keep;
-            S[t][1] *= keep;
-        }
-#pragma unroll
-        for (int u = 0; u < kTok / 32; ++u) {
-            const bf16x8 v = read_columns(s_v, at_vcol + 32 * u * 16);
-            if constexpr (!LOCAL) {
-#pragma unroll
-                for (int rt = 2 * u; rt < 4; ++rt)
-                    O[rt] = mfma_bf16(v, read_unit(s_p, at_row + 16 * rt * 16 + 4 * u * kUnit), O[rt]);
-            }
-            float f[8], r[8];
-            unpack8(v, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= w_lead[-e] * (u == 0 ? by32 : 1.f);
-            const bf16x8 w1 = pack8(f);
-            unpack8(w1, r);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] -= r[e];
-            const bf16x8 w2 = pack8(f);
-            bf16x8 w3;
-            if (fine) {
-                unpack8(w2, r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] -= r[e];
-                w3 = pack8(f);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const bf16x8 k0 = read_columns(s_k, at_kcol + 32 * u * 16 + 4 * t * kUnit);
-                const bf16x8 k1 = read_columns(s_k, at_kcol + 32 * u * 16 + 4 * t * kUnit + 8);
-                if (fine) {
-                    S[t][0] = mfma_bf16(k0, w3, S[t][0]);
-                    S[t][1] = mfma_bf16(k1, w3, S[t][1]);
+                    for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][d][e % 4];
+                    a[d] = pack8(f);
                 }
-                S[t][0] = mfma_bf16(k0, w2, S[t][0]);
-                S[t][1] = mfma_bf16(k1, w2, S[t][1]);
-                S[t][0] = mfma_bf16(k0, w1, S[t][0]);
-                S[t][1] = mfma_bf16(k1, w1, S[t][1]);
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    const bf16x8 q = read_unit(s_q, at_place + row_tile(rt) * 16 + 4 * t * kUnit);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        O[rt][d] = mfma_bf16(a[d], q, t == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : O[rt][d]);
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const float x = scale_state * fast_exp2(l2 * ((float)(place0 + row_tile(rt) - pad + 1) - shift));
+#pragma unroll
+                for (int d = 0; d < DT; ++d) O[rt][d] *= x;
             }
         }
-    }
-    if (!LOCAL && n > 0) emit((n - 1) / kTok * kTok);
 
-    if constexpr (LOCAL) {
+        // ---- the state update, 32 tokens at a time
+        const float keep = fast_exp2(l2 * (float)len);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) part[(t * 2 + y) * 64] = S[t][y];
-    } else {
-        if (g.index != g.count - 1 || op.state_out == nullptr || !vch_in) return;
+            for (int d = 0; d < DT; ++d) {
+                S[t][0][d] *= keep;
+                S[t][1][d] *= keep;
+            }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int kc = 32 * t + 8 * q4;
-            if (kc >= op.kd) continue;
-            float f[8];
+        for (int u = 0; u < kTok / 32; ++u) {
+            bf16x8 part3[DT][3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][e % 4];
-            write_state<SB>(op.state_out, state_at + kc * op.sk, op.sk, f);
+            for (int d = 0; d < DT; ++d) {
+                vcol[u][d] = read_columns(s_v, at_col + v_units + 8 * ((tile0 + d) & 1) + 32 * u * 16);
+                float f[8], r[8];
+                unpack8(vcol[u][d], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= w_lead[-32 * u - 16 * (e / 4) - e % 4];
+                part3[d][0] = pack8(f);
+                unpack8(part3[d][0], r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] -= r[e];
+                part3[d][1] = pack8(f);
+                if (fine) {
+                    unpack8(part3[d][1], r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] -= r[e];
+                    part3[d][2] = pack8(f);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const bf16x8 k = read_columns(s_k, at_col + 8 * y + 32 * u * 16 + 4 * t * kUnit);
+                    if (fine) {
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) S[t][y][d] = mfma_bf16(k, part3[d][2], S[t][y][d]);
+                    }
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) S[t][y][d] = mfma_bf16(k, part3[d][1], S[t][y][d]);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) S[t][y][d] = mfma_bf16(k, part3[d][0], S[t][y][d]);
+                }
         }
+    }
+    if (!LOCAL && n > 0) {
+        __syncthreads();
+        add_scores();
+        emit((n - 1) / kTok * kTok);
+    }
+
+    if constexpr (LOCAL) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) part[((d * NT + t) * 2 + y) * 64] = S[t][y][d];
+    } else {
+        if (g.index != g.count - 1 || op.state_out == nullptr) return;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int kc = 32 * t + 8 * q4;
+                if (kc >= op.kd || vch(d) >= op.vd) continue;
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][d][e % 4];
+                write_state<SB>(op.state_out, state_at + vch(d) * op.sv + kc * op.sk, op.sk, f);
+            }
     }
 }
 
@@ -477,8 +583,9 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
     const int count = (len + p.seg - 1) / p.seg;
     const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[b] : (int64_t)b;
     if (count <= 1 || slot >= p.max_slots) return;
-    const int lane = i & 63, y = (i >> 6) & 1, t = (i >> 7) % (KD / 32), wave = (i >> 7) / (KD / 32);
-    const int vch = 16 * wave + (lane & 15), kc = 32 * t + 8 * (lane >> 4) + 4 * y;
+    const int lane = i & 63, y = (i >> 6) & 1, t = (i >> 7) % (KD / 32), tile = (i >> 7) / (KD / 32);
+    const int vch = 32 * (tile >> 1) + column(lane & 15, tile & 1);
+    const int kc = 32 * t + 8 * (lane >> 4) + 4 * y;
     const bool in = vch < op.vd && kc < op.kd;
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
     if (in && resumes(p, op, b)) {
@@ -492,8 +599,7 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
                           : static_cast<const float *>(op.state_in)[at + e * op.sk];
         }
     }
-    const float ld = p.log_decay[h] * kLog2e;
-    const float keep = fast_exp2((ld < -1e30f ? -1e30f : ld) * (float)p.seg);
+    const float keep = fast_exp2(log2_decay(p, h) * (float)p.seg);
     const int64_t step = (int64_t)p.H * per_head;
     f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) +
                   ((int64_t)which * p.slots + begin / p.seg + b) * step + (int64_t)h * per_head + i;
@@ -523,41 +629,51 @@ __global__ __launch_bounds__(256) void la_group_sum(const float *src, uint16_t *
     store_state8<true>(dst, i * 8, s);
 }
 
-template <int KD, int NW, bool SB>
-hipError_t launch_kd(const Params &p, hipStream_t s) {
-    const int64_t n = (int64_t)p.slots * p.H * p.tiles * p.nops;
-    const int64_t run = (int64_t)8 * p.share * p.tiles * p.nops;
+template <int KD, int NW, int DT, int HP, bool SB>
+hipError_t launch_variant(const Params &p, hipStream_t s) {
+    constexpr int VT = 16 * DT * NW / HP;
+    const int64_t n = (int64_t)p.slots * (p.H / HP) * p.tiles * p.nops;
+    const int64_t run = (int64_t)8 * (p.share / HP) * p.tiles * p.nops;
     const dim3 grid((unsigned)((n + run - 1) / run * run)), block(64 * NW);
     if (p.seg != 0) {
-        la_walk<KD, NW, SB, true><<<grid, block, 0, s>>>(p);
-        const int blocks = (p.tiles * 16 * NW * KD / 4 + 255) / 256;
+        la_walk<KD, NW, DT, HP, SB, true><<<grid, block, 0, s>>>(p);
+        const int blocks = (p.tiles * VT * KD / 4 + 255) / 256;
         const dim3 cg((unsigned)(p.batch * p.H * blocks), (unsigned)p.nops);
-        la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, 16 * NW);
+        la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, VT);
     }
-    la_walk<KD, NW, SB, false><<<grid, block, 0, s>>>(p);
+    la_walk<KD, NW, DT, HP, SB, false><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
-template <int KD>
-hipError_t launch_nw(const Params &p, const Shape &h, hipStream_t s) {
-    if (h.nw == 4) return p.state_bf16 ? launch_kd<KD, 4, true>(p, s) : launch_kd<KD, 4, false>(p, s);
-    return p.state_bf16 ? launch_kd<KD, 8, true>(p, s) : launch_kd<KD, 8, false>(p, s);
+template <int KD, bool SB>
+hipError_t launch_kd(const Params &p, const Shape &h, hipStream_t s) {
+    constexpr int NW = KD == 256 ? 8 : 4, DT = KD == 256 ? 1 : 2;
+    if (h.vt == 128) return launch_variant<KD, NW, DT, 1, SB>(p, s);
+    if (h.heads == 2) return launch_variant<KD, NW, DT, 2, SB>(p, s);
+    return launch_variant<KD, 4, 1, 1, SB>(p, s);
+}
+template <bool SB>
+hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
+    if (h.kd == 64) return launch_kd<64, SB>(p, h, s);
+    if (h.kd == 128) return launch_kd<128, SB>(p, h, s);
+    return launch_kd<256, SB>(p, h, s);
 }
 }  // namespace
 
 // Segments: a walk is a chain of chunks, so a launch needs enough of them
 // side by side: kTarget workgroups, two per compute unit, each of at least
 // kLeast tokens.  Sequences no longer than a segment are not cut.
-Shape shape_of(int64_t T, int batch, int H, int kd, int vd, int nops) {
-    constexpr int64_t kTarget = 512, kLeast = 256;
+Shape shape_of(int64_t T, int batch, int H, int share, int kd, int vd, int nops) {
+    const int64_t kTarget = getenv("LA_T") ? atoi(getenv("LA_T")) : 512, kLeast = getenv("LA_L") ? atoi(getenv("LA_L")) : 256;
     Shape h;
     h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
-    h.nw = vd <= 64 ? 4 : 8;
-    h.tiles = (vd + 16 * h.nw - 1) / (16 * h.nw);
-    const int64_t want = T * H * h.tiles * nops / kTarget;  // tokens
+    h.vt = vd <= 64 ? 64 : 128;
+    h.heads = h.vt == 64 && share % 2 == 0 && nops == 1 ? 2 : 1;
+    h.tiles = (vd + h.vt - 1) / h.vt;
+    const int64_t want = T * (H / h.heads) * h.tiles * nops / kTarget;  // tokens
     const int64_t seg = std::max((want + kTok - 1) / kTok * kTok, kLeast);
     h.seg = T > seg ? (int)seg : 0;
     h.slots = h.seg != 0 ? (int)(T / seg) + batch : batch;
-    h.bytes = h.seg != 0 ? (size_t)nops * h.slots * H * h.tiles * 16 * h.nw * h.kd * sizeof(float) : 0;
+    h.bytes = h.seg != 0 ? (size_t)nops * h.slots * H * h.tiles * h.vt * h.kd * sizeof(float) : 0;
     return h;
 }
 
@@ -566,9 +682,7 @@ hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s) {
     p.tiles = h.tiles;
     p.seg = h.seg;
     p.slots = h.slots;
-    if (h.kd == 64) return launch_nw<64>(p, h, s);
-    if (h.kd == 128) return launch_nw<128>(p, h, s);
-    return launch_nw<256>(p, h, s);
+    return p.state_bf16 ? launch_any<true>(p, h, s) : launch_any<false>(p, h, s);
 }
 
 hipError_t launch_group_sum(const float *src, uint16_t *dst, const Params &p, int div, int width, hipStream_t s) {

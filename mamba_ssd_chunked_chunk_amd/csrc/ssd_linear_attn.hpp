@@ -64,11 +64,12 @@ struct Params {
 
 // What a launch takes of kd x vd channels (the largest of its operations').
 struct Shape {
-    int kd, nw, tiles;  // kd rounded up; wavefronts (of 16 value channels) and workgroups along vd
+    int kd, vt, tiles;  // kd rounded up; value channels of a workgroup, and workgroups along vd
+    int heads;          // heads of a workgroup
     int seg, slots;
     size_t bytes;       // of `parts`
 };
-Shape shape_of(int64_t T, int batch, int H, int kd, int vd, int nops);
+Shape shape_of(int64_t T, int batch, int H, int share, int kd, int vd, int nops);
 hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s);
 
 // sums the heads of each group: dst[t][g][w] = sum_i src[t][g * div + i][w]

@@ -51,7 +51,8 @@ struct Layout {
 Layout layout_of(const ssd_linear_attn_problem *p, bool backward) {
     Layout L = {};
     const int K = p->key_dim, V = p->value_dim, m = K > V ? K : V;
-    L.shape = ssd::la::shape_of(p->total_len, p->batch, p->nheads, backward ? m : K, backward ? m : V,
+    L.shape = ssd::la::shape_of(p->total_len, p->batch, p->nheads, p->nheads / p->ngroups,
+                                backward ? m : K, backward ? m : V,
                                 backward ? 3 : 1);
     L.bytes = align_up(L.shape.bytes);
     L.shared = backward && p->nheads != p->ngroups;
