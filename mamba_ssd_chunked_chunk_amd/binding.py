@@ -10,6 +10,7 @@ kernels; there is no fallback of any kind.  torch only provides device memory
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -90,6 +91,8 @@ SHORT_PATH_DEFAULT = -1  # ssd_problem.short_path_max: any negative value select
 def load_library():
     """Load libssd.so; raises if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -407,18 +410,36 @@ def ssd_linear_attn_workspace_size(prob: ssd_linear_attn_problem, backward=False
     return n.value
 
 
-def _token_stride(t, name, shape, device):
-    """Elements between tokens of a bf16 [T, n, D] tensor whose tokens are dense rows (a slice of a wider
-    projection is one); 0 for a dense tensor."""
-    import torch
+def _refuse_tensor(t, name, dtype, shape, device):
+    """Why a tensor is not a dense one of this type and shape on the device."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dense(t, name, dtype, shape, device):
+    """Address of a dense tensor of this type and shape on the device (one test where all is well)."""
+    if t is None or t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse_tensor(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _dense_or_none(t, name, dtype, shape, device):
+    return None if t is None or t.numel() == 0 else _dense(t, name, dtype, shape, device)
+
+
+def _token_stride(t, name, shape, device):
+    """Elements between tokens of a bf16 [T, n, D] tensor whose tokens are dense rows (a slice of a wider
+    projection is one); 0 for a dense tensor."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device:
+        _refuse_tensor(t, name, torch.bfloat16, shape, device)
     if t.is_contiguous():
         return 0
     T, n, D = shape
@@ -429,8 +450,16 @@ def _token_stride(t, name, shape, device):
     return t.stride(0) if T > 1 else 0
 
 
+@functools.lru_cache(maxsize=256)
+def _linear_attn_sizes(*sizes):
+    """(reference to the problem of these sizes, its workspace bytes forward and backward)"""
+    prob = make_linear_attn_problem(*sizes)
+    return (ctypes.byref(prob), ssd_linear_attn_workspace_size(prob), ssd_linear_attn_workspace_size(prob, True))
+
+
 def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
-    """Problem of a linear-attention call, its tensors checked."""
+    """What a linear-attention call goes by, its inputs checked: problem, workspace bytes (forward, backward),
+    device, shape of a state."""
     import torch
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t is None or t.dim() != 3:
@@ -440,52 +469,64 @@ def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
         raise ValueError("libssd runs on a HIP device; got tensors on " + str(dev))
     T, H, V = v.shape
     G, K = q.shape[1], q.shape[2]
-    strides = [_token_stride(q, "q", (T, G, K), dev), _token_stride(k, "k", (T, G, K), dev),
-               _token_stride(v, "v", (T, H, V), dev)]
-    _need(log_decay, "log_decay", torch.float32, (H,), dev)
-    return make_linear_attn_problem(T, batch, H, G, K, V, max_slots, state_dtype,
-                                    K ** -0.5 if scale is None else scale, *strides), dev
+    qk = (T, G, K)
+    strides = (_token_stride(q, "q", qk, dev), _token_stride(k, "k", qk, dev), _token_stride(v, "v", (T, H, V), dev))
+    _dense(log_decay, "log_decay", torch.float32, (H,), dev)
+    prob, forward, backward = _linear_attn_sizes(T, batch, H, G, K, V, max_slots, state_dtype,
+                                                 K ** -0.5 if scale is None else float(scale), *strides)
+    return prob, forward, backward, dev, (H, V, K)
 
 
 def _slots(cache_indices, has_initial_state, batch, dev):
+    """Addresses of cache_indices and has_initial_state (or None), checked."""
     import torch
     if cache_indices.dtype not in (torch.int32, torch.uint32):
         raise TypeError("cache_indices must be int32 or uint32")
-    if tuple(cache_indices.shape) != (batch,) or not cache_indices.is_contiguous() or cache_indices.device != dev:
-        raise ValueError("cache_indices must be a contiguous [batch] tensor on the same device")
+    idx = _dense(cache_indices, "cache_indices", cache_indices.dtype, (batch,), dev)
     if has_initial_state is None or has_initial_state.numel() == 0:
-        return None
+        return idx, None
     if has_initial_state.dtype == torch.bool:
         has_initial_state = has_initial_state.view(torch.uint8)
-    _need(has_initial_state, "has_initial_state", torch.uint8, (batch,), dev)
-    return has_initial_state
+    return idx, _dense(has_initial_state, "has_initial_state", torch.uint8, (batch,), dev)
 
 
-class _On:
-    """The device of a call made current, and the stream it runs on."""
-
-    def __init__(self, dev, stream):
-        import torch
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
-        self.guard = torch.cuda.stream(self.stream)  # makes the stream's device current too
-
-    def __enter__(self):
-        self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def __exit__(self, *a):
-        return self.guard.__exit__(*a)
-
-
-def _workspace(workspace, need, dev):
-    """The caller's workspace, checked, or a new one (allocated on the call's stream)."""
+def _launch(name, dev, stream, call):
+    """Runs ``call(stream)`` on the stream (the current one for None) with the tensors' device current, and raises
+    what it returns."""
     import torch
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev:
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        status = call((stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call((stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
+    if status != SSD_OK:
+        _check(status, name)
+
+
+def _run(name, dev, stream, need, workspace, call):
+    """Runs ``call(workspace address, bytes, stream)`` on the stream (the current one for None) with the tensors'
+    device current, and raises what it returns; a workspace that the caller does not give is allocated on that
+    stream.  Returns the workspace."""
+    import torch
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.numel() < need or
+                                  workspace.device != dev):
         raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        status = call(workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        # entering a stream makes its device current too
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            if workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            status = call(workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+    if status != SSD_OK:
+        _check(status, name)
     return workspace
 
 
@@ -505,21 +546,15 @@ def ssd_linear_attn_varlen_fwd_inplace(o, q, k, v, log_decay, pool, query_start_
     """
     import torch
     batch = query_start_loc.numel() - 1
-    sd = _state_dtype(pool, "pool")
-    prob, dev = _linear_attn(q, k, v, log_decay, batch, pool.shape[0], sd, scale)
-    _need(o, "o", torch.bfloat16, v.shape, dev)
-    _need(pool, "pool", pool.dtype, (pool.shape[0], prob.nheads, prob.value_dim, prob.key_dim), dev)
-    _need(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
-    has_initial_state = _slots(cache_indices, has_initial_state, batch, dev)
-    need = ssd_linear_attn_workspace_size(prob)
-    with _On(dev, stream) as st:
-        workspace = _workspace(workspace, need, dev)
-        status = load_library().ssd_linear_attn_varlen_fwd_inplace(
-            ctypes.byref(prob), _ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(pool),
-            _ptr(query_start_loc), _ptr(has_initial_state), _ptr(cache_indices), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel()), st)
-    _check(status, "ssd_linear_attn_varlen_fwd_inplace")
-    return workspace
+    slots = pool.shape[0]
+    prob, need, _, dev, state = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
+    out = _dense(o, "o", torch.bfloat16, v.shape, dev)
+    states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
+    f = load_library().ssd_linear_attn_varlen_fwd_inplace
+    return _run("ssd_linear_attn_varlen_fwd_inplace", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, out, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), states, qsl, flags, idx, ws, n, st))
 
 
 def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_states, query_start_loc, *, scale=None,
@@ -532,21 +567,15 @@ def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_stat
     batch = query_start_loc.numel() - 1
     if final_states is None:
         raise ValueError("final_states is required")
-    sd = _state_dtype(final_states, "final_states")
-    prob, dev = _linear_attn(q, k, v, log_decay, batch, max(batch, 1), sd, scale)
-    shape = (batch, prob.nheads, prob.value_dim, prob.key_dim)
-    _need(o, "o", torch.bfloat16, v.shape, dev)
-    initial_states = _opt(initial_states, "initial_states", final_states.dtype, shape, dev)
-    _need(final_states, "final_states", final_states.dtype, shape, dev)
-    _need(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
-    need = ssd_linear_attn_workspace_size(prob)
-    with _On(dev, stream) as st:
-        workspace = _workspace(workspace, need, dev)
-        status = load_library().ssd_linear_attn_varlen_fwd(
-            ctypes.byref(prob), _ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_states),
-            _ptr(final_states), _ptr(query_start_loc), _ptr(workspace), ctypes.c_size_t(workspace.numel()), st)
-    _check(status, "ssd_linear_attn_varlen_fwd")
-    return workspace
+    prob, need, _, dev, state = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
+                                             _state_dtype(final_states, "final_states"), scale)
+    out = _dense(o, "o", torch.bfloat16, v.shape, dev)
+    first = _dense_or_none(initial_states, "initial_states", final_states.dtype, (batch, *state), dev)
+    last = _dense(final_states, "final_states", final_states.dtype, (batch, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    f = load_library().ssd_linear_attn_varlen_fwd
+    return _run("ssd_linear_attn_varlen_fwd", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, out, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), first, last, qsl, ws, n, st))
 
 
 def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_decay, initial_states,
@@ -559,27 +588,22 @@ def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_d
     """
     import torch
     batch = query_start_loc.numel() - 1
-    states = [(t, n) for t, n in ((d_initial_states, "d_initial_states"), (initial_states, "initial_states"),
-                                  (d_final_states, "d_final_states")) if t is not None]
-    sd = _state_dtype(*states[0]) if states else STATE_F32
-    prob, dev = _linear_attn(q, k, v, log_decay, batch, max(batch, 1), sd, scale)
-    shape = (batch, prob.nheads, prob.value_dim, prob.key_dim)
-    for t, n in states:
-        _need(t, n, states[0][0].dtype, shape, dev)
-    _need(dq, "dq", torch.bfloat16, q.shape, dev)
-    _need(dk, "dk", torch.bfloat16, k.shape, dev)
-    _need(dv, "dv", torch.bfloat16, v.shape, dev)
-    _need(d_o, "d_o", torch.bfloat16, v.shape, dev)
-    _need(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
-    need = ssd_linear_attn_workspace_size(prob, backward=True)
-    with _On(dev, stream) as st:
-        workspace = _workspace(workspace, need, dev)
-        status = load_library().ssd_linear_attn_varlen_bwd(
-            ctypes.byref(prob), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(d_initial_states), _ptr(q), _ptr(k), _ptr(v),
-            _ptr(d_o), _ptr(log_decay), _ptr(initial_states), _ptr(d_final_states), _ptr(query_start_loc),
-            _ptr(workspace), ctypes.c_size_t(workspace.numel()), st)
-    _check(status, "ssd_linear_attn_varlen_bwd")
-    return workspace
+    states = ((d_initial_states, "d_initial_states"), (initial_states, "initial_states"),
+              (d_final_states, "d_final_states"))
+    kind = next((t for t in states if t[0] is not None), None)
+    prob, _, need, dev, state = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
+                                             STATE_F32 if kind is None else _state_dtype(*kind), scale)
+    d_first, first, d_last = (None if t is None else _dense(t, n, kind[0].dtype, (batch, *state), dev)
+                              for t, n in states)
+    bf16 = torch.bfloat16
+    out = [_dense(dq, "dq", bf16, q.shape, dev), _dense(dk, "dk", bf16, k.shape, dev),
+           _dense(dv, "dv", bf16, v.shape, dev)]
+    grad = _dense(d_o, "d_o", bf16, v.shape, dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    f = load_library().ssd_linear_attn_varlen_bwd
+    return _run("ssd_linear_attn_varlen_bwd", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, *out, d_first, q.data_ptr(), k.data_ptr(), v.data_ptr(), grad, log_decay.data_ptr(), first, d_last, qsl,
+        ws, n, st))
 
 
 def ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, has_initial_state, cache_indices, *, scale=None,
@@ -590,20 +614,24 @@ def ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, has_initial_state,
     """
     import torch
     batch = v.shape[0]
-    sd = _state_dtype(pool, "pool")
-    prob, dev = _linear_attn(q, k, v, log_decay, batch, pool.shape[0], sd, scale)
-    _need(o, "o", torch.bfloat16, v.shape, dev)
-    _need(pool, "pool", pool.dtype, (pool.shape[0], prob.nheads, prob.value_dim, prob.key_dim), dev)
-    has_initial_state = _slots(cache_indices, has_initial_state, batch, dev)
-    with _On(dev, stream) as st:
-        status = load_library().ssd_linear_attn_step_inplace(
-            ctypes.byref(prob), _ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(pool),
-            _ptr(has_initial_state), _ptr(cache_indices), st)
-    _check(status, "ssd_linear_attn_step_inplace")
+    slots = pool.shape[0]
+    prob, _, _, dev, state = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
+    out = _dense(o, "o", torch.bfloat16, v.shape, dev)
+    states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
+    idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
+    f = load_library().ssd_linear_attn_step_inplace
+    _launch("ssd_linear_attn_step_inplace", dev, stream, lambda st: f(
+        prob, out, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), states, flags, idx, st))
+
+
+@functools.lru_cache(maxsize=256)
+def _state_cache_sizes(*sizes):
+    return ctypes.byref(ssd_state_cache_problem(*sizes))
 
 
 def _state_cache(pool, codes, scales, pool_indices, entry_indices):
-    """Problem of a state-cache call, its tensors checked."""
+    """Problem, device and addresses (pool, codes, scales, pool_indices, entry_indices) of a state-cache call,
+    its tensors checked."""
     import torch
     dev = pool.device
     if dev.type != "cuda":
@@ -611,21 +639,22 @@ def _state_cache(pool, codes, scales, pool_indices, entry_indices):
     if pool.dim() != 4:
         raise ValueError("pool must be [slots, H, P, N]")
     S, H, P, N = pool.shape
-    sd = _state_dtype(pool, "pool")
-    _need(pool, "pool", pool.dtype, (S, H, P, N), dev)
-    formats = {torch.int8: CODE_I8, torch.float8_e4m3fn: CODE_E4M3}
-    if codes.dtype not in formats:
+    if codes.dtype == torch.int8:
+        form = CODE_I8
+    elif codes.dtype == torch.float8_e4m3fn:
+        form = CODE_E4M3
+    else:
         raise TypeError(f"codes: expected int8 or float8_e4m3fn, got {codes.dtype}")
-    E = codes.shape[0]
-    _need(codes, "codes", codes.dtype, (E, H, P, N), dev)
-    _need(scales, "scales", torch.float32, (E, H, P), dev)
-    n = pool_indices.numel()
+    E, n = codes.shape[0], pool_indices.numel()
     for t, name in ((pool_indices, "pool_indices"), (entry_indices, "entry_indices")):
         if t.dtype not in (torch.int32, torch.uint32):
             raise TypeError(f"{name} must be int32 or uint32")
-        if tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be a contiguous [{n}] tensor on {dev}")
-    return ssd_state_cache_problem(n, H, P, N, S, E, sd, formats[codes.dtype]), dev
+    prob = _state_cache_sizes(n, H, P, N, S, E, _state_dtype(pool, "pool"), form)
+    return prob, dev, (_dense(pool, "pool", pool.dtype, (S, H, P, N), dev),
+                       _dense(codes, "codes", codes.dtype, (E, H, P, N), dev),
+                       _dense(scales, "scales", torch.float32, (E, H, P), dev),
+                       _dense(pool_indices, "pool_indices", pool_indices.dtype, (n,), dev),
+                       _dense(entry_indices, "entry_indices", entry_indices.dtype, (n,), dev))
 
 
 def ssd_state_quantize(codes, scales, pool, pool_indices, entry_indices, *, stream=None):
@@ -634,18 +663,14 @@ def ssd_state_quantize(codes, scales, pool, pool_indices, entry_indices, *, stre
     entry_indices[i] of ``codes`` (int8 or float8_e4m3fn [E,H,P,N]) and
     ``scales`` (fp32 [E,H,P]).  A pair with an index out of range is skipped.
     """
-    prob, dev = _state_cache(pool, codes, scales, pool_indices, entry_indices)
-    with _On(dev, stream) as st:
-        status = load_library().ssd_state_quantize(ctypes.byref(prob), _ptr(codes), _ptr(scales), _ptr(pool),
-                                                   _ptr(pool_indices), _ptr(entry_indices), st)
-    _check(status, "ssd_state_quantize")
+    prob, dev, (p, c, f, i, j) = _state_cache(pool, codes, scales, pool_indices, entry_indices)
+    fn = load_library().ssd_state_quantize
+    _launch("ssd_state_quantize", dev, stream, lambda st: fn(prob, c, f, p, i, j, st))
 
 
 def ssd_state_dequantize(pool, codes, scales, pool_indices, entry_indices, *, stream=None):
     """Read parked states back: slot pool_indices[i] of ``pool`` becomes entry
     entry_indices[i] of ``codes`` times its scales."""
-    prob, dev = _state_cache(pool, codes, scales, pool_indices, entry_indices)
-    with _On(dev, stream) as st:
-        status = load_library().ssd_state_dequantize(ctypes.byref(prob), _ptr(pool), _ptr(codes), _ptr(scales),
-                                                     _ptr(pool_indices), _ptr(entry_indices), st)
-    _check(status, "ssd_state_dequantize")
+    prob, dev, (p, c, f, i, j) = _state_cache(pool, codes, scales, pool_indices, entry_indices)
+    fn = load_library().ssd_state_dequantize
+    _launch("ssd_state_dequantize", dev, stream, lambda st: fn(prob, p, c, f, i, j, st))

@@ -32,7 +32,6 @@
 // into three bf16 parts that carry its 24 bits where the state is returned in
 // fp32, so it is that of fp32 sums; into two, 2.4e-6 off in norm, where it
 // only enters bf16 values (outputs, bf16 states).
-#include <stdlib.h>
 #include "ssd_linear_attn.hpp"
 
 namespace ssd {
@@ -228,6 +227,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hw = wave / WH, h = h0 + hw;  // the wavefront's head
 
+    if (LOCAL && op.twin != 0) return;  // la_chain makes its states from the twin's
     const Segment g = find_segment(p, w);
     if (g.count == 0 || (LOCAL && g.index == g.count - 1)) return;
     const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[g.b] : (int64_t)g.b;
@@ -438,6 +438,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
                 f32x4 a[RB][2] = {};
 #pragma unroll
                 for (int u = 0; u < KD / 32; ++u) {
+                    if (NT > 4 && 32 * u >= kd) break;
                     bf16x8 q[RB];
 #pragma unroll
                     for (int i = 0; i < RB; ++i)
@@ -465,6 +466,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
             // ---- output from the state, out^T = S q^T (channels x tokens)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                if (NT > 4 && 32 * t >= kd) break;  // a wide launch may hold narrower operations
                 bf16x8 a[DT];
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
@@ -492,12 +494,14 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
         // ---- the state update, 32 tokens at a time
         const float keep = fast_exp2(l2 * (float)len);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+            if (NT > 4 && 32 * t >= kd) break;
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
                 S[t][0][d] *= keep;
                 S[t][1][d] *= keep;
             }
+        }
 #pragma unroll
         for (int u = 0; u < kTok / 32; ++u) {
             bf16x8 part3[DT][3];
@@ -521,7 +525,8 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
                 }
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                if (NT > 4 && 32 * t >= kd) break;
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const bf16x8 k = read_columns(s_k, at_col + 8 * y + 32 * u * 16 + 4 * t * kUnit);
@@ -534,6 +539,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
 #pragma unroll
                     for (int d = 0; d < DT; ++d) S[t][y][d] = mfma_bf16(k, part3[d][0], S[t][y][d]);
                 }
+            }
         }
     }
     if (!LOCAL && n > 0) {
@@ -567,7 +573,10 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
 
 // The segments' own states into the states that enter them, in place: one
 // thread per 4 state elements of a (sequence, head), in the order of the
-// walk's registers.  Sequences of one segment are left to the walk.
+// walk's registers.  Sequences of one segment are left to the walk.  With
+// `mirror` the states are those of another operation too, transposed (its k
+// channels are this one's v channels and the reverse), and are written there
+// as well.
 template <bool SB>
 __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
     const int per_head = p.tiles * VT * KD / 4;  // groups of 4
@@ -578,7 +587,7 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
     const int h = id % p.H, b = id / p.H;
     const int which = blockIdx.y;
     const Op &op = p.op[which];
-    if (i >= per_head) return;
+    if (i >= per_head || op.twin != 0) return;
     const int begin = clamp_row(p, p.qsl[b]), len = max(clamp_row(p, p.qsl[b + 1]) - begin, 0);
     const int count = (len + p.seg - 1) / p.seg;
     const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[b] : (int64_t)b;
@@ -601,24 +610,35 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
     }
     const float keep = fast_exp2(log2_decay(p, h) * (float)p.seg);
     const int64_t step = (int64_t)p.H * per_head;
-    f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) +
-                  ((int64_t)which * p.slots + begin / p.seg + b) * step + (int64_t)h * per_head + i;
-    for (int s = 0; s < count - 1; ++s, part += step) {
-        const f32x4 own = *part;
+    const int64_t head = (int64_t)(begin / p.seg + b) * step + (int64_t)h * per_head;
+    f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) + (int64_t)which * p.slots * step + head + i;
+    // (v channel kc, k channel vch) of the mirror: element vch % 4 of the group of its
+    // lane (a backward launch holds as many v channels as k channels)
+    const bool mirrored = op.mirror != 0;
+    const int mtile = kc / 32 * 2 + (kc >> 2) % 2, mt = vch / 32, my = (vch >> 2) % 2;
+    const int mlane = vch % 32 / 8 * 16 + kc % 32 / 8 * 4;
+    float *twin = p.parts + 4 * ((int64_t)op.mirror * p.slots * step + head +
+                                 ((mtile * (KD / 32) + mt) * 2 + my) * 64 + mlane) + vch % 4;
+    for (int s = 0; s < count; ++s, part += step, twin += 4 * step) {
+        const f32x4 own = s < count - 1 ? *part : f32x4{0.f, 0.f, 0.f, 0.f};
         *part = S;
+        if (mirrored) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) twin[4 * e] = S[e];
+        }
         S = S * keep + own;
     }
-    *part = S;
 }
 
 // One thread per 8 channels of a (token, group); the sequences' rows only.
-__global__ __launch_bounds__(256) void la_group_sum(const float *src, uint16_t *dst, const int32_t *qsl, int batch,
-                                                    int64_t n8, int G, int div, int w8) {
+__global__ __launch_bounds__(256) void la_group_sum(GroupSum a, const int32_t *qsl, int batch, int64_t n8, int G,
+                                                    int div, int w8) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n8) return;
     const int64_t tg = i / w8, t = tg / G;
     if (t < qsl[0] || t >= qsl[batch]) return;
     const int c = (int)(i - tg * w8) * 8;
+    const float *src = a.src[blockIdx.y];
     float s[8] = {};
     for (int d = 0; d < div; ++d) {
         float f[8];
@@ -626,7 +646,7 @@ __global__ __launch_bounds__(256) void la_group_sum(const float *src, uint16_t *
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += f[e];
     }
-    store_state8<true>(dst, i * 8, s);
+    store_state8<true>(a.dst[blockIdx.y], i * 8, s);
 }
 
 template <int KD, int NW, int DT, int HP, bool SB>
@@ -659,18 +679,47 @@ hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
 }
 }  // namespace
 
-// Segments: a walk is a chain of chunks, so a launch needs enough of them
-// side by side: kTarget workgroups, two per compute unit, each of at least
-// kLeast tokens.  Sequences no longer than a segment are not cut.
-Shape shape_of(int64_t T, int batch, int H, int share, int kd, int vd, int nops) {
-    const int64_t kTarget = getenv("LA_T") ? atoi(getenv("LA_T")) : 512, kLeast = getenv("LA_L") ? atoi(getenv("LA_L")) : 256;
+// A walk is a chain of chunks, so a launch needs many walks side by side: the
+// card holds kAtOnce workgroups (two on each of 256 compute units, one of the
+// widest).
+//   - Enough sequences and heads for that: only sequences of more than twice a
+//     workgroup's share of the tokens are cut, which would end alone (32 ragged
+//     prompts of 128 heads, longest 8192: 629 us, cut at half of that 789).
+//   - Else the sequences, taken to be of equal length, are cut in the number
+//     that gives the fewest tokens one after the other, counting kSetup tokens'
+//     time for each segment's states (65536 tokens of 16 heads: 32 segments
+//     388 us, 48 418, 64 440; backward of 4 x 4096 tokens of 16 heads: 5
+//     segments 246 us, 3 263, 4 257).
+// Cut sequences cost a pass over their k and v for the segments' states.
+Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backward) {
+    constexpr int64_t kLeast = 256, kSetup = 128;
+    const int nops = backward ? 3 : 1, kd = backward ? std::max(K, V) : K, vd = backward ? kd : V;
     Shape h;
     h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
     h.vt = vd <= 64 ? 64 : 128;
     h.heads = h.vt == 64 && share % 2 == 0 && nops == 1 ? 2 : 1;
-    h.tiles = (vd + h.vt - 1) / h.vt;
-    const int64_t want = T * (H / h.heads) * h.tiles * nops / kTarget;  // tokens
-    const int64_t seg = std::max((want + kTok - 1) / kTok * kTok, kLeast);
+    const int64_t kAtOnce = h.kd == 256 ? 256 : 512;
+    auto tiles = [&](int d) { return (d + h.vt - 1) / h.vt; };
+    h.tiles = tiles(vd);
+    // workgroups of a token: o has V channels, or dq and dk K and dv V
+    const int64_t walks = (int64_t)(H / h.heads) * (tiles(V) + (backward ? 2 * tiles(K) : 0));
+    int64_t seg;
+    if (batch * walks >= kAtOnce) {
+        seg = 2 * T * walks / kAtOnce;
+    } else {
+        const int64_t mean = (T + batch - 1) / batch;
+        int64_t best = 0, least = 0;
+        for (int64_t n = 1; n == 1 || mean / n >= kLeast; ++n) {
+            const int64_t rounds = (batch * walks * n + kAtOnce - 1) / kAtOnce;
+            const int64_t time = rounds * ((mean + n - 1) / n + kSetup);
+            if (best == 0 || time < least) best = n, least = time;
+            if (rounds > 4) break;  // more, shorter segments only add their setup
+        }
+        seg = (mean + best - 1) / best;
+        // nothing to gain from cutting: leave sequences longer than the mean whole too, within reason
+        if (best == 1) seg = 2 * seg;
+    }
+    seg = std::max((seg + kTok - 1) / kTok * kTok, kLeast);
     h.seg = T > seg ? (int)seg : 0;
     h.slots = h.seg != 0 ? (int)(T / seg) + batch : batch;
     h.bytes = h.seg != 0 ? (size_t)nops * h.slots * H * h.tiles * h.vt * h.kd * sizeof(float) : 0;
@@ -685,11 +734,10 @@ hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s) {
     return p.state_bf16 ? launch_any<true>(p, h, s) : launch_any<false>(p, h, s);
 }
 
-hipError_t launch_group_sum(const float *src, uint16_t *dst, const Params &p, int div, int width, hipStream_t s) {
+hipError_t launch_group_sum(const GroupSum &a, const Params &p, int div, int width, hipStream_t s) {
     const int G = p.H / div;
     const int64_t n8 = p.T * G * (width / 8);
-    la_group_sum<<<dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s>>>(src, dst, p.qsl, p.batch, n8, G, div,
-                                                                         width / 8);
+    la_group_sum<<<dim3((unsigned)((n8 + 255) / 256), 2), dim3(256), 0, s>>>(a, p.qsl, p.batch, n8, G, div, width / 8);
     return hipGetLastError();
 }
 

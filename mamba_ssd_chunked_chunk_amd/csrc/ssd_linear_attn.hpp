@@ -39,6 +39,9 @@ struct Op {
     const void *state_in;
     void *state_out;
     int64_t sv, sk;
+    // dk and dv walk with the same states, transposed: the segments' are made
+    // for `dv` alone (mirror: the other's number), and handed to dk (twin: 1)
+    int mirror, twin;
 };
 
 constexpr int kMaxOps = 3;
@@ -69,11 +72,15 @@ struct Shape {
     int seg, slots;
     size_t bytes;       // of `parts`
 };
-Shape shape_of(int64_t T, int batch, int H, int share, int kd, int vd, int nops);
+Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backward);
 hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s);
 
-// sums the heads of each group: dst[t][g][w] = sum_i src[t][g * div + i][w]
-hipError_t launch_group_sum(const float *src, uint16_t *dst, const Params &p, int div, int width, hipStream_t s);
+// sums the heads of each group, twice: dst[t][g][w] = sum_i src[t][g * div + i][w]
+struct GroupSum {
+    const float *src[2];
+    uint16_t *dst[2];
+};
+hipError_t launch_group_sum(const GroupSum &a, const Params &p, int div, int width, hipStream_t s);
 
 struct StepParams {
     const uint16_t *q, *k, *v;

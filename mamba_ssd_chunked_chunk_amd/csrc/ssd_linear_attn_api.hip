@@ -50,10 +50,8 @@ struct Layout {
 };
 Layout layout_of(const ssd_linear_attn_problem *p, bool backward) {
     Layout L = {};
-    const int K = p->key_dim, V = p->value_dim, m = K > V ? K : V;
-    L.shape = ssd::la::shape_of(p->total_len, p->batch, p->nheads, p->nheads / p->ngroups,
-                                backward ? m : K, backward ? m : V,
-                                backward ? 3 : 1);
+    L.shape = ssd::la::shape_of(p->total_len, p->batch, p->nheads, p->nheads / p->ngroups, p->key_dim, p->value_dim,
+                                backward);
     L.bytes = align_up(L.shape.bytes);
     L.shared = backward && p->nheads != p->ngroups;
     if (L.shared) {
@@ -246,10 +244,13 @@ ssd_status ssd_linear_attn_varlen_bwd(
     ov.sv = p->key_dim;
     ov.sk = 1;
     ov.state_out = d_initial;
+    ok.twin = 1;
+    ov.mirror = 1;
     if (d_initial != nullptr && d_initial == d_final) {
         // dv overwrites d_final with d_initial: dk, which reads it too, runs first
+        ok.twin = ov.mirror = 0;
         Params b = a;
-        b.op[0] = a.op[2];
+        b.op[0] = ov;
         if (ssd::la::launch_walk(a, L.shape, 2, s) != hipSuccess || ssd::la::launch_walk(b, L.shape, 1, s) != hipSuccess)
             return SSD_ERR_HIP;
     } else if (ssd::la::launch_walk(a, L.shape, 3, s) != hipSuccess) {
@@ -257,11 +258,10 @@ ssd_status ssd_linear_attn_varlen_bwd(
     }
     if (shared && p->total_len > 0) {
         const int div = p->nheads / p->ngroups;
-        if (ssd::la::launch_group_sum(reinterpret_cast<float *>(ws + L.dq), static_cast<uint16_t *>(dq), a, div,
-                                      p->key_dim, s) != hipSuccess ||
-            ssd::la::launch_group_sum(reinterpret_cast<float *>(ws + L.dk), static_cast<uint16_t *>(dk), a, div,
-                                      p->key_dim, s) != hipSuccess)
-            return SSD_ERR_HIP;
+        const ssd::la::GroupSum sums = {
+            {reinterpret_cast<const float *>(ws + L.dq), reinterpret_cast<const float *>(ws + L.dk)},
+            {static_cast<uint16_t *>(dq), static_cast<uint16_t *>(dk)}};
+        if (ssd::la::launch_group_sum(sums, a, div, p->key_dim, s) != hipSuccess) return SSD_ERR_HIP;
     }
     return SSD_OK;
 }
