@@ -681,18 +681,16 @@ hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
 
 // A walk is a chain of chunks, so a launch needs many walks side by side: the
 // card holds kAtOnce workgroups (two on each of 256 compute units, one of the
-// widest).
-//   - Enough sequences and heads for that: only sequences of more than twice a
-//     workgroup's share of the tokens are cut, which would end alone (32 ragged
-//     prompts of 128 heads, longest 8192: 629 us, cut at half of that 789).
-//   - Else the sequences, taken to be of equal length, are cut in the number
-//     that gives the fewest tokens one after the other, counting kSetup tokens'
-//     time for each segment's states (65536 tokens of 16 heads: 32 segments
-//     388 us, 48 418, 64 440; backward of 4 x 4096 tokens of 16 heads: 5
-//     segments 246 us, 3 263, 4 257).
-// Cut sequences cost a pass over their k and v for the segments' states.
+// widest).  Sequences are cut into segments of as many tokens as let their
+// number, T / seg and half a segment for each sequence's end, fill the card
+// once; cut sequences cost a pass over their k and v for the segments' states,
+// so more of them only cost (65536 tokens of 16 heads: 32 segments 388 us, 48
+// 418, 64 440).  Where the sequences alone fill it, only those of more than
+// twice a workgroup's share of the tokens are cut, which would end alone (32
+// ragged prompts of 128 heads, longest 8192: 629 us, cut at half of that 789).
+// A segment shorter than the mean sequence is made to divide it.
 Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backward) {
-    constexpr int64_t kLeast = 256, kSetup = 128;
+    constexpr int64_t kLeast = 256;
     const int nops = backward ? 3 : 1, kd = backward ? std::max(K, V) : K, vd = backward ? kd : V;
     Shape h;
     h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
@@ -703,21 +701,13 @@ Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backwa
     h.tiles = tiles(vd);
     // workgroups of a token: o has V channels, or dq and dk K and dv V
     const int64_t walks = (int64_t)(H / h.heads) * (tiles(V) + (backward ? 2 * tiles(K) : 0));
-    int64_t seg;
-    if (batch * walks >= kAtOnce) {
-        seg = 2 * T * walks / kAtOnce;
-    } else {
-        const int64_t mean = (T + batch - 1) / batch;
-        int64_t best = 0, least = 0;
-        for (int64_t n = 1; n == 1 || mean / n >= kLeast; ++n) {
-            const int64_t rounds = (batch * walks * n + kAtOnce - 1) / kAtOnce;
-            const int64_t time = rounds * ((mean + n - 1) / n + kSetup);
-            if (best == 0 || time < least) best = n, least = time;
-            if (rounds > 4) break;  // more, shorter segments only add their setup
-        }
-        seg = (mean + best - 1) / best;
-        // nothing to gain from cutting: leave sequences longer than the mean whole too, within reason
-        if (best == 1) seg = 2 * seg;
+    const int64_t mean = (T + batch - 1) / batch, room = kAtOnce - batch * walks / 2;
+    int64_t seg = 2 * T * walks / kAtOnce;
+    if (room > 0) seg = std::min(seg, T * walks / room);
+    seg = std::max(seg, kLeast);
+    if (seg < mean) {
+        const int64_t n = (mean + seg / 2) / seg;
+        seg = (mean + n - 1) / n;
     }
     seg = std::max((seg + kTok - 1) / kTok * kTok, kLeast);
     h.seg = T > seg ? (int)seg : 0;
