@@ -1,14 +1,15 @@
 // Pool states in 8 bits: rows of N elements quantised with one scale each,
-// and read back.  A row lies across the lanes that hold 8 elements of it
-// each; a thread takes kRows rows so that enough loads are in flight.  Both
-// directions are bound by HBM: 4 (or 2) + 1 bytes an element.
+// and read back.  A row lies across the lanes that hold 16 bytes of its state
+// each (4 elements in fp32, 8 in bf16), so every state access of a wavefront is
+// one run of memory; a thread takes kRows rows so that enough of them are in
+// flight.  Both directions are bound by HBM: 4 (or 2) + 1 bytes an element.
 #include "ssd_common.hpp"
 #include "ssd_linear_attn.hpp"
 
 namespace ssd {
 namespace {
 constexpr int kThreads = 256;
-constexpr int kRows = 4;
+constexpr int kRows = 8;
 
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
@@ -49,28 +50,47 @@ struct Span {
     }
 };
 
+// E consecutive elements of a state (16 bytes) as floats, and back
+template <bool SB, int E>
+__device__ __forceinline__ void load_elements(const void *base, int64_t idx, float (&f)[E]) {
+    if constexpr (SB) {
+        load_state8<true>(base, idx, f);
+    } else {
+        const f32x4 v = load_state4<false>(base, idx);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = v[e];
+    }
+}
+template <bool SB, int E>
+__device__ __forceinline__ void store_elements(void *base, int64_t idx, const float (&f)[E]) {
+    if constexpr (SB)
+        store_state8<true>(base, idx, f);
+    else
+        store_state4<false>(base, idx, f32x4{f[0], f[1], f[2], f[3]});
+}
+
 template <int LANES, bool SB, bool E4M3>
 __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const void *pool, uint8_t *codes,
                                                            float *scales, int blocks_per_pair) {
-    constexpr int RP = kThreads / LANES;
+    constexpr int RP = kThreads / LANES, E = SB ? 8 : 4;
     const Span<LANES> w(p, blocks_per_pair);
     if (!w.live) return;
-    const int c = (threadIdx.x % LANES) * 8;
+    const int c = (threadIdx.x % LANES) * E;
     const bool in = c < p.N;
-    float x[kRows][8];
+    float x[kRows][E];
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[n][e] = 0.f;
+        for (int e = 0; e < E; ++e) x[n][e] = 0.f;
         const int64_t row = w.first + n * RP;
-        if (in && row < p.rows_per_slot) load_state8<SB>(pool, (w.pool_row + row) * p.N + c, x[n]);
+        if (in && row < p.rows_per_slot) load_elements<SB, E>(pool, (w.pool_row + row) * p.N + c, x[n]);
     }
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
         const int64_t row = w.first + n * RP;
         uint32_t top = 0;  // magnitudes order as their bits, infinities and NaN last
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
             const uint32_t m = __float_as_uint(x[n][e]) & 0x7FFFFFFFu;
             top = top > m ? top : m;
         }
@@ -78,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const 
         if (row >= p.rows_per_slot) continue;
         const bool finite = top < 0x7F800000u;
         float s;
-        uint32_t lo = 0, hi = 0;
+        uint32_t q[E / 4] = {};
         if constexpr (E4M3) {
             // top = m 2^e: 448 = 1.75 2^8 holds m <= 1.75 with 2^(e-8)
             int k = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -86,10 +106,11 @@ __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const 
             s = top == 0 ? 0.f : __uint_as_float((uint32_t)k << 23);
             if (top != 0 && finite) {
                 const float inv = __uint_as_float((uint32_t)(254 - k) << 23);  // exact
-                lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[n][0] * inv, x[n][1] * inv, 0, false);
-                lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[n][2] * inv, x[n][3] * inv, lo, true);
-                hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[n][4] * inv, x[n][5] * inv, 0, false);
-                hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[n][6] * inv, x[n][7] * inv, hi, true);
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) {
+                    q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[n][4 * i] * inv, x[n][4 * i + 1] * inv, 0, false);
+                    q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[n][4 * i + 2] * inv, x[n][4 * i + 3] * inv, q[i], true);
+                }
             }
         } else {
             s = __uint_as_float(top) / 127.f;
@@ -97,15 +118,17 @@ __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const 
             if (s > 0.f && finite) {
                 const float inv = 1.f / s;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    lo |= (uint32_t)(nearest_code(x[n][e], s, inv) & 0xFF) << (8 * e);
-                    hi |= (uint32_t)(nearest_code(x[n][4 + e], s, inv) & 0xFF) << (8 * e);
-                }
+                for (int e = 0; e < E; ++e) q[e / 4] |= (uint32_t)(nearest_code(x[n][e], s, inv) & 0xFF) << (e % 4 * 8);
             }
         }
         if (!finite) s = __uint_as_float(0x7FC00000u);
         const int64_t at = w.entry_row + row;
-        if (in) *reinterpret_cast<u32x2 *>(codes + at * p.N + c) = u32x2{lo, hi};
+        if (in) {
+            if constexpr (SB)
+                *reinterpret_cast<u32x2 *>(codes + at * p.N + c) = u32x2{q[0], q[1]};
+            else
+                *reinterpret_cast<uint32_t *>(codes + at * p.N + c) = q[0];
+        }
         if (c == 0) scales[at] = s;
     }
 }
@@ -113,26 +136,28 @@ __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const 
 template <int LANES, bool SB, bool E4M3>
 __global__ __launch_bounds__(kThreads) void state_dequantize(CacheParams p, void *pool, const uint8_t *codes,
                                                              const float *scales, int blocks_per_pair) {
-    constexpr int RP = kThreads / LANES;
+    constexpr int RP = kThreads / LANES, E = SB ? 8 : 4;
     const Span<LANES> w(p, blocks_per_pair);
-    const int c = (threadIdx.x % LANES) * 8;
+    const int c = (threadIdx.x % LANES) * E;
     if (!w.live || c >= p.N) return;
-    u32x2 q[kRows];
+    uint32_t q[kRows][E / 4];
     float s[kRows];
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
         const int64_t row = w.first + n * RP;
         if (row >= p.rows_per_slot) continue;
-        q[n] = *reinterpret_cast<const u32x2 *>(codes + (w.entry_row + row) * p.N + c);
+        const uint32_t *at = reinterpret_cast<const uint32_t *>(codes + (w.entry_row + row) * p.N + c);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) q[n][i] = at[i];
         s[n] = scales[w.entry_row + row];
     }
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
         const int64_t row = w.first + n * RP;
         if (row >= p.rows_per_slot) continue;
-        float x[8];
+        float x[E];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < E / 4; ++i) {
             const uint32_t v = q[n][i];
             if constexpr (E4M3) {
                 const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(v, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(v, true);
@@ -145,13 +170,14 @@ __global__ __launch_bounds__(kThreads) void state_dequantize(CacheParams p, void
                 for (int e = 0; e < 4; ++e) x[4 * i + e] = (float)(int8_t)(v >> (8 * e)) * s[n];
             }
         }
-        store_state8<SB>(pool, (w.pool_row + row) * p.N + c, x);
+        store_elements<SB, E>(pool, (w.pool_row + row) * p.N + c, x);
     }
 }
 
 template <typename F>
 hipError_t by_lanes(const CacheParams &p, bool bf16, bool e4m3, F f) {
-    const int lanes = p.N <= 64 ? 8 : p.N <= 128 ? 16 : 32;
+    const int need = p.N / (bf16 ? 8 : 4);
+    const int lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
     const int64_t rows = kThreads / lanes * kRows;
     const int64_t bpp = (p.rows_per_slot + rows - 1) / rows;
     const dim3 grid((unsigned)(bpp * p.count));
@@ -169,8 +195,10 @@ hipError_t by_lanes(const CacheParams &p, bool bf16, bool e4m3, F f) {
         pick(std::integral_constant<int, 8>{});
     else if (lanes == 16)
         pick(std::integral_constant<int, 16>{});
-    else
+    else if (lanes == 32)
         pick(std::integral_constant<int, 32>{});
+    else
+        pick(std::integral_constant<int, 64>{});
     return hipGetLastError();
 }
 }  // namespace
