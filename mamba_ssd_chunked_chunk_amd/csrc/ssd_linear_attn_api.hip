@@ -136,8 +136,8 @@ ssd_status check_cache(const ssd_state_cache_problem *p, const void *codes, cons
     if (p->state_dtype != SSD_STATE_F32 && p->state_dtype != SSD_STATE_BF16) return SSD_ERR_UNSUPPORTED;
     if (p->code_format != SSD_CODE_I8 && p->code_format != SSD_CODE_E4M3) return SSD_ERR_UNSUPPORTED;
     if (p->dstate > SSD_MAX_DSTATE || p->dstate % 8 != 0) return SSD_ERR_UNSUPPORTED;
-    // a block holds at least 32 rows, and the grid has fewer than 2^31 blocks
-    if (((int64_t)p->nheads * p->head_dim + 31) / 32 > INT32_MAX / (p->count > 0 ? p->count : 1))
+    // a block holds at least 16 rows, and the grid has fewer than 2^31 blocks
+    if (((int64_t)p->nheads * p->head_dim + 15) / 16 > INT32_MAX / (p->count > 0 ? p->count : 1))
         return SSD_ERR_UNSUPPORTED;
     if (p->count > 0 && (codes == nullptr || scales == nullptr || pool == nullptr || pool_idx == nullptr ||
                          entry_idx == nullptr))

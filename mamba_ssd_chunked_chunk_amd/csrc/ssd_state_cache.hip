@@ -1,7 +1,7 @@
 // Pool states in 8 bits: rows of N elements quantised with one scale each,
 // and read back.  A row lies across the lanes that hold 16 bytes of its state
 // each (4 elements in fp32, 8 in bf16), so every state access of a wavefront is
-// one run of memory; a thread takes kRows rows so that enough of them are in
+// one run of memory; a thread takes several rows so that enough of them are in
 // flight.  Both directions are bound by HBM: 4 (or 2) + 1 bytes an element.
 #include "ssd_common.hpp"
 #include "ssd_linear_attn.hpp"
@@ -9,7 +9,7 @@
 namespace ssd {
 namespace {
 constexpr int kThreads = 256;
-constexpr int kRows = 8;
+constexpr int kRowsIn = 4, kRowsOut = 8;  // of a thread, quantising and reading back
 
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
@@ -34,8 +34,17 @@ __device__ __forceinline__ int nearest_code(float x, float s, float inv) {
     return (int)c;
 }
 
-// Where block `blk` works: the pair it moves (or none) and its first row.
-template <int LANES>
+// top / 127, correctly rounded: by Markstein's theorem one step from a product
+// with the rounded reciprocal gives it, away from the subnormal range.
+__device__ __forceinline__ float code_scale(float top) {
+    constexpr float inv = 1.f / 127.f;
+    if (top < 0x1p-100f) return top / 127.f;
+    const float q = top * inv;
+    return __builtin_fmaf(__builtin_fmaf(-127.f, q, top), inv, q);
+}
+
+// Where a block works: the pair it moves (or none) and its first row.
+template <int LANES, int ROWS>
 struct Span {
     int64_t pool_row, entry_row;  // of the pair's first row
     int64_t first;
@@ -46,7 +55,7 @@ struct Span {
         live = a < p.max_slots && b < p.max_entries;
         pool_row = (int64_t)a * p.rows_per_slot;
         entry_row = (int64_t)b * p.rows_per_slot;
-        first = (blockIdx.x - i * blocks_per_pair) * (kThreads / LANES * kRows) + threadIdx.x / LANES;
+        first = (blockIdx.x - i * blocks_per_pair) * (kThreads / LANES * ROWS) + threadIdx.x / LANES;
     }
 };
 
@@ -73,20 +82,20 @@ template <int LANES, bool SB, bool E4M3>
 __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const void *pool, uint8_t *codes,
                                                            float *scales, int blocks_per_pair) {
     constexpr int RP = kThreads / LANES, E = SB ? 8 : 4;
-    const Span<LANES> w(p, blocks_per_pair);
+    const Span<LANES, kRowsIn> w(p, blocks_per_pair);
     if (!w.live) return;
     const int c = (threadIdx.x % LANES) * E;
     const bool in = c < p.N;
-    float x[kRows][E];
+    float x[kRowsIn][E];
 #pragma unroll
-    for (int n = 0; n < kRows; ++n) {
+    for (int n = 0; n < kRowsIn; ++n) {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[n][e] = 0.f;
         const int64_t row = w.first + n * RP;
         if (in && row < p.rows_per_slot) load_elements<SB, E>(pool, (w.pool_row + row) * p.N + c, x[n]);
     }
 #pragma unroll
-    for (int n = 0; n < kRows; ++n) {
+    for (int n = 0; n < kRowsIn; ++n) {
         const int64_t row = w.first + n * RP;
         uint32_t top = 0;  // magnitudes order as their bits, infinities and NaN last
 #pragma unroll
@@ -113,12 +122,27 @@ __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const 
                 }
             }
         } else {
-            s = __uint_as_float(top) / 127.f;
+            s = code_scale(__uint_as_float(top));
             if (s < 1.17549435e-38f) s = 0.f;
             if (s > 0.f && finite) {
-                const float inv = 1.f / s;
+                // adding 1.5 2^23 rounds to a whole number, whose low byte is the code
+                const float inv = __builtin_amdgcn_rcpf(s);
+                float far = 0.f;  // the largest remainder
+                uint32_t y[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) q[e / 4] |= (uint32_t)(nearest_code(x[n][e], s, inv) & 0xFF) << (e % 4 * 8);
+                for (int e = 0; e < E; ++e) {
+                    const float m = __builtin_fmaf(x[n][e], inv, 0x1.8p23f);
+                    y[e] = __float_as_uint(m);
+                    far = fmaxf(far, fabsf(__builtin_fmaf(0x1.8p23f - m, s, x[n][e])));
+                }
+                if (2.f * far >= s) {  // a quotient at (or misjudged by the reciprocal near) a half: seldom
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = (uint32_t)nearest_code(x[n][e], s, inv);
+                }
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i)
+                    q[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(y[4 * i + 3], y[4 * i + 2], 0x0C0C0400),
+                                                 __builtin_amdgcn_perm(y[4 * i + 1], y[4 * i], 0x0C0C0400), 0x05040100);
             }
         }
         if (!finite) s = __uint_as_float(0x7FC00000u);
@@ -137,13 +161,13 @@ template <int LANES, bool SB, bool E4M3>
 __global__ __launch_bounds__(kThreads) void state_dequantize(CacheParams p, void *pool, const uint8_t *codes,
                                                              const float *scales, int blocks_per_pair) {
     constexpr int RP = kThreads / LANES, E = SB ? 8 : 4;
-    const Span<LANES> w(p, blocks_per_pair);
+    const Span<LANES, kRowsOut> w(p, blocks_per_pair);
     const int c = (threadIdx.x % LANES) * E;
     if (!w.live || c >= p.N) return;
-    uint32_t q[kRows][E / 4];
-    float s[kRows];
+    uint32_t q[kRowsOut][E / 4];
+    float s[kRowsOut];
 #pragma unroll
-    for (int n = 0; n < kRows; ++n) {
+    for (int n = 0; n < kRowsOut; ++n) {
         const int64_t row = w.first + n * RP;
         if (row >= p.rows_per_slot) continue;
         const uint32_t *at = reinterpret_cast<const uint32_t *>(codes + (w.entry_row + row) * p.N + c);
@@ -152,7 +176,7 @@ __global__ __launch_bounds__(kThreads) void state_dequantize(CacheParams p, void
         s[n] = scales[w.entry_row + row];
     }
 #pragma unroll
-    for (int n = 0; n < kRows; ++n) {
+    for (int n = 0; n < kRowsOut; ++n) {
         const int64_t row = w.first + n * RP;
         if (row >= p.rows_per_slot) continue;
         float x[E];
@@ -175,10 +199,10 @@ __global__ __launch_bounds__(kThreads) void state_dequantize(CacheParams p, void
 }
 
 template <typename F>
-hipError_t by_lanes(const CacheParams &p, bool bf16, bool e4m3, F f) {
+hipError_t by_lanes(const CacheParams &p, int thread_rows, bool bf16, bool e4m3, F f) {
     const int need = p.N / (bf16 ? 8 : 4);
     const int lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
-    const int64_t rows = kThreads / lanes * kRows;
+    const int64_t rows = kThreads / lanes * thread_rows;
     const int64_t bpp = (p.rows_per_slot + rows - 1) / rows;
     const dim3 grid((unsigned)(bpp * p.count));
     auto pick = [&](auto l) {
@@ -205,14 +229,14 @@ hipError_t by_lanes(const CacheParams &p, bool bf16, bool e4m3, F f) {
 
 hipError_t launch_state_quantize(const CacheParams &c, const void *pool, bool bf16, bool e4m3, void *codes,
                                  float *scales, hipStream_t s) {
-    return by_lanes(c, bf16, e4m3, [&](auto l, auto sb, auto e4, dim3 grid, int bpp) {
+    return by_lanes(c, kRowsIn, bf16, e4m3, [&](auto l, auto sb, auto e4, dim3 grid, int bpp) {
         state_quantize<decltype(l)::value, decltype(sb)::value, decltype(e4)::value>
             <<<grid, kThreads, 0, s>>>(c, pool, static_cast<uint8_t *>(codes), scales, bpp);
     });
 }
 hipError_t launch_state_dequantize(const CacheParams &c, void *pool, bool bf16, bool e4m3, const void *codes,
                                    const float *scales, hipStream_t s) {
-    return by_lanes(c, bf16, e4m3, [&](auto l, auto sb, auto e4, dim3 grid, int bpp) {
+    return by_lanes(c, kRowsOut, bf16, e4m3, [&](auto l, auto sb, auto e4, dim3 grid, int bpp) {
         state_dequantize<decltype(l)::value, decltype(sb)::value, decltype(e4)::value>
             <<<grid, kThreads, 0, s>>>(c, pool, static_cast<const uint8_t *>(codes), scales, bpp);
     });
