@@ -11,10 +11,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsIn = 4, kRowsOut = 8;  // of a thread, quantising and reading back
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+    return v > o ? v : o;
+}
+// largest over each aligned group of LANES lanes; every lane receives it
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    v = dpp_max<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_max<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_max<0x141>(v);  // row_half_mirror: groups of 8
+    if constexpr (LANES >= 16) v = dpp_max<0x140>(v);  // row_mirror: rows of 16
 #pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) {
+    for (int d = 16; d < LANES; d <<= 1) {
         const uint32_t o = (uint32_t)__shfl_xor((int)v, d, 64);
         v = v > o ? v : o;
     }
