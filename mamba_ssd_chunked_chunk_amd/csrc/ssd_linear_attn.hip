@@ -130,8 +130,8 @@ __device__ __forceinline__ bool resumes(const Params &p, const Op &op, int b) {
 }
 
 // The segment a workgroup takes.  Sequences are cut into segments of `seg`
-// tokens counted in walking order; slot w of the launch is segment w - first
-// of the last sequence whose first slot, qsl / seg + b, is at most w.  (A
+// tokens (0: not cut) counted in walking order; slot w of the launch is segment
+// w - first of the last sequence whose first slot, qsl / seg + b, is at most w.  (A
 // sequence of n tokens has at most n / seg + 1 segments, so their slots never
 // meet the next sequence's; slots in between are empty.)  Every lane tests one
 // sequence at a time, so 64-ary search finds it in one or two steps.
@@ -139,11 +139,11 @@ struct Segment {
     int b, index, count;  // sequence, segment of it, its number of segments (0: an empty slot)
     int begin, len;       // the sequence's first token and length
 };
-__device__ __forceinline__ Segment find_segment(const Params &p, int w) {
+__device__ __forceinline__ Segment find_segment(const Params &p, int w, int seg) {
     const int lane = threadIdx.x & 63;
     Segment g;
     int lo = 0, first = 0;
-    if (p.seg == 0) {  // one segment per sequence
+    if (seg == 0) {  // one segment per sequence
         lo = w;
         first = w;
     } else {
@@ -152,7 +152,7 @@ __device__ __forceinline__ Segment find_segment(const Params &p, int w) {
             const int step = (n + 63) / 64;
             const int i = lane * step;
             bool at = false;
-            if (i < n) at = clamp_row(p, p.qsl[lo + i]) / p.seg + lo + i <= w;
+            if (i < n) at = clamp_row(p, p.qsl[lo + i]) / seg + lo + i <= w;
             const int k = __popcll(__ballot(at)) - 1;
             if (k < 0) return Segment{0, 0, 0, 0, 0};
             lo += k * step;
@@ -163,12 +163,12 @@ __device__ __forceinline__ Segment find_segment(const Params &p, int w) {
     g.b = __builtin_amdgcn_readfirstlane(lo);
     g.begin = __builtin_amdgcn_readfirstlane(clamp_row(p, p.qsl[g.b]));
     g.len = max(__builtin_amdgcn_readfirstlane(clamp_row(p, p.qsl[g.b + 1])) - g.begin, 0);
-    if (p.seg == 0) {
+    if (seg == 0) {
         g.index = 0;
         g.count = 1;
     } else {
-        g.index = w - (g.begin / p.seg + g.b);
-        g.count = max((g.len + p.seg - 1) / p.seg, 1);
+        g.index = w - (g.begin / seg + g.b);
+        g.count = max((g.len + seg - 1) / seg, 1);
         if (g.index >= g.count) g.count = 0;
     }
     return g;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     const int together = p.share / HP * p.tiles * p.nops;
     const int run = (int)blockIdx.x / 8;
     int id = (run / together * 8 + (int)(blockIdx.x % 8)) * together + run % together;
-    if (id >= p.slots * (p.H / HP) * p.tiles * p.nops) return;
+    if (id >= (LOCAL ? p.sub_slots : p.slots) * (p.H / HP) * p.tiles * p.nops) return;
     const int which = id % p.nops;
     id /= p.nops;
     const int v0 = (id % p.tiles) * VT;
@@ -228,13 +228,16 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     const int hw = wave / WH, h = h0 + hw;  // the wavefront's head
 
     if (LOCAL && op.twin != 0) return;  // la_chain makes its states from the twin's
-    const Segment g = find_segment(p, w);
-    if (g.count == 0 || (LOCAL && g.index == g.count - 1)) return;
+    const int seg = LOCAL ? p.sub : p.seg;
+    const Segment g = find_segment(p, w, seg);
+    if (g.count == 0) return;
+    // nothing follows the last segment
+    if (LOCAL && g.index * p.sub >= (g.len - 1) / p.seg * p.seg) return;
     const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[g.b] : (int64_t)g.b;
     if (slot >= p.max_slots) return;  // padding
     // the segment's tokens: n of them, from t0 upwards
-    const int skip = p.seg == 0 ? 0 : g.index * p.seg;
-    const int n = p.seg == 0 ? g.len : min(p.seg, g.len - skip);
+    const int skip = g.index * seg;
+    const int n = seg == 0 ? g.len : min(seg, g.len - skip);
     const int64_t t0 = rev ? g.begin + g.len - skip - n : g.begin + skip;
     const float l2 = log2_decay(p, h);
     const float shift = rev ? 1.f : 0.f;
@@ -244,9 +247,10 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     const int tile0 = wave % WH * DT;  // the wavefront's first tile of the head's value channels
     auto vch = [&](int d) { return v0 + 32 * ((tile0 + d) >> 1) + column(l16, (tile0 + d) & 1); };
     const int64_t state_at = (slot * p.H + h) * p.state_size;
-    // the wavefront's part of the segment's slot in the workspace
+    // the wavefront's part of the slot of the segment's (first) states in the workspace
+    const int64_t part_slot = LOCAL ? w : g.count > 1 ? g.begin / p.sub + g.b + (int64_t)g.index * (p.seg / p.sub) : 0;
     f32x4 *const part = reinterpret_cast<f32x4 *>(
-        p.parts + ((((int64_t)which * p.slots + w) * p.H + h) * p.tiles * VT + v0 + 16 * tile0) * KD) + lane;
+        p.parts + ((((int64_t)which * p.sub_slots + part_slot) * p.H + h) * p.tiles * VT + v0 + 16 * tile0) * KD) + lane;
     f32x4 S[NT][2][DT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -571,62 +575,71 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     }
 }
 
-// The segments' own states into the states that enter them, in place: one
-// thread per 4 state elements of a (sequence, head), in the order of the
-// walk's registers.  Sequences of one segment are left to the walk.  With
+// The states of the segments' parts (of `sub` tokens) into the states that
+// enter the segments, in place of their first parts': a thread takes 4 state elements of a (sequence, head) at a time, in the order of
+// the walk's registers.  Sequences of one segment are left to the walk.  With
 // `mirror` the states are those of another operation too, transposed (its k
 // channels are this one's v channels and the reverse), and are written there
 // as well.
 template <bool SB>
 __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
+    constexpr int kAhead = 8;
     const int per_head = p.tiles * VT * KD / 4;  // groups of 4
-    const int blocks = (per_head + 255) / 256;
-    int id = blockIdx.x;
-    const int i = (id % blocks) * 256 + (int)threadIdx.x;
-    id /= blocks;
-    const int h = id % p.H, b = id / p.H;
+    const int h = blockIdx.x % p.H, b = blockIdx.x / p.H;
     const int which = blockIdx.y;
     const Op &op = p.op[which];
-    if (i >= per_head || op.twin != 0) return;
+    if (op.twin != 0) return;
     const int begin = clamp_row(p, p.qsl[b]), len = max(clamp_row(p, p.qsl[b + 1]) - begin, 0);
-    const int count = (len + p.seg - 1) / p.seg;
+    const int count = (len + p.seg - 1) / p.seg, parts = p.seg / p.sub;  // segments, and parts of one
+    const int last = (count - 1) * parts;
     const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[b] : (int64_t)b;
     if (count <= 1 || slot >= p.max_slots) return;
-    const int lane = i & 63, y = (i >> 6) & 1, t = (i >> 7) % (KD / 32), tile = (i >> 7) / (KD / 32);
-    const int vch = 32 * (tile >> 1) + column(lane & 15, tile & 1);
-    const int kc = 32 * t + 8 * (lane >> 4) + 4 * y;
-    const bool in = vch < op.vd && kc < op.kd;
-    f32x4 S = {0.f, 0.f, 0.f, 0.f};
-    if (in && resumes(p, op, b)) {
-        const int64_t at = (slot * p.H + h) * p.state_size + (int64_t)vch * op.sv + kc * op.sk;
-        if (op.sk == 1) {
-            S = load_state4<SB>(op.state_in, at);
-        } else {
+    for (int i = blockIdx.z * 256 + (int)threadIdx.x; i < per_head; i += gridDim.z * 256) {
+        const int lane = i & 63, y = (i >> 6) & 1, t = (i >> 7) % (KD / 32), tile = (i >> 7) / (KD / 32);
+        const int vch = 32 * (tile >> 1) + column(lane & 15, tile & 1);
+        const int kc = 32 * t + 8 * (lane >> 4) + 4 * y;
+        const bool in = vch < op.vd && kc < op.kd;
+        f32x4 S = {0.f, 0.f, 0.f, 0.f};
+        if (in && resumes(p, op, b)) {
+            const int64_t at = (slot * p.H + h) * p.state_size + (int64_t)vch * op.sv + kc * op.sk;
+            if (op.sk == 1) {
+                S = load_state4<SB>(op.state_in, at);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                S[e] = SB ? bf16_bits_to_float(static_cast<const uint16_t *>(op.state_in)[at + e * op.sk])
-                          : static_cast<const float *>(op.state_in)[at + e * op.sk];
+                for (int e = 0; e < 4; ++e)
+                    S[e] = SB ? bf16_bits_to_float(static_cast<const uint16_t *>(op.state_in)[at + e * op.sk])
+                              : static_cast<const float *>(op.state_in)[at + e * op.sk];
+            }
         }
-    }
-    const float keep = fast_exp2(log2_decay(p, h) * (float)p.seg);
-    const int64_t step = (int64_t)p.H * per_head;
-    const int64_t head = (int64_t)(begin / p.seg + b) * step + (int64_t)h * per_head;
-    f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) + (int64_t)which * p.slots * step + head + i;
-    // (v channel kc, k channel vch) of the mirror: element vch % 4 of the group of its
-    // lane (a backward launch holds as many v channels as k channels)
-    const bool mirrored = op.mirror != 0;
-    const int mtile = kc / 32 * 2 + (kc >> 2) % 2, mt = vch / 32, my = (vch >> 2) % 2;
-    const int mlane = vch % 32 / 8 * 16 + kc % 32 / 8 * 4;
-    float *twin = p.parts + 4 * ((int64_t)op.mirror * p.slots * step + head +
-                                 ((mtile * (KD / 32) + mt) * 2 + my) * 64 + mlane) + vch % 4;
-    for (int s = 0; s < count; ++s, part += step, twin += 4 * step) {
-        const f32x4 own = s < count - 1 ? *part : f32x4{0.f, 0.f, 0.f, 0.f};
-        *part = S;
-        if (mirrored) {
+        const float keep = fast_exp2(log2_decay(p, h) * (float)p.sub);
+        const int64_t step = (int64_t)p.H * per_head;
+        const int64_t head = (int64_t)(begin / p.sub + b) * step + (int64_t)h * per_head;
+        f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) + (int64_t)which * p.sub_slots * step + head + i;
+        // (v channel kc, k channel vch) of the mirror: element vch % 4 of the group of its
+        // lane (a backward launch holds as many v channels as k channels)
+        const bool mirrored = op.mirror != 0;
+        const int mtile = kc / 32 * 2 + (kc >> 2) % 2, mt = vch / 32, my = (vch >> 2) % 2;
+        const int mlane = vch % 32 / 8 * 16 + kc % 32 / 8 * 4;
+        float *twin = p.parts + 4 * ((int64_t)op.mirror * p.sub_slots * step + head +
+                                     ((mtile * (KD / 32) + mt) * 2 + my) * 64 + mlane) + vch % 4;
+        for (int s = 0; s <= last; s += kAhead) {
+            f32x4 own[kAhead];  // loaded ahead of the chain
 #pragma unroll
-            for (int e = 0; e < 4; ++e) twin[4 * e] = S[e];
+            for (int a = 0; a < kAhead; ++a) own[a] = s + a < last ? part[a * step] : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                if (s + a <= last && (s + a) % parts == 0) {
+                    part[a * step] = S;
+                    if (mirrored) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) twin[4 * (a * step + e)] = S[e];
+                    }
+                }
+                S = S * keep + own[a];
+            }
+            part += kAhead * step;
+            twin += 4 * kAhead * step;
         }
-        S = S * keep + own;
     }
 }
 
@@ -652,16 +665,18 @@ __global__ __launch_bounds__(256) void la_group_sum(GroupSum a, const int32_t *q
 template <int KD, int NW, int DT, int HP, bool SB>
 hipError_t launch_variant(const Params &p, hipStream_t s) {
     constexpr int VT = 16 * DT * NW / HP;
-    const int64_t n = (int64_t)p.slots * (p.H / HP) * p.tiles * p.nops;
-    const int64_t run = (int64_t)8 * (p.share / HP) * p.tiles * p.nops;
-    const dim3 grid((unsigned)((n + run - 1) / run * run)), block(64 * NW);
+    const int64_t each = (int64_t)(p.H / HP) * p.tiles * p.nops, run = (int64_t)8 * (p.share / HP) * p.tiles * p.nops;
+    auto grid = [&](int slots) { return dim3((unsigned)((slots * each + run - 1) / run * run)); };
+    const dim3 block(64 * NW);
     if (p.seg != 0) {
-        la_walk<KD, NW, DT, HP, SB, true><<<grid, block, 0, s>>>(p);
-        const int blocks = (p.tiles * VT * KD / 4 + 255) / 256;
-        const dim3 cg((unsigned)(p.batch * p.H * blocks), (unsigned)p.nops);
+        la_walk<KD, NW, DT, HP, SB, true><<<grid(p.sub_slots), block, 0, s>>>(p);
+        // blocks for the card, or one for each head
+        const int64_t heads = (int64_t)p.batch * p.H;
+        const int most = p.tiles * VT * KD / 1024, split = (int)std::min<int64_t>(most, (2048 + heads - 1) / heads);
+        const dim3 cg((unsigned)heads, (unsigned)p.nops, (unsigned)split);
         la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, VT);
     }
-    la_walk<KD, NW, DT, HP, SB, false><<<grid, block, 0, s>>>(p);
+    la_walk<KD, NW, DT, HP, SB, false><<<grid(p.slots), block, 0, s>>>(p);
     return hipGetLastError();
 }
 template <int KD, bool SB>
@@ -710,9 +725,19 @@ Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backwa
         seg = (mean + n - 1) / n;
     }
     seg = std::max((seg + kTok - 1) / kTok * kTok, kLeast);
-    h.seg = T > seg ? (int)seg : 0;
-    h.slots = h.seg != 0 ? (int)(T / seg) + batch : batch;
-    h.bytes = h.seg != 0 ? (size_t)nops * h.slots * H * h.tiles * h.vt * h.kd * sizeof(float) : 0;
+    // parts: the pass for the states has no output to wait for and walks fewer
+    // segments (none of them the last), so it may be cut finer
+    const int64_t local = (int64_t)(H / h.heads) * (tiles(V) + (backward ? tiles(K) : 0)) *
+                          std::max<int64_t>(T / seg - batch / 2, 1);
+    const int64_t parts = std::max<int64_t>(1, std::min((kAtOnce + local - 1) / local, seg / kLeast));
+    const int64_t sub = (seg + parts * kTok - 1) / (parts * kTok) * kTok;
+    seg = sub * parts;
+    const bool cut = T > seg;
+    h.seg = cut ? (int)seg : 0;
+    h.sub = cut ? (int)sub : 0;
+    h.slots = cut ? (int)(T / seg) + batch : batch;
+    h.sub_slots = cut ? (int)(T / sub) + batch : 0;
+    h.bytes = (size_t)nops * h.sub_slots * H * h.tiles * h.vt * h.kd * sizeof(float);
     return h;
 }
 
@@ -720,7 +745,9 @@ hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s) {
     p.nops = nops;
     p.tiles = h.tiles;
     p.seg = h.seg;
+    p.sub = h.sub;
     p.slots = h.slots;
+    p.sub_slots = h.sub_slots;
     return p.state_bf16 ? launch_any<true>(p, h, s) : launch_any<false>(p, h, s);
 }
 

@@ -62,14 +62,15 @@ struct Params {
     // the launch (set by launch_walk)
     int nops, tiles;  // tiles: workgroups along the value channels
     int seg, slots;   // tokens of a segment (0: whole sequences) and slots of segments
-    float *parts;     // [nops][slots][H][tiles * VT][KD] states of the segments, in register order
+    int sub, sub_slots;  // the same of the parts of segments (seg is a multiple of sub)
+    float *parts;     // [nops][sub_slots][H][tiles * VT][KD] states of the parts, in register order
 };
 
 // What a launch takes of kd x vd channels (the largest of its operations').
 struct Shape {
     int kd, vt, tiles;  // kd rounded up; value channels of a workgroup, and workgroups along vd
     int heads;          // heads of a workgroup
-    int seg, slots;
+    int seg, slots, sub, sub_slots;
     size_t bytes;       // of `parts`
 };
 Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backward);
