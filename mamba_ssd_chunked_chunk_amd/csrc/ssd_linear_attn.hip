@@ -129,35 +129,58 @@ __device__ __forceinline__ bool resumes(const Params &p, const Op &op, int b) {
     return op.state_in != nullptr && (p.init_all != 0 || (p.has_init != nullptr && p.has_init[b] != 0));
 }
 
-// The segment a workgroup takes.  Sequences are cut into segments of `seg`
-// tokens (0: not cut) counted in walking order; slot w of the launch is segment
-// w - first of the last sequence whose first slot, qsl / seg + b, is at most w.  (A
-// sequence of n tokens has at most n / seg + 1 segments, so their slots never
-// meet the next sequence's; slots in between are empty.)  Every lane tests one
-// sequence at a time, so 64-ary search finds it in one or two steps.
+// The segment a workgroup takes: sequences are cut into segments of `seg`
+// tokens (0: not cut), counted in walking order, and number w of the launch is
+// one of them or none.
 struct Segment {
-    int b, index, count;  // sequence, segment of it, its number of segments (0: an empty slot)
+    int b, index, count;  // sequence, segment of it, its number of segments (0: none)
     int begin, len;       // the sequence's first token and length
 };
 __device__ __forceinline__ Segment find_segment(const Params &p, int w, int seg) {
     const int lane = threadIdx.x & 63;
+    const Segment none = {0, 0, 0, 0, 0};
     Segment g;
-    int lo = 0, first = 0;
-    if (seg == 0) {  // one segment per sequence
+    if (p.batch <= 64) {
+        // Longest sequences first, since what starts last must not be long (32
+        // ragged prompts of 128 heads, 18 to 7975 tokens, the last of 5032: 606 ->
+        // 533 us).  Lane b holds sequence b and counts the segments ahead of its own.
+        int begin = 0, len = -1, count = 0, first = 0;
+        if (lane < p.batch) {
+            begin = clamp_row(p, p.qsl[lane]);
+            len = max(clamp_row(p, p.qsl[lane + 1]) - begin, 0);
+            count = seg == 0 ? 1 : max((len + seg - 1) / seg, 1);
+        }
+        for (int j = 0; j < p.batch; ++j) {
+            const int l = __builtin_amdgcn_readlane(len, j), c = __builtin_amdgcn_readlane(count, j);
+            first += l > len || (l == len && j < lane) ? c : 0;
+        }
+        const uint64_t at = __ballot(first <= w && w < first + count);
+        if (at == 0) return none;
+        g.b = (int)__builtin_ctzll(at);
+        g.begin = __builtin_amdgcn_readlane(begin, g.b);
+        g.len = __builtin_amdgcn_readlane(len, g.b);
+        g.count = __builtin_amdgcn_readlane(count, g.b);
+        g.index = w - __builtin_amdgcn_readlane(first, g.b);
+        return g;
+    }
+    // Many sequences: in their order.  Sequence b's numbers start at qsl / seg +
+    // b (a sequence of n tokens has at most n / seg + 1 segments, so they never
+    // meet the next one's; those in between are nobody's), and every lane tests
+    // one sequence at a time: a 64-ary search.
+    int lo = 0;
+    if (seg == 0) {
         lo = w;
-        first = w;
     } else {
         int n = p.batch;
-        while (true) {
+        while (n > 1) {
             const int step = (n + 63) / 64;
             const int i = lane * step;
             bool at = false;
             if (i < n) at = clamp_row(p, p.qsl[lo + i]) / seg + lo + i <= w;
             const int k = __popcll(__ballot(at)) - 1;
-            if (k < 0) return Segment{0, 0, 0, 0, 0};
+            if (k < 0) return none;
             lo += k * step;
             n = min(step, n - k * step);
-            if (n <= 1) break;
         }
     }
     g.b = __builtin_amdgcn_readfirstlane(lo);
@@ -169,7 +192,7 @@ __device__ __forceinline__ Segment find_segment(const Params &p, int w, int seg)
     } else {
         g.index = w - (g.begin / seg + g.b);
         g.count = max((g.len + seg - 1) / seg, 1);
-        if (g.index >= g.count) g.count = 0;
+        if (g.index < 0 || g.index >= g.count) g.count = 0;
     }
     return g;
 }
@@ -248,7 +271,8 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     auto vch = [&](int d) { return v0 + 32 * ((tile0 + d) >> 1) + column(l16, (tile0 + d) & 1); };
     const int64_t state_at = (slot * p.H + h) * p.state_size;
     // the wavefront's part of the slot of the segment's (first) states in the workspace
-    const int64_t part_slot = LOCAL ? w : g.count > 1 ? g.begin / p.sub + g.b + (int64_t)g.index * (p.seg / p.sub) : 0;
+    const int64_t part_slot =
+        g.count > 1 ? g.begin / p.sub + g.b + (LOCAL ? g.index : (int64_t)g.index * (p.seg / p.sub)) : 0;
     f32x4 *const part = reinterpret_cast<f32x4 *>(
         p.parts + ((((int64_t)which * p.sub_slots + part_slot) * p.H + h) * p.tiles * VT + v0 + 16 * tile0) * KD) + lane;
     f32x4 S[NT][2][DT];
@@ -702,20 +726,24 @@ hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
 // so more of them only cost (65536 tokens of 16 heads: 32 segments 388 us, 48
 // 418, 64 440).  Where the sequences alone fill it, only those of more than
 // twice a workgroup's share of the tokens are cut, which would end alone (32
-// ragged prompts of 128 heads, longest 8192: 629 us, cut at half of that 789).
+// ragged prompts of 128 heads, longest 7975 tokens: 533 us, cut at half of that
+// 575, at a quarter 696).
 // A segment shorter than the mean sequence is made to divide it.
-Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backward) {
+Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, int nops, int nlocal) {
     constexpr int64_t kLeast = 256;
-    const int nops = backward ? 3 : 1, kd = backward ? std::max(K, V) : K, vd = backward ? kd : V;
+    const int vd = *std::max_element(vds, vds + nops);
     Shape h;
     h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
     h.vt = vd <= 64 ? 64 : 128;
     h.heads = h.vt == 64 && share % 2 == 0 && nops == 1 ? 2 : 1;
     const int64_t kAtOnce = h.kd == 256 ? 256 : 512;
-    auto tiles = [&](int d) { return (d + h.vt - 1) / h.vt; };
-    h.tiles = tiles(vd);
-    // workgroups of a token: o has V channels, or dq and dk K and dv V
-    const int64_t walks = (int64_t)(H / h.heads) * (tiles(V) + (backward ? 2 * tiles(K) : 0));
+    auto tiles = [&](int n) {
+        int sum = 0;
+        for (int i = 0; i < n; ++i) sum += (vds[i] + h.vt - 1) / h.vt;
+        return (int64_t)(H / h.heads) * sum;
+    };
+    h.tiles = (vd + h.vt - 1) / h.vt;
+    const int64_t walks = tiles(nops);  // workgroups of a token
     const int64_t mean = (T + batch - 1) / batch, room = kAtOnce - batch * walks / 2;
     int64_t seg = 2 * T * walks / kAtOnce;
     if (room > 0) seg = std::min(seg, T * walks / room);
@@ -727,8 +755,7 @@ Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backwa
     seg = std::max((seg + kTok - 1) / kTok * kTok, kLeast);
     // parts: the pass for the states has no output to wait for and walks fewer
     // segments (none of them the last), so it may be cut finer
-    const int64_t local = (int64_t)(H / h.heads) * (tiles(V) + (backward ? tiles(K) : 0)) *
-                          std::max<int64_t>(T / seg - batch / 2, 1);
+    const int64_t local = tiles(nlocal) * std::max<int64_t>(T / seg - batch / 2, 1);
     const int64_t parts = std::max<int64_t>(1, std::min((kAtOnce + local - 1) / local, seg / kLeast));
     const int64_t sub = (seg + parts * kTok - 1) / (parts * kTok) * kTok;
     seg = sub * parts;

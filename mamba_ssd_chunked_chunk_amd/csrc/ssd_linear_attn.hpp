@@ -73,7 +73,8 @@ struct Shape {
     int seg, slots, sub, sub_slots;
     size_t bytes;       // of `parts`
 };
-Shape shape_of(int64_t T, int batch, int H, int share, int K, int V, bool backward);
+// vds: the value channels of its nops operations, of which the first nlocal have segments' states of their own
+Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, int nops, int nlocal);
 hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s);
 
 // sums the heads of each group, twice: dst[t][g][w] = sum_i src[t][g * div + i][w]
