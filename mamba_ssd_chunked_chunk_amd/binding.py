@@ -393,7 +393,27 @@ def ssd_validate_inputs(prob: ssd_problem, query_start_loc, cache_indices, strea
 
 
 # ---------------------------------------------------------------------------
-# linear attention with a fixed decay per head, and the 8-bit state cache
+# linear attention with a fixed decay per head, and the 8-bit state cache.
+# Decode steps call these once a layer and token, so what they check they check
+# in few operations: _inputs() imports torch once, addresses go to ctypes as
+# they are, and problems are made once for each set of sizes.
+
+torch = None  # imported by the first call
+
+
+def _raw_stream(dev):
+    """Handle of the device's current stream."""
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _import_torch():
+    global torch, _raw_stream
+    import torch as module
+    torch = module
+    handle = getattr(module._C, "_cuda_getCurrentRawStream", None)
+    if handle is not None:  # the same without a Stream object
+        _raw_stream = lambda dev: handle(dev.index)  # noqa: E731
+
 
 def make_linear_attn_problem(total_len, batch, nheads, ngroups, key_dim, value_dim, max_slots=1,
                              state_dtype=STATE_F32, scale=1.0, q_stride=0, k_stride=0,
@@ -437,7 +457,8 @@ def _dense_or_none(t, name, dtype, shape, device):
 def _token_stride(t, name, shape, device):
     """Elements between tokens of a bf16 [T, n, D] tensor whose tokens are dense rows (a slice of a wider
     projection is one); 0 for a dense tensor."""
-    import torch
+    if torch is None:
+        _import_torch()
     if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device:
         _refuse_tensor(t, name, torch.bfloat16, shape, device)
     if t.is_contiguous():
@@ -459,8 +480,9 @@ def _linear_attn_sizes(*sizes):
 
 def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
     """What a linear-attention call goes by, its inputs checked: problem, workspace bytes (forward, backward),
-    device, shape of a state."""
-    import torch
+    device, shape of a state, addresses of q, k, v and log_decay."""
+    if torch is None:
+        _import_torch()
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t is None or t.dim() != 3:
             raise ValueError(f"{name} must be [T, heads, dim]")
@@ -468,18 +490,18 @@ def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
     if dev.type != "cuda":
         raise ValueError("libssd runs on a HIP device; got tensors on " + str(dev))
     T, H, V = v.shape
-    G, K = q.shape[1], q.shape[2]
-    qk = (T, G, K)
-    strides = (_token_stride(q, "q", qk, dev), _token_stride(k, "k", qk, dev), _token_stride(v, "v", (T, H, V), dev))
-    _dense(log_decay, "log_decay", torch.float32, (H,), dev)
-    prob, forward, backward = _linear_attn_sizes(T, batch, H, G, K, V, max_slots, state_dtype,
-                                                 K ** -0.5 if scale is None else float(scale), *strides)
-    return prob, forward, backward, dev, (H, V, K)
+    _, G, K = qk = q.shape
+    if qk[0] != T:
+        _refuse_tensor(q, "q", torch.bfloat16, (T, G, K), dev)
+    prob, forward, backward = _linear_attn_sizes(
+        T, batch, H, G, K, V, max_slots, state_dtype, K ** -0.5 if scale is None else float(scale),
+        _token_stride(q, "q", qk, dev), _token_stride(k, "k", qk, dev), _token_stride(v, "v", (T, H, V), dev))
+    decay = _dense(log_decay, "log_decay", torch.float32, (H,), dev)
+    return prob, forward, backward, dev, (H, V, K), (q.data_ptr(), k.data_ptr(), v.data_ptr(), decay)
 
 
 def _slots(cache_indices, has_initial_state, batch, dev):
     """Addresses of cache_indices and has_initial_state (or None), checked."""
-    import torch
     if cache_indices.dtype not in (torch.int32, torch.uint32):
         raise TypeError("cache_indices must be int32 or uint32")
     idx = _dense(cache_indices, "cache_indices", cache_indices.dtype, (batch,), dev)
@@ -493,40 +515,31 @@ def _slots(cache_indices, has_initial_state, batch, dev):
 def _launch(name, dev, stream, call):
     """Runs ``call(stream)`` on the stream (the current one for None) with the tensors' device current, and raises
     what it returns."""
-    import torch
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     if dev.index == torch.cuda.current_device():
-        status = call((stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
+        status = call(_raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            status = call((stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
+            status = call(_raw_stream(dev) if stream is None else stream.cuda_stream)
     if status != SSD_OK:
         _check(status, name)
 
 
 def _run(name, dev, stream, need, workspace, call):
-    """Runs ``call(workspace address, bytes, stream)`` on the stream (the current one for None) with the tensors'
-    device current, and raises what it returns; a workspace that the caller does not give is allocated on that
-    stream.  Returns the workspace."""
-    import torch
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.numel() < need or
-                                  workspace.device != dev):
-        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        if workspace is None:
+    """The same for ``call(workspace address, bytes, stream)``.  A workspace that the caller does not give is
+    allocated on the call's stream.  Returns the workspace (None where none was given and none is needed)."""
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev:
+            raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+    elif need:
+        if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        status = call(workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        # entering a stream makes its device current too
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-            if workspace is None:
+        else:
+            with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            status = call(workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
-    if status != SSD_OK:
-        _check(status, name)
+    at, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _launch(name, dev, stream, lambda st: call(at, size, st))
     return workspace
 
 
@@ -542,19 +555,19 @@ def ssd_linear_attn_varlen_fwd_inplace(o, q, k, v, log_decay, pool, query_start_
     the last sequence are left alone); has_initial_state uint8/bool [batch] or
     None; cache_indices int32/uint32 [batch], S or more (or negative) for a
     padding entry.  ``scale``: None for K ** -0.5.  Runs on ``stream`` or the
-    current stream; asynchronous.  Returns the workspace tensor.
+    current stream; asynchronous.  Returns the workspace tensor (None where none
+    is needed).
     """
-    import torch
     batch = query_start_loc.numel() - 1
     slots = pool.shape[0]
-    prob, need, _, dev, state = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
+    prob, need, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
     out = _dense(o, "o", torch.bfloat16, v.shape, dev)
     states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
     qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
     idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
     f = load_library().ssd_linear_attn_varlen_fwd_inplace
     return _run("ssd_linear_attn_varlen_fwd_inplace", dev, stream, need, workspace, lambda ws, n, st: f(
-        prob, out, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), states, qsl, flags, idx, ws, n, st))
+        prob, out, *inputs, states, qsl, flags, idx, ws, n, st))
 
 
 def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_states, query_start_loc, *, scale=None,
@@ -563,11 +576,10 @@ def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_stat
     ``initial_states[b]`` ([batch,H,V,K], or None for zero) and leaves
     ``final_states[b]``; both fp32 or both bf16.  Returns the workspace tensor.
     """
-    import torch
     batch = query_start_loc.numel() - 1
     if final_states is None:
         raise ValueError("final_states is required")
-    prob, need, _, dev, state = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
+    prob, need, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
                                              _state_dtype(final_states, "final_states"), scale)
     out = _dense(o, "o", torch.bfloat16, v.shape, dev)
     first = _dense_or_none(initial_states, "initial_states", final_states.dtype, (batch, *state), dev)
@@ -575,7 +587,7 @@ def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_stat
     qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
     f = load_library().ssd_linear_attn_varlen_fwd
     return _run("ssd_linear_attn_varlen_fwd", dev, stream, need, workspace, lambda ws, n, st: f(
-        prob, out, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), first, last, qsl, ws, n, st))
+        prob, out, *inputs, first, last, qsl, ws, n, st))
 
 
 def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_decay, initial_states,
@@ -586,12 +598,11 @@ def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_d
     (zero).  State tensors [batch,H,V,K], all fp32 or all bf16.  Returns the
     workspace tensor.
     """
-    import torch
     batch = query_start_loc.numel() - 1
     states = ((d_initial_states, "d_initial_states"), (initial_states, "initial_states"),
               (d_final_states, "d_final_states"))
     kind = next((t for t in states if t[0] is not None), None)
-    prob, _, need, dev, state = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
+    prob, _, need, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
                                              STATE_F32 if kind is None else _state_dtype(*kind), scale)
     d_first, first, d_last = (None if t is None else _dense(t, n, kind[0].dtype, (batch, *state), dev)
                               for t, n in states)
@@ -602,8 +613,7 @@ def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_d
     qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
     f = load_library().ssd_linear_attn_varlen_bwd
     return _run("ssd_linear_attn_varlen_bwd", dev, stream, need, workspace, lambda ws, n, st: f(
-        prob, *out, d_first, q.data_ptr(), k.data_ptr(), v.data_ptr(), grad, log_decay.data_ptr(), first, d_last, qsl,
-        ws, n, st))
+        prob, *out, d_first, *inputs[:3], grad, inputs[3], first, d_last, qsl, ws, n, st))
 
 
 def ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, has_initial_state, cache_indices, *, scale=None,
@@ -612,16 +622,15 @@ def ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, has_initial_state,
     include/ssd.h): row b of o, q, k, v is sequence b's token; other arguments
     as for ssd_linear_attn_varlen_fwd_inplace.  One kernel, no workspace.
     """
-    import torch
     batch = v.shape[0]
     slots = pool.shape[0]
-    prob, _, _, dev, state = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
+    prob, _, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
     out = _dense(o, "o", torch.bfloat16, v.shape, dev)
     states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
     idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
     f = load_library().ssd_linear_attn_step_inplace
     _launch("ssd_linear_attn_step_inplace", dev, stream, lambda st: f(
-        prob, out, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), states, flags, idx, st))
+        prob, out, *inputs, states, flags, idx, st))
 
 
 @functools.lru_cache(maxsize=256)
@@ -632,7 +641,8 @@ def _state_cache_sizes(*sizes):
 def _state_cache(pool, codes, scales, pool_indices, entry_indices):
     """Problem, device and addresses (pool, codes, scales, pool_indices, entry_indices) of a state-cache call,
     its tensors checked."""
-    import torch
+    if torch is None:
+        _import_torch()
     dev = pool.device
     if dev.type != "cuda":
         raise ValueError("libssd runs on a HIP device; got tensors on " + str(dev))
