@@ -730,7 +730,7 @@ hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
 // 575, at a quarter 696).
 // A segment shorter than the mean sequence is made to divide it.
 Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, int nops, int nlocal) {
-    constexpr int64_t kLeast = 256;
+    constexpr int64_t kLeast = 128;
     const int vd = *std::max_element(vds, vds + nops);
     Shape h;
     h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
@@ -759,7 +759,7 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     const int64_t parts = std::max<int64_t>(1, std::min((kAtOnce + local - 1) / local, seg / kLeast));
     const int64_t sub = (seg + parts * kTok - 1) / (parts * kTok) * kTok;
     seg = sub * parts;
-    const bool cut = T > seg;
+    const bool cut = T > std::max<int64_t>(seg, 2 * kLeast);
     h.seg = cut ? (int)seg : 0;
     h.sub = cut ? (int)sub : 0;
     h.slots = cut ? (int)(T / seg) + batch : batch;
