@@ -42,10 +42,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 
-// LDS layout of a chunk's rows: unit c of row r at byte c kUnit + 16 r.  Every
-// place is a lane's base plus a constant, which is the offset field of the
-// instruction: one register serves a whole phase.
-constexpr int kUnit = kTok * 16 + 64;
+// LDS layout of a chunk's CT rows: unit c of row r at byte c unit_bytes + 16 r.
+// Every place is a lane's base plus a constant, which is the offset field of
+// the instruction: one register serves a whole phase.
+constexpr int unit_bytes(int CT) { return CT * 16 + 64; }
 
 __device__ __forceinline__ bf16x8 read_unit(const char *s, int at) {
     return *reinterpret_cast<const bf16x8 *>(s + at);
@@ -205,25 +205,28 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void *base, 
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every such buffer
 
 // KD: channels of k and q the kernel holds (kd rounded up; the rest is zero);
-// NW wavefronts of DT tiles of 16 value channels, for HP heads.
+// CT: tokens of a chunk; NW wavefronts of DT tiles of 16 value channels, for HP
+// heads.
 // LOCAL: only the state a segment leaves when it starts from zero.
-template <int KD, int NW, int DT, int HP, bool SB, bool LOCAL>
-__global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
+template <int KD, int CT, int NW, int DT, int HP, bool SB, bool LOCAL>
+__global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
+    constexpr int kUnit = unit_bytes(CT);
+    constexpr int RT = CT / 16;      // 16-token tiles of a chunk
     constexpr int NTH = 64 * NW;
     constexpr int WH = NW / HP;      // wavefronts of a head
     constexpr int VT = 16 * DT * WH; // value channels of the workgroup, of each head
     constexpr int UK = KD / 8;       // units of a q or k row
     constexpr int UV = HP * VT / 8;  // and of the heads' v rows together
     constexpr int NT = KD / 32;      // blocks of 32 k channels of a wavefront's state
-    constexpr int LK = kTok * UK / NTH, LV = kTok * UV / NTH;  // 16-byte loads of a thread
+    constexpr int LK = CT * UK / NTH, LV = CT * UV / NTH;  // 16-byte loads of a thread
     constexpr int RK = NTH / UK, RV = NTH / UV;                // rows between them
-    constexpr int kScores = kTok / 8 * kUnit;
+    constexpr int kScores = CT / 8 * kUnit;
     static_assert(VT % 32 == 0, "pairs of tiles");
     __shared__ __attribute__((aligned(16))) char s_q[LOCAL ? 16 : UK * kUnit];
     __shared__ __attribute__((aligned(16))) char s_k[UK * kUnit];
     __shared__ __attribute__((aligned(16))) char s_v[UV * kUnit];
     __shared__ __attribute__((aligned(16))) char s_p[LOCAL ? 16 : HP * kScores];
-    __shared__ float s_pair[HP][96], s_lead[HP][64];
+    __shared__ float s_pair[HP][CT + 32], s_lead[HP][CT];
 
     // Consecutive workgroups go to the 8 XCDs in turn.  The workgroups that
     // read the same rows (a group's heads, their blocks of channels, the
@@ -304,7 +307,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     }
 
     // ---- constants of the walk.  Place r of a chunk of len tokens is its
-    // token r - pad (pad = 64 - len), or in reverse 63 - r: a short chunk ends
+    // token r - pad (pad = CT - len), or in reverse CT - 1 - r: a short chunk ends
     // at the last place, where the weights of the state update are the full
     // chunk's, and starts with rows of zeros.
     // In LDS: weights of the scores by distance i - j (0 above the diagonal),
@@ -312,8 +315,8 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     if (tid < HP * 128) {
         const int i = tid & 127, d = i - 31;
         const float l2h = HP == 1 ? l2 : log2_decay(p, h0 + (tid >> 7));
-        if (i < 95) s_pair[tid >> 7][i] = d >= 0 ? op.scale_pair * fast_exp2(l2h * (float)d) : 0.f;
-        if (i < 64) s_lead[tid >> 7][i] = op.scale_update * fast_exp2(l2h * ((float)i + shift));
+        if (i < CT + 31) s_pair[tid >> 7][i] = d >= 0 ? op.scale_pair * fast_exp2(l2h * (float)d) : 0.f;
+        if (i < CT) s_lead[tid >> 7][i] = op.scale_update * fast_exp2(l2h * ((float)i + shift));
     }
     const bool fine = !SB && op.state_out != nullptr;  // three parts of the weighted v, or two
 
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
 
     u32x4 fq[LOCAL ? 1 : LK], fk[LK], fv[LV];
     auto fetch = [&](int c0) {  // the chunk's rows, lowest token first, into registers
-        const int len = min(kTok, n - c0);
+        const int len = min(CT, n - c0);
         const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
         const auto bk = rows_buffer(gk + first * ks, (uint32_t)((len - 1) * ks + kd) * 2);
         const auto bv = rows_buffer(gv + first * vs, (uint32_t)((len - 1) * vs + HP * vd) * 2);
@@ -361,22 +364,22 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     // in 16-row tile rt of q, scores and outputs, lane l16 is token place0 + row_tile(rt)
     auto row_tile = [](int rt) { return 32 * (rt >> 1) + 4 * (rt & 1); };
     const int place0 = 8 * (l16 >> 2) + (l16 & 3);
-    f32x4 O[4][DT] = {};
+    f32x4 O[RT][DT] = {};
     // Stores the outputs of the chunk at c0: a token a tile, channels 8 q4 .. of
     // a pair of tiles (half of them with one tile).  A chunk's outputs leave behind
     // the barriers of the next one, ahead of its loads: waiting for loads then
     // never waits for younger stores.
     auto emit = [&](int c0) {
-        const int len = min(kTok, n - c0), pad = kTok - len;
+        const int len = min(CT, n - c0), pad = CT - len;
         const int64_t first = rev ? t0 + n - c0 - len : t0 + c0;
         const int eb = out_f32 ? 4 : 2;
         const auto bo = rows_buffer(static_cast<char *>(op.out) + (first * os + (int64_t)h * vd) * eb,
                                     (uint32_t)((len - 1) * os + vd) * eb);
         const int vc = v0 + 32 * (tile0 >> 1) + 8 * q4 + 4 * (tile0 & 1);
-        const int tok0 = rev ? 63 - place0 : place0 - pad;
+        const int tok0 = rev ? CT - 1 - place0 : place0 - pad;
         const uint32_t at0 = (uint32_t)((tok0 * os + vc) * eb);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
+        for (int rt = 0; rt < RT; ++rt) {
             const int more = row_tile(rt);
             const int tok = rev ? tok0 - more : tok0 + more;
             const uint32_t at = vc < vd && (uint32_t)tok < (uint32_t)len
@@ -410,17 +413,17 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     const int at_col = (4 * q4 + (l16 >> 2)) * 16 + (l16 & 3) * kUnit;
     const int v_units = (hw * (VT / 8) + 4 * (tile0 >> 1)) * kUnit;
     const float *const w_pair = s_pair[0] + 31 + place0 - 4 * q4;
-    const float *const w_lead = s_lead[hw] + 63 - 4 * q4;
+    const float *const w_lead = s_lead[hw] + CT - 1 - 4 * q4;
     const int scores = hw * kScores;
 
     // the chunk's v columns, kept for the scores' product
-    bf16x8 vcol[kTok / 32][DT];
+    bf16x8 vcol[CT / 32][DT];
     // out^T += v^T scores^T of the chunk whose scores are complete
     auto add_scores = [&]() {
 #pragma unroll
-        for (int u = 0; u < kTok / 32; ++u)
+        for (int u = 0; u < CT / 32; ++u)
 #pragma unroll
-            for (int rt = 2 * u; rt < 4; ++rt) {
+            for (int rt = 2 * u; rt < RT; ++rt) {
                 const bf16x8 x = read_unit(s_p, scores + at_place + row_tile(rt) * 16 + 4 * u * kUnit);
 #pragma unroll
                 for (int d = 0; d < DT; ++d) O[rt][d] = mfma_bf16(vcol[u][d], x, O[rt][d]);
@@ -430,39 +433,40 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     // Two barriers a chunk: between them lie (A to B) the rows' way into LDS
     // and the scores' product of the chunk before, and (B to A) everything else.
 #pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += kTok) {
-        const int len = min(kTok, n - c0), pad = kTok - len;
+    for (int c0 = 0; c0 < n; c0 += CT) {
+        const int len = min(CT, n - c0), pad = CT - len;
         __syncthreads();  // A: the previous chunk's rows are read, its scores written
         // token i of the chunk to its place; tokens past it (zeros) wrap to the places before it
         const int ft = opaque(tid), ck = unit_of(ft, UK), rk = row_of(ft, UK), cv = unit_of(ft, UV),
                   rv = row_of(ft, UV);
 #pragma unroll
         for (int i = 0; i < LK; ++i) {
-            const int r = rev ? 63 - (rk + i * RK) : (rk + i * RK + pad) & 63;
+            const int r = rev ? CT - 1 - (rk + i * RK) : (rk + i * RK + pad) & (CT - 1);
             *reinterpret_cast<u32x4 *>(s_k + ck * kUnit + r * 16) = fk[i];
             if constexpr (!LOCAL) *reinterpret_cast<u32x4 *>(s_q + ck * kUnit + r * 16) = fq[i];
         }
 #pragma unroll
         for (int i = 0; i < LV; ++i) {
-            const int r = rev ? 63 - (rv + i * RV) : (rv + i * RV + pad) & 63;
+            const int r = rev ? CT - 1 - (rv + i * RV) : (rv + i * RV + pad) & (CT - 1);
             *reinterpret_cast<u32x4 *>(s_v + cv * kUnit + r * 16) = fv[i];
         }
         if (!LOCAL && c0 > 0) {
             add_scores();
-            emit(c0 - kTok);
+            emit(c0 - CT);
         }
         __syncthreads();  // B
-        if (c0 + kTok < n) fetch(c0 + kTok);
+        if (c0 + CT < n) fetch(c0 + CT);
 
         if constexpr (!LOCAL) {
             // ---- weighted scores, for all heads, in blocks of 16 RB tokens i
-            // (lanes) x 32 tokens j (8 a lane): with four wavefronts 32 x 32 blocks
-            // (rt, c) = (0, 0) (2, 0) (2, 1), with eight 16 x 32 ones
-            constexpr int RB = NW == 4 ? 2 : 1;
+            // (lanes) x 32 tokens j (8 a lane): of 64 tokens (rt, c) = (0, 0) (2, 0)
+            // (2, 1), of 32 (0, 0) (1, 0)
+            constexpr int RB = CT == 64 ? 2 : 1;
+            static_assert(NW >= 3, "a wavefront for each block");
 #pragma unroll
-            for (int m = 0; m < 6 / RB; ++m) {
+            for (int m = 0; m < (CT == 64 ? 3 : 2); ++m) {
                 if (m != wave) continue;
-                const int c = m < 4 / RB ? 0 : 1, rt = RB * m - 2 * c;
+                const int c = m == 2 ? 1 : 0, rt = RB * (m - c);
                 f32x4 a[RB][2] = {};
 #pragma unroll
                 for (int u = 0; u < KD / 32; ++u) {
@@ -486,7 +490,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             f[e] = a[i][e / 4][e % 4] *
-                                   w_pair[96 * x + row_tile(rt + i) - 32 * c - 16 * (e / 4) - e % 4];
+                                   w_pair[(CT + 32) * x + row_tile(rt + i) - 32 * c - 16 * (e / 4) - e % 4];
                         *reinterpret_cast<bf16x8 *>(s_p + x * kScores + at_place + row_tile(rt + i) * 16 +
                                                     4 * c * kUnit) = pack8(f);
                     }
@@ -504,7 +508,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
                     a[d] = pack8(f);
                 }
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
+                for (int rt = 0; rt < RT; ++rt) {
                     const bf16x8 q = read_unit(s_q, at_place + row_tile(rt) * 16 + 4 * t * kUnit);
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
@@ -512,7 +516,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
                 }
             }
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
+            for (int rt = 0; rt < RT; ++rt) {
                 const float x = scale_state * fast_exp2(l2 * ((float)(place0 + row_tile(rt) - pad + 1) - shift));
 #pragma unroll
                 for (int d = 0; d < DT; ++d) O[rt][d] *= x;
@@ -531,7 +535,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
             }
         }
 #pragma unroll
-        for (int u = 0; u < kTok / 32; ++u) {
+        for (int u = 0; u < CT / 32; ++u) {
             bf16x8 part3[DT][3];
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
@@ -573,7 +577,7 @@ __global__ __launch_bounds__(64 * NW, 2) void la_walk(Params p) {
     if (!LOCAL && n > 0) {
         __syncthreads();
         add_scores();
-        emit((n - 1) / kTok * kTok);
+        emit((n - 1) / CT * CT);
     }
 
     if constexpr (LOCAL) {
@@ -649,7 +653,7 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
         for (int s = 0; s <= last; s += kAhead) {
             f32x4 own[kAhead];  // loaded ahead of the chain
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) own[a] = s + a < last ? part[a * step] : f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int a = 0; a < kAhead; ++a) own[a] = in && s + a < last ? part[a * step] : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
                 if (s + a <= last && (s + a) % parts == 0) {
@@ -686,41 +690,41 @@ __global__ __launch_bounds__(256) void la_group_sum(GroupSum a, const int32_t *q
     store_state8<true>(a.dst[blockIdx.y], i * 8, s);
 }
 
-template <int KD, int NW, int DT, int HP, bool SB>
+template <int KD, int CT, int NW, int DT, int HP, bool SB>
 hipError_t launch_variant(const Params &p, hipStream_t s) {
     constexpr int VT = 16 * DT * NW / HP;
     const int64_t each = (int64_t)(p.H / HP) * p.tiles * p.nops, run = (int64_t)8 * (p.share / HP) * p.tiles * p.nops;
     auto grid = [&](int slots) { return dim3((unsigned)((slots * each + run - 1) / run * run)); };
     const dim3 block(64 * NW);
     if (p.seg != 0) {
-        la_walk<KD, NW, DT, HP, SB, true><<<grid(p.sub_slots), block, 0, s>>>(p);
+        la_walk<KD, CT, NW, DT, HP, SB, true><<<grid(p.sub_slots), block, 0, s>>>(p);
         // blocks for the card, or one for each head
         const int64_t heads = (int64_t)p.batch * p.H;
         const int most = p.tiles * VT * KD / 1024, split = (int)std::min<int64_t>(most, (2048 + heads - 1) / heads);
         const dim3 cg((unsigned)heads, (unsigned)p.nops, (unsigned)split);
         la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, VT);
     }
-    la_walk<KD, NW, DT, HP, SB, false><<<grid(p.slots), block, 0, s>>>(p);
+    la_walk<KD, CT, NW, DT, HP, SB, false><<<grid(p.slots), block, 0, s>>>(p);
     return hipGetLastError();
 }
 template <int KD, bool SB>
 hipError_t launch_kd(const Params &p, const Shape &h, hipStream_t s) {
-    constexpr int NW = KD == 256 ? 8 : 4, DT = KD == 256 ? 1 : 2;
-    if (h.vt == 128) return launch_variant<KD, NW, DT, 1, SB>(p, s);
-    if (h.heads == 2) return launch_variant<KD, NW, DT, 2, SB>(p, s);
-    return launch_variant<KD, 4, 1, 1, SB>(p, s);
+    if (h.vt == 128) return launch_variant<KD, 64, 4, 2, 1, SB>(p, s);
+    if (h.heads == 2) return launch_variant<KD, 64, 4, 2, 2, SB>(p, s);
+    return launch_variant<KD, 64, 4, 1, 1, SB>(p, s);
 }
 template <bool SB>
 hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
     if (h.kd == 64) return launch_kd<64, SB>(p, h, s);
     if (h.kd == 128) return launch_kd<128, SB>(p, h, s);
-    return launch_kd<256, SB>(p, h, s);
+    if (h.vt == 128) return launch_variant<256, 64, 8, 1, 1, SB>(p, s);
+    return launch_variant<256, 32, 4, 1, 1, SB>(p, s);
 }
 }  // namespace
 
 // A walk is a chain of chunks, so a launch needs many walks side by side: the
-// card holds kAtOnce workgroups (two on each of 256 compute units, one of the
-// widest).  Sequences are cut into segments of as many tokens as let their
+// card holds kAtOnce workgroups (two on each of 256 compute units, one or three
+// with wide keys).  Sequences are cut into segments of as many tokens as let their
 // number, T / seg and half a segment for each sequence's end, fill the card
 // once; cut sequences cost a pass over their k and v for the segments' states,
 // so more of them only cost (65536 tokens of 16 heads: 32 segments 388 us, 48
@@ -734,17 +738,24 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     const int vd = *std::max_element(vds, vds + nops);
     Shape h;
     h.kd = kd <= 64 ? 64 : kd <= 128 ? 128 : 256;
-    h.vt = vd <= 64 ? 64 : 128;
-    h.heads = h.vt == 64 && share % 2 == 0 && nops == 1 ? 2 : 1;
-    const int64_t kAtOnce = h.kd == 256 ? 256 : 512;
+    const int64_t mean = (T + batch - 1) / batch;
+    // Wide keys: one workgroup of 8 wavefronts and 128 value channels fills a
+    // compute unit's LDS; where sequences are short, and their states most of the
+    // traffic, three with 64 channels and chunks of 32 tokens move them faster (20
+    // sequences of 27 tokens in the mean, backward: 82 -> 62 us; packed documents
+    // of 1700: 413 -> 508).
+    h.vt = vd <= 64 || (h.kd == 256 && mean <= 256) ? 64 : 128;
+    h.heads = h.vt == 64 && h.kd < 256 && share % 2 == 0 && nops == 1 ? 2 : 1;
+    const int64_t kAtOnce = h.kd < 256 ? 512 : h.vt == 64 ? 768 : 256;
     auto tiles = [&](int n) {
         int sum = 0;
         for (int i = 0; i < n; ++i) sum += (vds[i] + h.vt - 1) / h.vt;
         return (int64_t)(H / h.heads) * sum;
     };
-    h.tiles = (vd + h.vt - 1) / h.vt;
+    // with states handed on transposed (la_chain), as many v channels as k channels
+    h.tiles = (nlocal < nops ? h.kd : vd) / h.vt + ((nlocal < nops ? 0 : vd) % h.vt != 0);
     const int64_t walks = tiles(nops);  // workgroups of a token
-    const int64_t mean = (T + batch - 1) / batch, room = kAtOnce - batch * walks / 2;
+    const int64_t room = kAtOnce - batch * walks / 2;
     int64_t seg = 2 * T * walks / kAtOnce;
     if (room > 0) seg = std::min(seg, T * walks / room);
     seg = std::max(seg, kLeast);

@@ -13,7 +13,14 @@ BF16 = torch.finfo(torch.bfloat16).eps / 2  # largest relative error of one roun
 # w x <= 0.54 for w = 2^-x), and the chain's own products: under 128 units of
 # 2^-24.
 FP32 = 2.0 ** -17
-CHUNK = 64
+
+
+def chunk_of(rows, batch, K, V, backward=False):
+    """Tokens of a chunk, which decide what reaches an output through rounded scores and what through the rounded
+    state: 32 where more than 128 channels are summed over for at most 64 value channels or short sequences, else
+    64 (a backward launch goes by the wider of K and V)."""
+    k, v = (max(K, V), max(K, V)) if backward else (K, V)
+    return 32 if k > 128 and (v <= 64 or -(-rows // batch) <= 256) else 64
 
 
 def draw(lens, H, G, K, V, seed, *, slots=0, tail=0):
@@ -79,7 +86,7 @@ def gradients(d, lens, scale, initial=None, d_final=None):
     return torch.autograd.grad(loss, (q, k, v, S0), allow_unused=True, materialize_grads=True)
 
 
-def magnitudes(q, k, v, lam, c_pair, c_state, c_update, S, reverse=False):
+def magnitudes(q, k, v, lam, c_pair, c_state, c_update, S, reverse=False, chunk=64):
     """The chunked sum of one sequence with magnitudes in place of its rounded operands: for each output the sum of
     |rounded operand| |exact operand| (scores and the state are rounded to bf16, once each), and the sum of the
     magnitudes of all the final state's terms.  The scalar c's multiply pairs, state reads and state updates."""
@@ -89,8 +96,8 @@ def magnitudes(q, k, v, lam, c_pair, c_state, c_update, S, reverse=False):
     out = torch.zeros(n, *v.shape[1:], dtype=torch.float64)
     S, A = S.clone(), S.abs()
     qh, kh, vh = (x.transpose(0, 1) for x in (q, k, v))  # [H, n, .]
-    for c in range(0, n, CHUNK):
-        s = slice(c, min(c + CHUNK, n))
+    for c in range(0, n, chunk):
+        s = slice(c, min(c + chunk, n))
         m = s.stop - s.start
         i = torch.arange(m, dtype=torch.float64)
         gap = i[:, None] - i[None, :]
@@ -116,7 +123,7 @@ def forward_bounds(d, lens, scale, initial=None):
         S = initial[b].double() if initial is not None else torch.zeros(H, V, K, dtype=torch.float64)
         s = slice(at, at + n)
         m, A = magnitudes(spread(d["q"][s].double(), H), spread(d["k"][s].double(), H), d["v"][s].double(), lam,
-                          scale, scale, 1.0, S)
+                          scale, scale, 1.0, S, chunk=chunk_of(d["v"].shape[0], len(lens), K, V))
         o.append(m)
         f.append(A)
         at += n
@@ -129,15 +136,15 @@ def backward_bounds(d, lens, scale, initial=None, d_final=None):
     G = d["q"].shape[1]
     lam = torch.exp(d["log_decay"].double())
     zero = torch.zeros(H, V, K, dtype=torch.float64)
-    dq, dk, dv, di, at = [], [], [], [], 0
+    dq, dk, dv, di, at, chunk = [], [], [], [], 0, chunk_of(d["v"].shape[0], len(lens), K, V, True)
     for b, n in enumerate(lens):
         s = slice(at, at + n)
         q, k, v, g = (spread(d[x][s].double(), H) for x in ("q", "k", "v", "d_o"))
         S = initial[b].double() if initial is not None else zero
         R = d_final[b].double() if d_final is not None else zero
-        dq.append(magnitudes(g, v, k, lam, scale, scale, 1.0, S.transpose(1, 2))[0])
-        dk.append(magnitudes(v, g, q, lam, scale, 1.0, scale, R.transpose(1, 2), reverse=True)[0])
-        m, A = magnitudes(k, q, g, lam, scale, 1.0, scale, R, reverse=True)
+        dq.append(magnitudes(g, v, k, lam, scale, scale, 1.0, S.transpose(1, 2), chunk=chunk)[0])
+        dk.append(magnitudes(v, g, q, lam, scale, 1.0, scale, R.transpose(1, 2), reverse=True, chunk=chunk)[0])
+        m, A = magnitudes(k, q, g, lam, scale, 1.0, scale, R, reverse=True, chunk=chunk)
         dv.append(m)
         di.append(A)
         at += n

@@ -413,3 +413,122 @@ def test_captured_and_replayed():
         eager = _all_calls(c, lens)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(want, got, eager))
+
+
+# ------------------------------------------------------------------ as a differentiable function
+
+def test_autograd_of_a_fused_projection():
+    """Gradients reach the projection whose slices q, k and v are, and the initial states, with the loss on both
+    outputs; rows behind the last sequence get zeros."""
+    from mamba_ssd_chunked_chunk_amd.linear_attention import linear_attention
+    lens, H, G, K, V, tail = [90, 0, 300], 4, 2, 64, 64, 11
+    d = L.draw(lens, H, G, K, V, 1600, tail=tail)
+    T = sum(lens) + tail
+    c = cuda(d)
+    fused = torch.cat([c[n].reshape(T, -1) for n in "qkv"], 1).requires_grad_()
+    initial = c["initial"].clone().requires_grad_()
+    q, k, v = fused.split([G * K, G * K, H * V], 1)
+    o, final = linear_attention(q.view(T, G, K), k.view(T, G, K), v.view(T, H, V), c["log_decay"],
+                                c["query_start_loc"], initial, padded=True)
+    assert bool((o[sum(lens):] == 0).all())
+    df, di = torch.autograd.grad([o, final], [fused, initial], [c["d_o"], c["d_final"]])
+    want = L.gradients(d, lens, K ** -0.5, d["initial"], d["d_final"])
+    bounds = L.backward_bounds(d, lens, K ** -0.5, d["initial"], d["d_final"])
+    n = sum(lens)
+    got = [x.reshape(T, h, w) for x, h, w in zip(df.split([G * K, G * K, H * V], 1), (G, G, H), (K, K, V))]
+    for g, w, b in zip(got, want, bounds):
+        assert L.worst(g[:n], w, b, rounding(BF16)) <= 1 and bool((g[n:] == 0).all())
+    assert L.worst(di, want[3], bounds[3], rounding(F32)) <= 1
+
+
+@pytest.mark.parametrize("use", ["o", "final", "expanded"])
+def test_autograd_of_one_output(use):
+    from mamba_ssd_chunked_chunk_amd.linear_attention import linear_attention
+    lens = [70, 33]
+    d = L.draw(lens, 2, 2, 64, 64, 1610)
+    c = cuda(d)
+    x = [c[n].clone().requires_grad_() for n in "qkv"]
+    o, final = linear_attention(*x, c["log_decay"], c["query_start_loc"], scale=0.2)
+    zero = torch.zeros_like(d["d_o"])
+    if use == "o":
+        grads, e, df = torch.autograd.grad(o, x, c["d_o"]), d, None
+    elif use == "final":
+        grads, e, df = torch.autograd.grad(final, x, c["d_final"], allow_unused=True), dict(d, d_o=zero), d["d_final"]
+    else:  # the gradient of a sum: one number, expanded
+        grads, e, df = torch.autograd.grad(o.sum(), x), dict(d, d_o=torch.ones_like(d["d_o"])), None
+    want = L.gradients(e, lens, 0.2, None, df)
+    bounds = L.backward_bounds(e, lens, 0.2, None, df)
+    for g, w, b in zip(grads, want, bounds):
+        assert L.worst(g, w, b, rounding(BF16)) <= 1
+
+
+def test_autograd_refuses_a_learned_decay():
+    from mamba_ssd_chunked_chunk_amd.linear_attention import linear_attention
+    d = cuda(L.draw([5], 1, 1, 64, 64, 1620))
+    with pytest.raises(ValueError, match="gradient"):
+        linear_attention(d["q"], d["k"], d["v"], d["log_decay"].requires_grad_(), d["query_start_loc"])
+
+
+# ------------------------------------------------------------------ together
+
+def test_prompt_steps_preemption_and_resumption():
+    """A server's life: prompts in one ragged batch, decode steps, one sequence parked in 8 bits while the others go
+    on, read back into another slot and continued: its later outputs are those of the state that the codes stand for."""
+    lens, H, G, K, V, S = [150, 7, 64], 4, 2, 64, 64, 6
+    steps = 4
+    d = L.draw([n + 2 * steps for n in lens], H, G, K, V, 1700, slots=S)
+    scale, lam = K ** -0.5, torch.exp(d["log_decay"].double())
+    starts = [int(x) for x in d["query_start_loc"]]
+    c = cuda(d)
+    pool, slots = c["pool"].clone(), c["cache_indices"]
+
+    def rows(first, count):
+        return torch.cat([torch.arange(starts[b] + first(b), starts[b] + first(b) + count(b)) for b in range(3)])
+
+    at = rows(lambda b: 0, lambda b: lens[b]).cuda()
+    qsl = torch.tensor([0, 150, 157, 221], dtype=torch.int32, device="cuda")
+    o = torch.zeros_like(c["v"])
+    part = torch.empty(221, H, V, dtype=BF16, device="cuda")
+    binding.ssd_linear_attn_varlen_fwd_inplace(part, c["q"][at], c["k"][at], c["v"][at], c["log_decay"], pool, qsl,
+                                               None, slots)
+    o[at] = part
+    ones = torch.ones(3, dtype=torch.uint8, device="cuda")
+
+    def step(t, idx):
+        at = torch.tensor([starts[b] + lens[b] + t for b in range(3)], device="cuda")
+        out = o[at]
+        binding.ssd_linear_attn_step_inplace(out, c["q"][at], c["k"][at], c["v"][at], c["log_decay"], pool, ones, idx)
+        o[at] = out
+
+    for t in range(steps):
+        step(t, slots)
+    codes = torch.zeros(2, H, V, K, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(2, H, V, device="cuda")
+    entry = torch.tensor([1], dtype=torch.int32, device="cuda")
+    binding.ssd_state_quantize(codes, scales, pool, slots[1:2], entry)
+    pool[slots[1].long()] = float("nan")  # the slot goes to somebody else
+    away = slots.clone()
+    away[1] = S  # padding: sequence 1 is not there
+    for t in range(steps, 2 * steps):
+        step(t, away)
+    free = [s for s in range(S) if s not in slots.tolist()][0]
+    back = torch.tensor([free], dtype=torch.int32, device="cuda")
+    binding.ssd_state_dequantize(pool, codes, scales, back, entry)
+    away[:] = S
+    away[1] = free
+    for t in range(steps, 2 * steps):
+        step(t, away)
+
+    # the reference: uninterrupted for 0 and 2; sequence 1 continued from what its codes stand for
+    full = [n + 2 * steps for n in lens]
+    want, _ = L.reference(d, full, scale)
+    bound, _ = L.forward_bounds(d, full, scale)
+    s1 = slice(starts[1] + lens[1] + steps, starts[2])
+    stored = (codes[1].double() * scales[1].double()[..., None]).cpu()
+    want[s1], _ = L.recur(*(L.spread(d[n][s1].double(), H) for n in "qk"), d["v"][s1].double(), lam, scale, stored)
+    assert L.worst(o, want, bound, rounding(BF16)) <= 1
+    # and those codes are within half a code of the state that was parked
+    T1 = slice(starts[1], starts[1] + lens[1] + steps)
+    _, parked = L.recur(*(L.spread(d[n][T1].double(), H) for n in "qk"), d["v"][T1].double(), lam, scale,
+                        torch.zeros(H, V, K, dtype=torch.float64))
+    assert bool(((stored - parked).abs() <= scales[1].cpu().double()[..., None] * (0.5 + 2.0 ** -9)).all())
