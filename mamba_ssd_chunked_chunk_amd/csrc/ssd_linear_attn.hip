@@ -611,7 +611,7 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
 // as well.
 template <bool SB>
 __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     const int per_head = p.tiles * VT * KD / 4;  // groups of 4
     const int h = blockIdx.x % p.H, b = blockIdx.x / p.H;
     const int which = blockIdx.y;
@@ -650,19 +650,21 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
         const int mlane = vch % 32 / 8 * 16 + kc % 32 / 8 * 4;
         float *twin = p.parts + 4 * ((int64_t)op.mirror * p.sub_slots * step + head +
                                      ((mtile * (KD / 32) + mt) * 2 + my) * 64 + mlane) + vch % 4;
+        int rest = 0;  // parts until the next segment starts
         for (int s = 0; s <= last; s += kAhead) {
             f32x4 own[kAhead];  // loaded ahead of the chain
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) own[a] = in && s + a < last ? part[a * step] : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (s + a <= last && (s + a) % parts == 0) {
+                if (s + a <= last && rest == 0) {
                     part[a * step] = S;
                     if (mirrored) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) twin[4 * (a * step + e)] = S[e];
                     }
                 }
+                rest = rest == 0 ? parts - 1 : rest - 1;
                 S = S * keep + own[a];
             }
             part += kAhead * step;
@@ -700,7 +702,7 @@ hipError_t launch_variant(const Params &p, hipStream_t s) {
         la_walk<KD, CT, NW, DT, HP, SB, true><<<grid(p.sub_slots), block, 0, s>>>(p);
         // blocks for the card, or one for each head
         const int64_t heads = (int64_t)p.batch * p.H;
-        const int most = p.tiles * VT * KD / 1024, split = (int)std::min<int64_t>(most, (2048 + heads - 1) / heads);
+        const int most = p.tiles * VT * KD / 1024, split = (int)std::min<int64_t>(most, (4096 + heads - 1) / heads);
         const dim3 cg((unsigned)heads, (unsigned)p.nops, (unsigned)split);
         la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, VT);
     }
@@ -770,7 +772,8 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     const int64_t parts = std::max<int64_t>(1, std::min((kAtOnce + local - 1) / local, seg / kLeast));
     const int64_t sub = (seg + parts * kTok - 1) / (parts * kTok) * kTok;
     seg = sub * parts;
-    const bool cut = T > std::max<int64_t>(seg, 2 * kLeast);
+    // (512 tokens: the longest walk that takes no longer than the two more launches)
+    const bool cut = T > std::max<int64_t>(seg, 512);
     h.seg = cut ? (int)seg : 0;
     h.sub = cut ? (int)sub : 0;
     h.slots = cut ? (int)(T / seg) + batch : batch;
