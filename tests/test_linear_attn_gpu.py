@@ -80,6 +80,14 @@ def test_prompt_many_sequences():
     check_prompt(lens, 2, 1, 64, 64, 500, tail=3)
 
 
+@pytest.mark.parametrize("n,extra", [(65, []), (700, []), (5000, [2000])])
+def test_prompt_more_sequences_than_lanes(n, extra):
+    """More than 64 sequences are found by search, in steps of 64; with a long one among them some are cut."""
+    lens = [int(x) for x in torch.randint(0, 3, (n,), generator=torch.Generator().manual_seed(n))]
+    lens[n // 2:n // 2] = extra
+    check_prompt(lens, 2, 2, 8, 8, 510 + n, init="half")
+
+
 @pytest.mark.parametrize("lens", [[3000], [1700, 5, 900, 2100], [64 * 40], [64 * 40 + 1, 64 * 40 - 1]])
 def test_prompt_long(lens):
     check_prompt(lens, 2, 1, 64, 128, 600, init="half", tail=5)
@@ -122,6 +130,36 @@ def test_padding_entries_and_unread_slots(lens):
     assert L.worst(pool[slots[live].cuda()], final[live], bf[live], rounding(F32)) <= 1
     others = [s for s in range(4) if s not in slots[live].tolist()]
     assert bool(torch.isnan(pool[others]).all())
+
+
+def test_slots_behind_2_31_elements():
+    """A pool whose last slot starts behind element 2^31, and rows of it read and written by prompt and step."""
+    H, K, V = 64, 128, 128
+    S = 2 ** 31 // (H * K * V) + 2
+    lens = [70]
+    d = L.draw(lens, H, 8, K, V, 805)
+    c = cuda(d)
+    pool = torch.zeros(S, H, V, K, dtype=BF16, device="cuda")
+    pool[S - 1] = c["initial"][0].bfloat16()
+    first = pool[S - 1].cpu().float()[None]
+    idx = torch.tensor([S - 1], dtype=torch.int32, device="cuda")
+    ones = torch.ones(1, dtype=torch.uint8, device="cuda")
+    o = torch.empty_like(c["v"])
+    binding.ssd_linear_attn_varlen_fwd_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool, c["query_start_loc"],
+                                               ones, idx, scale=0.1)
+    want, final = L.reference(d, lens, 0.1, first)
+    bo, bf = L.forward_bounds(d, lens, 0.1, first)
+    assert L.worst(o, want, bo, rounding(BF16)) <= 1
+    assert L.worst(pool[S - 1:], final, bf, rounding(BF16)) <= 1
+    assert not bool(pool[:S - 1].any())
+    kept = pool[S - 1].cpu().double()
+    binding.ssd_linear_attn_step_inplace(o[:1], c["q"][:1], c["k"][:1], c["v"][:1], c["log_decay"], pool, ones, idx,
+                                         scale=0.1)
+    one, state = L.recur(L.spread(d["q"][:1].double(), H), L.spread(d["k"][:1].double(), H), d["v"][:1].double(),
+                         torch.exp(d["log_decay"].double()), 0.1, kept)
+    assert L.worst(pool[S - 1], state, kept.abs() * 2.0 ** -22 + 2.0 ** -22, rounding(BF16)) <= 1
+    assert L.worst(o[:1], one, 0.1 * (state.abs() * L.spread(d["q"][:1].double(), H)[0].abs()[:, None, :]).sum(-1)[None]
+                   * 2.0 ** -16, rounding(BF16)) <= 1
 
 
 def test_no_rows_at_all():
@@ -294,8 +332,29 @@ def test_backward_states(initial, final, dtype):
 
 
 @pytest.mark.parametrize("lens", [[2500], [1500, 3, 900, 1800]])
-def test_backward_long(lens):
-    check_backward(lens, 2, 1, 64, 128, 1350)
+@pytest.mark.parametrize("K,V", [(64, 128), (136, 40), (32, 160)])
+def test_backward_long(lens, K, V):
+    check_backward(lens, 2, 1, K, V, 1350 + K)
+
+
+def test_backward_many_sequences():
+    lens = [int(x) for x in torch.randint(0, 40, (100,), generator=torch.Generator().manual_seed(9))] + [700]
+    check_backward(lens, 2, 1, 64, 64, 1360, tail=3)
+
+
+def test_backward_long_states_in_one_buffer():
+    """The same as the next with cut sequences, whose segments' states dk and dv do not share here."""
+    lens = [900, 1300]
+    d = L.draw(lens, 2, 2, 64, 64, 1411)
+    c = cuda(d)
+    g = [torch.empty_like(c[n]) for n in "qkv"]
+    df = c["d_final"].clone()
+    binding.ssd_linear_attn_varlen_bwd(*g, df, c["q"], c["k"], c["v"], c["d_o"], c["log_decay"], c["initial"], df,
+                                       c["query_start_loc"], scale=0.2)
+    want = L.gradients(d, lens, 0.2, d["initial"], d["d_final"])
+    bounds = L.backward_bounds(d, lens, 0.2, d["initial"], d["d_final"])
+    for got, w, b, t in zip(g + [df], want, bounds, (BF16, BF16, BF16, F32)):
+        assert L.worst(got, w, b, rounding(t)) <= 1
 
 
 def test_backward_decay_limits():
