@@ -27,6 +27,14 @@
 //   - of 32 rows of q or scores, the first 16-row tile takes 0 .. 3, 8 .. 11,
 //     .., the second the others.
 //
+// What bounds it: a chunk of a 128 x 128 head moves 64 KB and keeps a SIMD's
+// matrix core busy for 2400 cycles.  65536 tokens of 16 heads: the walk 230 us
+// (1.07 GB at 4.7 TB/s, a copy's 5.1 being the most), the pass for segments'
+// states 131 us (0.52 GB at 4.0 TB/s): memory.  32 ragged prompts of 128 heads
+// that share q and k by 16: 538 us, of which rows alone would take 415 and the
+// arithmetic alone 370: products, LDS and memory overlap only in part with two
+// workgroups a compute unit.
+//
 // Rounding: scores and the state are rounded to bf16 once as operands of the
 // output, which is bf16 itself.  The weighted v of the state update is split
 // into three bf16 parts that carry its 24 bits where the state is returned in
@@ -745,7 +753,7 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     // compute unit's LDS; where sequences are short, and their states most of the
     // traffic, three with 64 channels and chunks of 32 tokens move them faster (20
     // sequences of 27 tokens in the mean, backward: 82 -> 62 us; packed documents
-    // of 1700: 413 -> 508).
+    // of 1700: 390 -> 508).
     h.vt = vd <= 64 || (h.kd == 256 && mean <= 256) ? 64 : 128;
     h.heads = h.vt == 64 && h.kd < 256 && share % 2 == 0 && nops == 1 ? 2 : 1;
     const int64_t kAtOnce = h.kd < 256 ? 512 : h.vt == 64 ? 768 : 256;
