@@ -14,8 +14,9 @@
 // state registers are, as they are, the operand of the next product.
 //
 // LDS is what a wavefront of 16 channels is bound by (32 ragged prompts of 128
-// heads: 65% of the cycles, and half as many again lost to conflicts), since
-// all of them read all of q and k; 32 channels (DT 2) halve that.  The orders
+// heads: active 64% of a compute unit's cycles, 42% of those in conflicts), since
+// all of them read all of q and k; 32 channels (DT 2) and the orders below bring
+// that to 38%, 24% of those in conflicts.  The orders
 // below let every large read touch each bank once:
 //   - rows lie unit by unit (16 bytes, 8 channels), units 16 banks apart;
 //   - operands along tokens come from the transposing read, 4 rows of 4 half
@@ -27,13 +28,13 @@
 //   - of 32 rows of q or scores, the first 16-row tile takes 0 .. 3, 8 .. 11,
 //     .., the second the others.
 //
-// What bounds it: a chunk of a 128 x 128 head moves 64 KB and keeps a SIMD's
-// matrix core busy for 2400 cycles.  65536 tokens of 16 heads: the walk 230 us
-// (1.07 GB at 4.7 TB/s, a copy's 5.1 being the most), the pass for segments'
-// states 131 us (0.52 GB at 4.0 TB/s): memory.  32 ragged prompts of 128 heads
-// that share q and k by 16: 538 us, of which rows alone would take 415 and the
-// arithmetic alone 370: products, LDS and memory overlap only in part with two
-// workgroups a compute unit.
+// What bounds it: 65536 tokens of 16 heads of 128 x 128: the walk 244 us (1.07 GB
+// at 4.4 TB/s, a copy's being 5.1), the pass for segments' states 140 us (0.54
+// GB at 3.8 TB/s): memory; the call takes 393 us, 368 with most products left
+// out and 250 with no rows moved after the first.  32 ragged prompts of 128 heads
+// that share q and k by 16: 553 us, 431 with most products left out, 355 with no
+// rows moved: with two workgroups a compute unit the two overlap only in part
+// (matrix cores busy 34% of the cycles, LDS 38%).
 //
 // Rounding: scores and the state are rounded to bf16 once as operands of the
 // output, which is bf16 itself.  The weighted v of the state update is split
@@ -150,8 +151,8 @@ __device__ __forceinline__ Segment find_segment(const Params &p, int w, int seg)
     Segment g;
     if (p.batch <= 64) {
         // Longest sequences first, since what starts last must not be long (32
-        // ragged prompts of 128 heads, 18 to 7975 tokens, the last of 5032: 606 ->
-        // 533 us).  Lane b holds sequence b and counts the segments ahead of its own.
+        // ragged prompts of 128 heads, 18 to 7975 tokens, the last of 5032: 620 ->
+        // 553 us).  Lane b holds sequence b and counts the segments ahead of its own.
         int begin = 0, len = -1, count = 0, first = 0;
         if (lane < p.batch) {
             begin = clamp_row(p, p.qsl[lane]);
@@ -737,11 +738,11 @@ hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
 // with wide keys).  Sequences are cut into segments of as many tokens as let their
 // number, T / seg and half a segment for each sequence's end, fill the card
 // once; cut sequences cost a pass over their k and v for the segments' states,
-// so more of them only cost (65536 tokens of 16 heads: 32 segments 388 us, 48
-// 418, 64 440).  Where the sequences alone fill it, only those of more than
+// so more of them only cost (65536 tokens of 16 heads: kAtOnce 512 393 us, 768
+// 439, 1024 425).  Where the sequences alone fill it, only those of more than
 // twice a workgroup's share of the tokens are cut, which would end alone (32
-// ragged prompts of 128 heads, longest 7975 tokens: 533 us, cut at half of that
-// 575, at a quarter 696).
+// ragged prompts of 128 heads, longest 7975 tokens: 553 us, from one share on
+// 588, from half a share 705).
 // A segment shorter than the mean sequence is made to divide it.
 Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, int nops, int nlocal) {
     constexpr int64_t kLeast = 128;
@@ -752,8 +753,8 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     // Wide keys: one workgroup of 8 wavefronts and 128 value channels fills a
     // compute unit's LDS; where sequences are short, and their states most of the
     // traffic, three with 64 channels and chunks of 32 tokens move them faster (20
-    // sequences of 27 tokens in the mean, backward: 82 -> 62 us; packed documents
-    // of 1700: 390 -> 508).
+    // sequences of 27 tokens in the mean, backward: 83 -> 65 us; packed documents
+    // of 1700: 394 -> 512).
     h.vt = vd <= 64 || (h.kd == 256 && mean <= 256) ? 64 : 128;
     h.heads = h.vt == 64 && h.kd < 256 && share % 2 == 0 && nops == 1 ? 2 : 1;
     const int64_t kAtOnce = h.kd < 256 ? 512 : h.vt == 64 ? 768 : 256;

@@ -3,9 +3,9 @@
 // each (4 elements in fp32, 8 in bf16), so every state access of a wavefront is
 // one run of memory; a thread takes several rows so that enough of them are in
 // flight.  Both directions are bound by HBM: 4 (or 2) + 1 bytes an element.
-// 268 MB of fp32 state to int8: 80 us (4.2 TB/s); back: 54 us (6.2 TB/s, the
-// codes partly from the cache); 1.07 GB from e4m3: 256 us (5.3 TB/s).  Eight
-// elements a lane instead of 16 bytes: 77 us back; 8 rows a thread to int8: 102.
+// 268 MB of fp32 state to int8: 87 us (3.9 TB/s); back: 56 us (6.0 TB/s, over a
+// large copy's 5.1); 1.07 GB from e4m3: 257 us (5.2 TB/s).  Lanes of 8 elements of
+// fp32 and 4 rows a thread: 88 us, and 77 back; 16 rows a thread to int8: 103.
 #include "ssd_common.hpp"
 #include "ssd_linear_attn.hpp"
 
