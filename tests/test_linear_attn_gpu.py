@@ -88,6 +88,15 @@ def test_prompt_more_sequences_than_lanes(n, extra):
     check_prompt(lens, 2, 2, 8, 8, 510 + n, init="half")
 
 
+@pytest.mark.parametrize("n", [64, 65])
+def test_cut_sequences_among_as_many_as_lanes(n):
+    """Up to 64 sequences only the parts of cut ones are numbered; beyond, all are."""
+    lens = [b % 4 for b in range(n)]
+    lens[0], lens[31], lens[n - 1] = 1500, 2049, 1024
+    check_prompt(lens, 2, 2, 64, 64, 520, init="half", tail=2)
+    check_backward(lens, 2, 1, 64, 64, 521, tail=2)
+
+
 @pytest.mark.parametrize("lens", [[3000], [1700, 5, 900, 2100], [64 * 40], [64 * 40 + 1, 64 * 40 - 1]])
 def test_prompt_long(lens):
     check_prompt(lens, 2, 1, 64, 128, 600, init="half", tail=5)
