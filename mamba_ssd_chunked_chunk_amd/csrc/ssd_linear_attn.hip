@@ -797,6 +797,10 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     h.slots = cut ? (int)(T / seg) + batch : batch;
     h.sub_slots = cut ? (int)(T / sub) + batch : 0;
     h.bytes = (size_t)nops * h.sub_slots * H * h.tiles * h.vt * h.kd * sizeof(float);
+    // (in whole runs of the workgroups that share rows, on 8 XCDs)
+    const int64_t each = (int64_t)(H / h.heads) * h.tiles * nops, run = (int64_t)8 * (share / h.heads) * h.tiles * nops;
+    const int64_t blocks = (std::max(h.slots, h.sub_slots) * each + run - 1) / run * run;
+    h.threads = std::max(blocks * (h.kd == 256 && h.vt == 128 ? 512 : 256), cut ? (int64_t)batch * H * 256 : 0);
     return h;
 }
 

@@ -72,6 +72,7 @@ struct Shape {
     int heads;          // heads of a workgroup
     int seg, slots, sub, sub_slots;
     size_t bytes;       // of `parts`
+    int64_t threads;    // of its largest grid, which 32 bits have to hold
 };
 // vds: the value channels of its nops operations, of which the first nlocal have segments' states of their own
 Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, int nops, int nlocal);
@@ -107,6 +108,8 @@ struct CacheParams {
     int count, N;
     uint32_t max_slots, max_entries;
 };
+// threads of the larger of the two launches, which 32 bits have to hold
+int64_t state_cache_threads(const CacheParams &c, bool bf16);
 hipError_t launch_state_quantize(const CacheParams &c, const void *pool, bool bf16, bool e4m3, void *codes,
                                  float *scales, hipStream_t s);
 hipError_t launch_state_dequantize(const CacheParams &c, void *pool, bool bf16, bool e4m3, const void *codes,

@@ -3,6 +3,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "ssd.h"
 #include "ssd_linear_attn.hpp"
 
@@ -26,7 +28,7 @@ ssd_status check(const ssd_linear_attn_problem *p) {
         return SSD_ERR_BAD_SHAPE;
     if (p->state_dtype != SSD_STATE_F32 && p->state_dtype != SSD_STATE_BF16) return SSD_ERR_UNSUPPORTED;
     if (!dim_ok(p->key_dim) || !dim_ok(p->value_dim)) return SSD_ERR_UNSUPPORTED;
-    // the kernels' grids: up to 4 blocks of channels, 3 recurrences, 8 blocks of 256 threads per head of states
+    // numbers of workgroups are ints (up to 4 blocks of channels, 3 recurrences); threads are counted with the layout
     if (((int64_t)p->batch + p->total_len / 256) * p->nheads > INT32_MAX / 64) return SSD_ERR_UNSUPPORTED;
     if (!isfinite(p->scale)) return SSD_ERR_UNSUPPORTED;
     const int64_t qk = (int64_t)p->ngroups * p->key_dim, vv = (int64_t)p->nheads * p->value_dim;
@@ -47,6 +49,7 @@ struct Layout {
     ssd::la::Shape shape;
     bool shared;
     size_t dq, dk, bytes;  // the segments' states come first
+    int64_t threads;       // of the largest launch
 };
 Layout layout_of(const ssd_linear_attn_problem *p, bool backward) {
     Layout L = {};
@@ -60,8 +63,10 @@ Layout layout_of(const ssd_linear_attn_problem *p, bool backward) {
     else
         L.shape = ssd::la::shape_of(p->total_len, p->batch, p->nheads, share, K, o, 1, 1);
     L.bytes = align_up(L.shape.bytes);
+    L.threads = L.shape.threads;
     L.shared = backward && p->nheads != p->ngroups;
     if (L.shared) {
+        L.threads = std::max(L.threads, p->total_len * p->ngroups * (p->key_dim / 8) + 255);
         const size_t n = align_up((size_t)p->total_len * p->nheads * p->key_dim * sizeof(float));
         L.dq = L.bytes;
         L.dk = L.dq + n;
@@ -110,6 +115,7 @@ ssd_status forward(const ssd_linear_attn_problem *p, void *o, const void *q, con
         !aligned(state_out, 16) || !aligned(log_decay, 4) || !aligned(qsl, 4) || !aligned(cache_idx, 4))
         return SSD_ERR_MISALIGNED;
     const Layout L = layout_of(p, false);
+    if (L.threads > UINT32_MAX) return SSD_ERR_UNSUPPORTED;
     const ssd_status sw = check_workspace(L, ws, ws_bytes);
     if (sw != SSD_OK) return sw;
 
@@ -135,6 +141,11 @@ ssd_status forward(const ssd_linear_attn_problem *p, void *o, const void *q, con
     return ssd::la::launch_walk(a, L.shape, 1, static_cast<hipStream_t>(stream)) == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
+ssd::CacheParams cache_params(const ssd_state_cache_problem *p, const uint32_t *pool_idx, const uint32_t *entry_idx) {
+    return ssd::CacheParams{pool_idx, entry_idx, (int64_t)p->nheads * p->head_dim, p->count, p->dstate,
+                            (uint32_t)p->max_slots, (uint32_t)p->max_entries};
+}
+
 ssd_status check_cache(const ssd_state_cache_problem *p, const void *codes, const void *scales, const void *pool,
                        const void *pool_idx, const void *entry_idx) {
     if (p == nullptr) return SSD_ERR_NULL_ARG;
@@ -143,8 +154,9 @@ ssd_status check_cache(const ssd_state_cache_problem *p, const void *codes, cons
     if (p->state_dtype != SSD_STATE_F32 && p->state_dtype != SSD_STATE_BF16) return SSD_ERR_UNSUPPORTED;
     if (p->code_format != SSD_CODE_I8 && p->code_format != SSD_CODE_E4M3) return SSD_ERR_UNSUPPORTED;
     if (p->dstate > SSD_MAX_DSTATE || p->dstate % 8 != 0) return SSD_ERR_UNSUPPORTED;
-    // a block holds at least 16 rows, and the grid has fewer than 2^31 blocks
-    if (((int64_t)p->nheads * p->head_dim + 15) / 16 > INT32_MAX / (p->count > 0 ? p->count : 1))
+    // blocks and threads of the launches (a block holds at least 16 rows)
+    if (((int64_t)p->nheads * p->head_dim + 15) / 16 > INT32_MAX / (p->count > 0 ? p->count : 1) ||
+        ssd::state_cache_threads(cache_params(p, nullptr, nullptr), p->state_dtype == SSD_STATE_BF16) > UINT32_MAX)
         return SSD_ERR_UNSUPPORTED;
     if (p->count > 0 && (codes == nullptr || scales == nullptr || pool == nullptr || pool_idx == nullptr ||
                          entry_idx == nullptr))
@@ -155,11 +167,6 @@ ssd_status check_cache(const ssd_state_cache_problem *p, const void *codes, cons
     return SSD_OK;
 }
 
-ssd::CacheParams cache_params(const ssd_state_cache_problem *p, const uint32_t *pool_idx, const uint32_t *entry_idx) {
-    return ssd::CacheParams{pool_idx, entry_idx, (int64_t)p->nheads * p->head_dim, p->count, p->dstate,
-                            (uint32_t)p->max_slots, (uint32_t)p->max_entries};
-}
-
 }  // namespace
 
 extern "C" {
@@ -168,7 +175,9 @@ ssd_status ssd_linear_attn_workspace_size(const ssd_linear_attn_problem *prob, i
     if (bytes == nullptr) return SSD_ERR_NULL_ARG;
     const ssd_status st = check(prob);
     if (st != SSD_OK) return st;
-    *bytes = layout_of(prob, backward != 0).bytes;
+    const Layout L = layout_of(prob, backward != 0);
+    if (L.threads > UINT32_MAX) return SSD_ERR_UNSUPPORTED;
+    *bytes = L.bytes;
     return SSD_OK;
 }
 
@@ -204,6 +213,7 @@ ssd_status ssd_linear_attn_varlen_bwd(
         !aligned(d_final, 16) || !aligned(log_decay, 4) || !aligned(query_start_loc, 4))
         return SSD_ERR_MISALIGNED;
     const Layout L = layout_of(prob, true);
+    if (L.threads > UINT32_MAX) return SSD_ERR_UNSUPPORTED;
     const ssd_status sw = check_workspace(L, workspace, workspace_bytes);
     if (sw != SSD_OK) return sw;
 
@@ -280,6 +290,7 @@ ssd_status ssd_linear_attn_step_inplace(
     const ssd_status st = check(prob);
     if (st != SSD_OK) return st;
     if (prob->total_len != prob->batch) return SSD_ERR_BAD_SHAPE;
+    if ((int64_t)prob->batch * prob->nheads > UINT32_MAX / 256) return SSD_ERR_UNSUPPORTED;  // 256 threads each
     if (o == nullptr || q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || pool == nullptr ||
         cache_indices == nullptr)
         return SSD_ERR_NULL_ARG;

@@ -6,6 +6,8 @@
 // 268 MB of fp32 state to int8: 87 us (3.9 TB/s); back: 56 us (6.0 TB/s, over a
 // large copy's 5.1); 1.07 GB from e4m3: 257 us (5.2 TB/s).  Lanes of 8 elements of
 // fp32 and 4 rows a thread: 88 us, and 77 back; 16 rows a thread to int8: 103.
+#include <algorithm>
+
 #include "ssd_common.hpp"
 #include "ssd_linear_attn.hpp"
 
@@ -211,12 +213,19 @@ __global__ __launch_bounds__(kThreads) void state_dequantize(CacheParams p, void
     }
 }
 
+int lanes_of(const CacheParams &p, bool bf16) {
+    const int need = p.N / (bf16 ? 8 : 4);
+    return need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
+}
+int64_t blocks_per_pair(const CacheParams &p, int lanes, int thread_rows) {
+    const int64_t rows = kThreads / lanes * thread_rows;
+    return (p.rows_per_slot + rows - 1) / rows;
+}
+
 template <typename F>
 hipError_t by_lanes(const CacheParams &p, int thread_rows, bool bf16, bool e4m3, F f) {
-    const int need = p.N / (bf16 ? 8 : 4);
-    const int lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
-    const int64_t rows = kThreads / lanes * thread_rows;
-    const int64_t bpp = (p.rows_per_slot + rows - 1) / rows;
+    const int lanes = lanes_of(p, bf16);
+    const int64_t bpp = blocks_per_pair(p, lanes, thread_rows);
     const dim3 grid((unsigned)(bpp * p.count));
     auto pick = [&](auto l) {
         constexpr int L = decltype(l)::value;
@@ -239,6 +248,10 @@ hipError_t by_lanes(const CacheParams &p, int thread_rows, bool bf16, bool e4m3,
     return hipGetLastError();
 }
 }  // namespace
+
+int64_t state_cache_threads(const CacheParams &c, bool bf16) {
+    return blocks_per_pair(c, lanes_of(c, bf16), std::min(kRowsIn, kRowsOut)) * c.count * kThreads;
+}
 
 hipError_t launch_state_quantize(const CacheParams &c, const void *pool, bool bf16, bool e4m3, void *codes,
                                  float *scales, hipStream_t s) {

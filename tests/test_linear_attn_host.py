@@ -55,6 +55,40 @@ def test_problems_accepted(lib, kw):
     assert binding.ssd_linear_attn_workspace_size(prob(**kw), backward=True) >= 0
 
 
+def test_more_threads_than_a_launch_holds(lib):
+    """A grid's threads fit 32 bits (256 or 512 a workgroup): refused on the host beyond, workspace or not."""
+    n = ctypes.c_size_t(0)
+    V = [ctypes.c_void_p(BASE)] * 13
+
+    def size(p, backward=0):
+        return lib.ssd_linear_attn_workspace_size(ctypes.byref(p), backward, ctypes.byref(n))
+
+    few = dict(nheads=16, ngroups=16, key_dim=8, value_dim=8)
+    ok, bad = (prob(total_len=b, batch=b, **few) for b in ((1 << 19), (1 << 20)))
+    assert size(ok) == 0
+    assert size(bad) == UNSUPPORTED and size(bad, 1) == UNSUPPORTED
+    assert lib.ssd_linear_attn_varlen_fwd_inplace(ctypes.byref(bad), *V[:10], 1 << 60, None) == UNSUPPORTED
+    assert lib.ssd_linear_attn_varlen_fwd(ctypes.byref(bad), *V[:9], 1 << 60, None) == UNSUPPORTED
+    assert lib.ssd_linear_attn_varlen_bwd(ctypes.byref(bad), *V[:13], 1 << 60, None) == UNSUPPORTED
+    assert lib.ssd_linear_attn_step_inplace(ctypes.byref(bad), *V[:8], None) == UNSUPPORTED
+    # 512 threads, and four blocks of channels, of the widest heads
+    wide = dict(nheads=16, ngroups=16, key_dim=256, value_dim=256)
+    assert size(prob(total_len=257 << 19, batch=1 << 19, **wide)) == UNSUPPORTED
+    # the sums of shared heads: one thread for 8 channels of dq
+    long = dict(total_len=(1 << 31) - 1, batch=1, nheads=2, ngroups=1, value_dim=64)
+    assert size(prob(key_dim=8, **long), 1) == 0
+    assert size(prob(key_dim=16, **long), 1) == UNSUPPORTED and size(prob(key_dim=16, **long)) == 0
+
+
+def test_more_threads_than_a_state_cache_launch_holds(lib):
+    a = [ctypes.c_void_p(BASE)] * 5
+    for kw in (dict(count=1 << 18, nheads=1 << 4, head_dim=64, dstate=256),
+               dict(count=1 << 18, nheads=1 << 8, head_dim=64, dstate=8)):
+        p = cache(max_slots=1 << 30, max_entries=1 << 30, **kw)
+        assert lib.ssd_state_quantize(ctypes.byref(p), *a, None) == UNSUPPORTED
+        assert lib.ssd_state_dequantize(ctypes.byref(p), *a, None) == UNSUPPORTED
+
+
 def test_workspace_size_arguments(lib):
     n = ctypes.c_size_t(0)
     assert lib.ssd_linear_attn_workspace_size(None, 0, ctypes.byref(n)) == NULL
