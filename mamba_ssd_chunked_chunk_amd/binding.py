@@ -530,8 +530,9 @@ def _run(name, dev, stream, need, workspace, call):
     """The same for ``call(workspace address, bytes, stream)``.  A workspace that the caller does not give is
     allocated on the call's stream.  Returns the workspace (None where none was given and none is needed)."""
     if workspace is not None:
-        if workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev:
-            raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+        if (workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev
+                or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on {dev}")
     elif need:
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)

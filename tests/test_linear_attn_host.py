@@ -193,6 +193,21 @@ def test_cache_pointer_refusals(lib):
     assert lib.ssd_state_dequantize(ctypes.byref(cache(count=0)), *[None] * 5, None) == 0
 
 
+def test_workspaces_refused_by_the_binding():
+    """A workspace has to hold its bytes itself: an expanded byte has their number, not their memory."""
+    torch = pytest.importorskip("torch")
+    binding._import_torch()
+    cpu, byte = torch.device("cpu"), torch.zeros(1, dtype=torch.uint8)
+
+    def call(*_):
+        raise AssertionError("launched")
+
+    for bad in (byte.expand(512), byte.expand(512).view(8, 64), torch.zeros(1024, dtype=torch.uint8)[::2],
+                torch.zeros(256, dtype=torch.uint8), torch.zeros(512, dtype=torch.int8)):
+        with pytest.raises(ValueError, match="workspace"):
+            binding._run("x", cpu, None, 512, bad, call)
+
+
 def test_binding_refusals():
     torch = pytest.importorskip("torch")
     bf = torch.bfloat16
