@@ -440,6 +440,7 @@ ssd_status ssd_linear_attn_varlen_fwd(
  *   d_o               IN   bf16 [T,H,V] (dense)
  *   d_final           IN   state_dtype [batch,H,V,K], or NULL (zero); may be
  *                     the same buffer as d_initial
+ * d_initial may not be the buffer of initial_states (SSD_ERR_UNSUPPORTED).
  * log_decay gets no gradient.                                             */
 ssd_status ssd_linear_attn_varlen_bwd(
     const ssd_linear_attn_problem *prob, void *dq, void *dk, void *dv, void *d_initial,

@@ -216,6 +216,8 @@ ssd_status ssd_linear_attn_varlen_bwd(
     if (L.threads > UINT32_MAX) return SSD_ERR_UNSUPPORTED;
     const ssd_status sw = check_workspace(L, workspace, workspace_bytes);
     if (sw != SSD_OK) return sw;
+    // dq reads initial_states in the launch in which dv writes d_initial
+    if (d_initial != nullptr && d_initial == initial_states) return SSD_ERR_UNSUPPORTED;
 
     const ssd_linear_attn_problem *p = prob;
     hipStream_t s = static_cast<hipStream_t>(stream);

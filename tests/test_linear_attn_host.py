@@ -131,6 +131,13 @@ def test_backward_refusals(lib):
     assert lib.ssd_linear_attn_varlen_bwd(None, *[ctypes.c_void_p(BASE)] * 13, 0, None) == NULL
 
 
+def test_backward_refuses_states_it_would_overwrite(lib):
+    """dq reads initial_states in the launch in which dv writes d_initial."""
+    a = [ctypes.c_void_p(BASE + i * 4096) for i in range(13)]
+    a[3] = a[9]  # d_initial, initial_states
+    assert lib.ssd_linear_attn_varlen_bwd(ctypes.byref(prob()), *a, 1 << 40, None) == UNSUPPORTED
+
+
 def test_step_refusals(lib):
     p = prob(total_len=4)
     # o q k v log_decay pool has_init cache_idx
