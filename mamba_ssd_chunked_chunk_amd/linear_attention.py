@@ -9,6 +9,13 @@ import torch
 from . import binding
 
 
+def _aligned(g):
+    """A gradient as the library takes it: dense, from a 16-byte boundary on (autograd may hand over part of a
+    longer one)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _LinearAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_decay, query_start_loc, initial_states, scale, padded, state_dtype):
@@ -30,8 +37,8 @@ class _LinearAttention(torch.autograd.Function):
         q, k, v, log_decay, query_start_loc, initial = ctx.saved_tensors
         if d_o is None and d_final is None:
             return (None,) * 9
-        d_o = torch.zeros_like(v, memory_format=torch.contiguous_format) if d_o is None else d_o.contiguous()
-        d_final = None if d_final is None else d_final.contiguous()
+        d_o = torch.zeros_like(v, memory_format=torch.contiguous_format) if d_o is None else _aligned(d_o)
+        d_final = None if d_final is None else _aligned(d_final)
         dq, dk, dv = (ctx.new(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         batch = query_start_loc.numel() - 1
         d_initial = None

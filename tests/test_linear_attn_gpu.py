@@ -171,6 +171,29 @@ def test_slots_behind_2_31_elements():
                    * 2.0 ** -16, rounding(BF16)) <= 1
 
 
+def test_tokens_behind_2_31_elements():
+    """Rows whose offset passes 31 bits in q, k, v and o (4 GiB each; only the last ones are anybody's)."""
+    H, K, V, n, T = 1, 64, 64, 150, (1 << 25) + 200
+    d = L.draw([n], H, 1, K, V, 560, slots=1)
+    c = cuda(d)
+    first = T - n - 7
+    long = {}
+    for name in ("q", "k", "v"):
+        long[name] = torch.empty(T, 1, 64, dtype=BF16, device="cuda")
+        long[name][first:first + n] = c[name]
+    long["query_start_loc"] = torch.tensor([first, first + n], dtype=torch.int32, device="cuda")
+    outs = []
+    for src in (c, long):
+        pool, o = c["pool"].clone(), torch.full_like(src["v"], 7.0)
+        binding.ssd_linear_attn_varlen_fwd_inplace(o, src["q"], src["k"], src["v"], c["log_decay"], pool,
+                                                   src["query_start_loc"], None, c["cache_indices"])
+        outs.append((o, pool))
+    (o, pool), (far, far_pool) = outs
+    assert first * 64 > 2**31 - 1
+    assert torch.equal(far[first:first + n], o) and torch.equal(far_pool, pool)
+    assert bool((far[first + n:] == 7.0).all()) and bool((far[first - 1000:first] == 7.0).all())
+
+
 def test_no_rows_at_all():
     d = L.draw([0, 0], 2, 1, 64, 64, 810, slots=2)
     c = cuda(d)
@@ -528,6 +551,20 @@ def test_autograd_of_one_output(use):
     bounds = L.backward_bounds(e, lens, 0.2, None, df)
     for g, w, b in zip(grads, want, bounds):
         assert L.worst(g, w, b, rounding(BF16)) <= 1
+
+
+def test_autograd_of_gradients_that_start_anywhere():
+    """A gradient that reaches the function as a view of a longer one: dense, but on no 16-byte boundary."""
+    from mamba_ssd_chunked_chunk_amd.linear_attention import linear_attention
+    lens = [70, 33]
+    c = cuda(L.draw(lens, 2, 2, 64, 64, 1640))
+    x = [c[n].clone().requires_grad_() for n in ("q", "k", "v", "initial")]
+    outs = linear_attention(*x[:3], c["log_decay"], c["query_start_loc"], x[3])
+    given = [c["d_o"], c["d_final"]]
+    want = torch.autograd.grad(outs, x, given, retain_graph=True)
+    moved = [torch.cat([g.new_zeros(3), g.flatten()])[3:].view(g.shape) for g in given]
+    assert all(g.is_contiguous() and g.data_ptr() % 16 != 0 for g in moved)
+    assert all(torch.equal(a, b) for a, b in zip(want, torch.autograd.grad(outs, x, moved)))
 
 
 def test_autograd_refuses_a_learned_decay():
