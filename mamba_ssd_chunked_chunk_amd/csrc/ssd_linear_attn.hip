@@ -28,11 +28,11 @@
 //   - of 32 rows of q or scores, the first 16-row tile takes 0 .. 3, 8 .. 11,
 //     .., the second the others.
 //
-// What bounds it: 65536 tokens of 16 heads of 128 x 128: the walk 244 us (1.07 GB
-// at 4.4 TB/s, a copy's being 5.1), the pass for segments' states 140 us (0.54
-// GB at 3.8 TB/s): memory; the call takes 393 us, 368 with most products left
-// out and 250 with no rows moved after the first.  32 ragged prompts of 128 heads
-// that share q and k by 16: 553 us, 431 with most products left out, 355 with no
+// What bounds it: 65536 tokens of 16 heads of 128 x 128: the walk 236 us (1.07 GB
+// at 4.5 TB/s, a copy's being 5.1), the pass for segments' states 132 us (0.54
+// GB at 4.1 TB/s): memory; the call takes 392 us, 370 with most products left
+// out and 241 with no rows moved after the first.  32 ragged prompts of 128 heads
+// that share q and k by 16: 527 us, 402 with most products left out, 328 with no
 // rows moved: with two workgroups a compute unit the two overlap only in part
 // (matrix cores busy 34% of the cycles, LDS 38%).
 //
@@ -156,8 +156,8 @@ __device__ __forceinline__ Segment find_segment(const Params &p, int w, int seg)
     Segment g;
     if (p.batch <= 64) {
         // Longest sequences first, since what starts last must not be long (32
-        // ragged prompts of 128 heads, 18 to 7975 tokens, the last of 5032: 620 ->
-        // 553 us).  Lane b holds sequence b and counts the segments ahead of its own.
+        // ragged prompts of 128 heads, 18 to 7975 tokens, the last of 5032: 601 ->
+        // 531 us).  Lane b holds sequence b and counts the segments ahead of its own.
         int begin = 0, len = -1, count = 0, first = 0;
         if (lane < p.batch) {
             begin = clamp_row(p, p.qsl[lane]);
@@ -747,11 +747,11 @@ hipError_t launch_any(const Params &p, const Shape &h, hipStream_t s) {
 // with wide keys).  Sequences are cut into segments of as many tokens as let their
 // number, T / seg and half a segment for each sequence's end, fill the card
 // once; cut sequences cost a pass over their k and v for the segments' states,
-// so more of them only cost (65536 tokens of 16 heads: kAtOnce 512 393 us, 768
-// 439, 1024 425).  Where the sequences alone fill it, only those of more than
+// so more of them only cost (65536 tokens of 16 heads: kAtOnce 512 391 us, 768
+// 424, 1024 421).  Where the sequences alone fill it, only those of more than
 // twice a workgroup's share of the tokens are cut, which would end alone (32
-// ragged prompts of 128 heads, longest 7975 tokens: 553 us, from one share on
-// 588, from half a share 705).
+// ragged prompts of 128 heads, longest 7975 tokens: 531 us, from one share on
+// 547, from half a share 667).
 // A segment shorter than the mean sequence is made to divide it.
 Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, int nops, int nlocal) {
     constexpr int64_t kLeast = 128;
@@ -762,8 +762,8 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     // Wide keys: one workgroup of 8 wavefronts and 128 value channels fills a
     // compute unit's LDS; where sequences are short, and their states most of the
     // traffic, three with 64 channels and chunks of 32 tokens move them faster (20
-    // sequences of 27 tokens in the mean, backward: 83 -> 65 us; packed documents
-    // of 1700: 394 -> 512).
+    // sequences of 27 tokens in the mean, backward: 76 -> 59 us; packed documents
+    // of 1700: 387 -> 503).
     h.vt = vd <= 64 || (h.kd == 256 && mean <= 256) ? 64 : 128;
     h.heads = h.vt == 64 && h.kd < 256 && share % 2 == 0 && nops == 1 ? 2 : 1;
     const int64_t kAtOnce = h.kd < 256 ? 512 : h.vt == 64 ? 768 : 256;

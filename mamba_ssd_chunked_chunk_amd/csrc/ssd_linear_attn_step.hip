@@ -3,9 +3,9 @@
 // Each thread holds 8 consecutive key channels of kRows rows of the state
 // (16-byte loads and stores; the lanes of a row cover it contiguously), so
 // the state is read once and written once.  That is the bound: 8 K V bytes a
-// head in fp32 against 4 K V flop (512 tokens of 128 heads of 64 x 128: 841 us,
+// head in fp32 against 4 K V flop (512 tokens of 128 heads of 64 x 128: 845 us,
 // 5.1 TB/s, as fast as a copy).  A block takes at most 64 rows of a 128-channel
-// state, so that a single token of 16 heads still spreads over 32 of them (4.7
+// state, so that a single token of 16 heads still spreads over 32 of them (4.4
 // us).
 #include "ssd_linear_attn.hpp"
 

@@ -4,7 +4,7 @@
 // one run of memory; a thread takes several rows so that enough of them are in
 // flight.  Both directions are bound by HBM: 4 (or 2) + 1 bytes an element.
 // 268 MB of fp32 state to int8: 87 us (3.9 TB/s); back: 56 us (6.0 TB/s, over a
-// large copy's 5.1); 1.07 GB from e4m3: 257 us (5.2 TB/s).  Lanes of 8 elements of
+// large copy's 5.1); 1.07 GB from e4m3: 258 us (5.2 TB/s; medians).  Lanes of 8 elements of
 // fp32 and 4 rows a thread: 88 us, and 77 back; 16 rows a thread to int8: 103.
 #include <algorithm>
 
