@@ -379,8 +379,13 @@ ssd_status ssd_validate_inputs(const ssd_problem *prob, const int32_t *query_sta
  *   - q, k and v may have a stride between tokens (slices of one projection);
  *     everything else is dense.
  * log_decay is a constant of the layer, normally negative; 0 is a plain sum
- * and -infinity forgets everything but the token itself.  Activations are
- * bf16; the states, all sums and the chain between chunks are fp32.
+ * and -infinity forgets everything but the token itself.  Above 0 the states
+ * grow, and the powers of lambda that the sums above apply have to be finite in
+ * fp32: up to lambda^(n-1) for the n tokens of a sequence, lambda^n where it
+ * starts from a state (or, backward, has d_final or returns d_initial).  Beyond
+ * that a sequence's results of that head may be infinite or NaN, also where rows
+ * of zeros keep the exact sum finite.  Activations are bf16; the states, all
+ * sums and the chain between chunks are fp32.
  * Results are deterministic (bitwise run to run).  A NaN or infinity in one
  * token reaches every later token of its sequence and head, and may reach
  * the earlier ones of the same 64-token chunk; never another sequence.     */

@@ -301,8 +301,10 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int d = 0; d < DT; ++d) S[t][0][d] = S[t][1][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bool zero = true;  // no state enters the first chunk
     if constexpr (!LOCAL) {
         if (g.count > 1) {
+            zero = false;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -310,6 +312,7 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) S[t][y][d] = part[((d * NT + t) * 2 + y) * 64];
         } else if (resumes(p, op, g.b)) {
+            zero = false;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -330,11 +333,13 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
     // chunk's, and starts with rows of zeros.
     // In LDS: weights of the scores by distance i - j (0 above the diagonal),
     // from distance -31 on, and of the tokens in the state update, last first.
+    // Both stop at the segment's tokens: where lambda > 1 a power of the padded
+    // rows may be infinite, and rows of zeros would make it NaN.
     if (tid < HP * 128) {
         const int i = tid & 127, d = i - 31;
         const float l2h = HP == 1 ? l2 : log2_decay(p, h0 + (tid >> 7));
-        if (i < CT + 31) s_pair[tid >> 7][i] = d >= 0 ? op.scale_pair * fast_exp2(l2h * (float)d) : 0.f;
-        if (i < CT) s_lead[tid >> 7][i] = op.scale_update * fast_exp2(l2h * ((float)i + shift));
+        if (i < CT + 31) s_pair[tid >> 7][i] = d >= 0 && d < n ? op.scale_pair * fast_exp2(l2h * (float)d) : 0.f;
+        if (i < CT) s_lead[tid >> 7][i] = i < n ? op.scale_update * fast_exp2(l2h * ((float)i + shift)) : 0.f;
     }
     const bool fine = !SB && op.state_out != nullptr;  // three parts of the weighted v, or two
 
@@ -453,6 +458,8 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
 #pragma unroll 1
     for (int c0 = 0; c0 < n; c0 += CT) {
         const int len = min(CT, n - c0), pad = CT - len;
+        // a state of zeros stays one, also where lambda^len is infinite
+        const float l2s = !LOCAL && zero && c0 == 0 ? -1e30f : l2;
         __syncthreads();  // A: the previous chunk's rows are read, its scores written
         // token i of the chunk to its place; tokens past it (zeros) wrap to the places before it
         const int ft = opaque(tid), ck = unit_of(ft, UK), rk = row_of(ft, UK), cv = unit_of(ft, UV),
@@ -535,14 +542,14 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const float x = scale_state * fast_exp2(l2 * ((float)(place0 + row_tile(rt) - pad + 1) - shift));
+                const float x = scale_state * fast_exp2(l2s * ((float)(place0 + row_tile(rt) - pad + 1) - shift));
 #pragma unroll
                 for (int d = 0; d < DT; ++d) O[rt][d] *= x;
             }
         }
 
         // ---- the state update, 32 tokens at a time
-        const float keep = fast_exp2(l2 * (float)len);
+        const float keep = fast_exp2(l2s * (float)len);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (NT > 4 && 32 * t >= kd) break;

@@ -438,6 +438,64 @@ def test_backward_against_differences():
         assert abs(got - want) <= 5 * 2 * L.BF16 * noise.item(), name
 
 
+def growth_error(log_decay, lens):
+    """What the weights lambda^n of a growing state add to the bounds, relative: their exponent n log2(lambda) takes
+    three roundings (log2 e, its product with log_decay, the product with n), so they are off by n log_decay 3 2^-24."""
+    return 3 * 2.0 ** -24 * max(float(log_decay.max()), 0.0) * max(lens)
+
+
+def check_growth(lens, log_decay, H, G, K, V, seed, init, dtype=F32):
+    d = L.draw(lens, H, G, K, V, seed, slots=len(lens))
+    d["log_decay"] = torch.tensor(log_decay)
+    scale, extra = K ** -0.5, growth_error(d["log_decay"], lens)
+    c = cuda(d)
+    o, pool, flags = prompt(d, c, scale, dtype, init)
+    slots = d["cache_indices"].long()
+    initial = d["pool"].to(dtype)[slots].float() * flags[:, None, None, None]
+    want, final = L.reference(d, lens, scale, initial)
+    bo, bf = L.forward_bounds(d, lens, scale, initial)
+    assert float(final.abs().max()) < torch.finfo(F32).max and float(want.abs().max()) < torch.finfo(BF16).max
+    assert L.worst(o, want, bo * (1 + extra / L.BF16), rounding(BF16)) <= 1
+    assert L.worst(pool.cpu()[slots], final, bf * (1 + extra / L.FP32), rounding(dtype)) <= 1
+
+
+# decays whose 63rd power passes fp32 (1.41 on), as far as the sequences' own powers do not
+GROWTH = [([10, 1, 0, 3], [2.0, 1.41, 8.0, 0.5], "all"), ([40, 7], [2.0, 1.0, 1.9, -1.0], "all"),
+          ([31, 32, 33], [2.4, 2.0, 1.5, 0.0], "half"), ([2], [60.0, 41.0, 2.0, 80.0], "none"),
+          ([1], [80.0, 44.0, 5.0, -5.0], "all"), ([63, 64], [1.2, 1.25, 1.3, 1.0], "half"),
+          ([100, 65], [0.7, 0.75, 0.8, 0.5], "all")]
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128), (128, 64), (256, 64), (200, 136)])
+@pytest.mark.parametrize("lens,log_decay,init", GROWTH)
+def test_growing_states(lens, log_decay, init, K, V):
+    """A short chunk's weights stop at its own tokens, and a state of zeros stays zero, whatever lambda^64 is."""
+    for G in (2, 4):
+        check_growth(lens, log_decay, 4, G, K, V, 850, init)
+    check_growth(lens, log_decay, 4, 2, K, V, 851, init, BF16)
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128), (200, 40)])
+@pytest.mark.parametrize("lens,log_decay,init", GROWTH)
+def test_backward_of_growing_states(lens, log_decay, init, K, V):
+    d = L.draw(lens, 4, 2, K, V, 860)
+    d["log_decay"] = torch.tensor(log_decay)
+    scale, extra = K ** -0.5, growth_error(d["log_decay"], lens)
+    c, states = cuda(d), init != "none"
+    grads = [torch.empty_like(c[n]) for n in "qkv"] + [torch.empty_like(c["initial"]) if states else None]
+    binding.ssd_linear_attn_varlen_bwd(*grads, c["q"], c["k"], c["v"], c["d_o"], c["log_decay"],
+                                       c["initial"] if states else None, c["d_final"] if states else None,
+                                       c["query_start_loc"], scale=scale)
+    i, f = (d["initial"], d["d_final"]) if states else (None, None)
+    want = L.gradients(d, lens, scale, i, f)
+    bounds = L.backward_bounds(d, lens, scale, i, f)
+    for name, got, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+        assert float(w.abs().max()) < torch.finfo(BF16).max
+        assert L.worst(got, w, b * (1 + extra / L.BF16), rounding(BF16)) <= 1, name
+    if states:
+        assert L.worst(grads[3], want[3], bounds[3] * (1 + extra / L.FP32), rounding(F32)) <= 1
+
+
 # ------------------------------------------------------------------ ways of calling
 
 def _all_calls(c, lens):
