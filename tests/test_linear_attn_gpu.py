@@ -496,6 +496,40 @@ def test_backward_of_growing_states(lens, log_decay, init, K, V):
         assert L.worst(grads[3], want[3], bounds[3] * (1 + extra / L.FP32), rounding(F32)) <= 1
 
 
+# ------------------------------------------------------------------ cut sequences, in every variant
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("K,V", [(256, 64), (200, 40), (256, 200), (128, 64), (64, 128)])
+def test_prompt_long_in_every_width(K, V, dtype):
+    """Cut sequences: the chunks of 32 tokens (wide keys, up to 64 value channels) and of 64, states of either type."""
+    check_prompt([1500, 5, 900], 2, 1, K, V, 620 + K + V, dtype=dtype, init="half", tail=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,G", [(2, 1), (3, 3)])
+@pytest.mark.parametrize("K,V", [(256, 72), (96, 200), (64, 64)])
+def test_backward_of_one_long_sequence_among_short_ones(K, V, H, G, dtype):
+    """Short in the mean, so that wide keys take chunks of 32 tokens and 4 blocks of channels, and one of them cut."""
+    lens = [(7 * b) % 41 for b in range(20)]
+    lens[13] = 1200
+    check_backward(lens, H, G, K, V, 1370 + K + V + H, dtype=dtype, tail=2)
+
+
+@pytest.mark.parametrize("lens", [[2500], [1500, 3, 900, 1800]])
+@pytest.mark.parametrize("K,V", [(64, 128), (136, 40)])
+def test_backward_long_of_bf16_states(lens, K, V):
+    check_backward(lens, 2, 1, K, V, 1380 + K, dtype=BF16)
+
+
+@pytest.mark.parametrize("n", [60, 64, 65, 90])
+def test_lengths_around_a_segment(n):
+    """Cut sequences side by side and apart, empty ones between, of lengths around the least segment (128 tokens)."""
+    at = torch.randint(0, 12, (n,), generator=torch.Generator().manual_seed(n))
+    lens = [[0, 1, 64, 100, 127, 128, 129, 130, 191, 256, 257, 390][int(i)] for i in at]
+    check_prompt(lens, 2, 2, 8, 8, 530 + n, init="half", tail=1)
+    check_backward(lens, 2, 1, 8, 8, 531 + n)
+
+
 # ------------------------------------------------------------------ ways of calling
 
 def _all_calls(c, lens):
