@@ -138,6 +138,38 @@ __device__ __forceinline__ bool resumes(const Params &p, const Op &op, int b) {
     return op.state_in != nullptr && (p.init_all != 0 || (p.has_init != nullptr && p.has_init[b] != 0));
 }
 
+// Only sequences of more than a segment are cut, and only those have states in
+// the workspace.  Ahead of a sequence that starts at row `begin` there are at most
+// begin / (seg + 1) of them (and at most b sequences at all): its number among
+// those that could be, which is less than p.cuts and another for each cut one.
+__device__ __forceinline__ int cut_number(const Params &p, int begin, int b) { return min(b, begin / (p.seg + 1)); }
+
+// The workspace's slot of a cut sequence's first part.  floor(begin / sub) grows by
+// at least its number of parts less one up to the next cut sequence and cut_number
+// by one, so their slots never meet; p.sub_slots holds them whatever the table says.
+__device__ __forceinline__ int first_slot(const Params &p, int begin, int b) {
+    return begin / p.sub + cut_number(p, begin, b);
+}
+
+// The last sequence b with number(b, its first row) <= w, or -1, for numbers that
+// never decrease: every lane tests one sequence at a time, a 64-ary search.
+template <typename F>
+__device__ __forceinline__ int last_up_to(const Params &p, int w, F number) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = p.batch;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int i = lane * step;
+        bool at = false;
+        if (i < n) at = number(lo + i, clamp_row(p, p.qsl[lo + i])) <= w;
+        const int k = __popcll(__ballot(at)) - 1;
+        if (k < 0) return -1;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // The segment a workgroup takes: sequences are cut into segments of `seg`
 // tokens (0: not cut), counted in walking order, and number w of the launch is
 // one of them or none.  LOCAL: a part, p.seg / seg of which make a segment; of up
@@ -183,32 +215,20 @@ __device__ __forceinline__ Segment find_segment(const Params &p, int w, int seg)
     }
     // Many sequences: in their order.  Sequence b's numbers start at qsl / seg +
     // b (a sequence of n tokens has at most n / seg + 1 segments, so they never
-    // meet the next one's; those in between are nobody's), and every lane tests
-    // one sequence at a time: a 64-ary search.
-    int lo = 0;
-    if (seg == 0) {
-        lo = w;
-    } else {
-        int n = p.batch;
-        while (n > 1) {
-            const int step = (n + 63) / 64;
-            const int i = lane * step;
-            bool at = false;
-            if (i < n) at = clamp_row(p, p.qsl[lo + i]) / seg + lo + i <= w;
-            const int k = __popcll(__ballot(at)) - 1;
-            if (k < 0) return none;
-            lo += k * step;
-            n = min(step, n - k * step);
-        }
-    }
-    g.b = __builtin_amdgcn_readfirstlane(lo);
+    // meet the next one's; those in between are nobody's), a cut one's parts at
+    // their slot.
+    auto number = [&](int b, int begin) { return LOCAL ? first_slot(p, begin, b) : begin / seg + b; };
+    const int b = seg == 0 ? w : last_up_to(p, w, number);
+    if (b < 0) return none;
+    g.b = __builtin_amdgcn_readfirstlane(b);
     g.begin = __builtin_amdgcn_readfirstlane(clamp_row(p, p.qsl[g.b]));
     g.len = max(__builtin_amdgcn_readfirstlane(clamp_row(p, p.qsl[g.b + 1])) - g.begin, 0);
     if (seg == 0) {
         g.index = 0;
         g.count = 1;
     } else {
-        g.index = w - (g.begin / seg + g.b);
+        if (LOCAL && g.len <= p.seg) return none;
+        g.index = w - number(g.b, g.begin);
         g.count = max((g.len + seg - 1) / seg, 1);
         if (g.index < 0 || g.index >= g.count) g.count = 0;
     }
@@ -293,7 +313,7 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
     const int64_t state_at = (slot * p.H + h) * p.state_size;
     // the wavefront's part of the slot of the segment's (first) states in the workspace
     const int64_t part_slot =
-        g.count > 1 ? g.begin / p.sub + g.b + (LOCAL ? g.index : (int64_t)g.index * (p.seg / p.sub)) : 0;
+        g.count > 1 ? first_slot(p, g.begin, g.b) + (LOCAL ? g.index : (int64_t)g.index * (p.seg / p.sub)) : 0;
     f32x4 *const part = reinterpret_cast<f32x4 *>(
         p.parts + ((((int64_t)which * p.sub_slots + part_slot) * p.H + h) * p.tiles * VT + v0 + 16 * tile0) * KD) + lane;
     f32x4 S[NT][2][DT];
@@ -629,8 +649,9 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
 }
 
 // The states of the segments' parts (of `sub` tokens) into the states that
-// enter the segments, in place of their first parts': a thread takes 4 state elements of a (sequence, head) at a time, in the order of
-// the walk's registers.  Sequences of one segment are left to the walk.  With
+// enter the segments, in place of their first parts': a block takes one head of the
+// cut sequence of number c, a thread 4 state elements at a time, in the order of the
+// walk's registers.  Sequences of one segment are left to the walk.  With
 // `mirror` the states are those of another operation too, transposed (its k
 // channels are this one's v channels and the reverse), and are written there
 // as well.
@@ -638,15 +659,34 @@ template <bool SB>
 __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
     constexpr int kAhead = 4;
     const int per_head = p.tiles * VT * KD / 4;  // groups of 4
-    const int h = blockIdx.x % p.H, b = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, c = blockIdx.x / p.H;
     const int which = blockIdx.y;
     const Op &op = p.op[which];
     if (op.twin != 0) return;
-    const int begin = clamp_row(p, p.qsl[b]), len = max(clamp_row(p, p.qsl[b + 1]) - begin, 0);
+    int b, begin, len;
+    if (p.batch <= 64) {  // one load: lane l looks at sequence l
+        const int lane = threadIdx.x & 63;
+        begin = len = 0;
+        if (lane < p.batch) {
+            begin = clamp_row(p, p.qsl[lane]);
+            len = clamp_row(p, p.qsl[lane + 1]) - begin;
+        }
+        const uint64_t at = __ballot(len > p.seg && cut_number(p, begin, lane) == c);
+        if (at == 0) return;
+        b = (int)__builtin_ctzll(at);
+        begin = __builtin_amdgcn_readlane(begin, b);
+        len = __builtin_amdgcn_readlane(len, b);
+    } else {
+        b = last_up_to(p, c, [&](int i, int first) { return cut_number(p, first, i); });
+        if (b < 0) return;
+        begin = clamp_row(p, p.qsl[b]);
+        len = clamp_row(p, p.qsl[b + 1]) - begin;
+        if (len <= p.seg || cut_number(p, begin, b) != c) return;
+    }
     const int count = (len + p.seg - 1) / p.seg, parts = p.seg / p.sub;  // segments, and parts of one
     const int last = (count - 1) * parts;
     const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[b] : (int64_t)b;
-    if (count <= 1 || slot >= p.max_slots) return;
+    if (slot >= p.max_slots) return;
     for (int i = blockIdx.z * 256 + (int)threadIdx.x; i < per_head; i += gridDim.z * 256) {
         const int lane = i & 63, y = (i >> 6) & 1, t = (i >> 7) % (KD / 32), tile = (i >> 7) / (KD / 32);
         const int vch = 32 * (tile >> 1) + column(lane & 15, tile & 1);
@@ -666,7 +706,7 @@ __global__ __launch_bounds__(256) void la_chain(Params p, int KD, int VT) {
         }
         const float keep = fast_exp2(log2_decay(p, h) * (float)p.sub);
         const int64_t step = (int64_t)p.H * per_head;
-        const int64_t head = (int64_t)(begin / p.sub + b) * step + (int64_t)h * per_head;
+        const int64_t head = first_slot(p, begin, b) * step + (int64_t)h * per_head;
         f32x4 *part = reinterpret_cast<f32x4 *>(p.parts) + (int64_t)which * p.sub_slots * step + head + i;
         // (v channel kc, k channel vch) of the mirror: element vch % 4 of the group of its
         // lane (a backward launch holds as many v channels as k channels)
@@ -724,9 +764,9 @@ hipError_t launch_variant(const Params &p, hipStream_t s) {
     auto grid = [&](int slots) { return dim3((unsigned)((slots * each + run - 1) / run * run)); };
     const dim3 block(64 * NW);
     if (p.seg != 0) {
-        la_walk<KD, CT, NW, DT, HP, SB, true><<<grid(p.batch <= 64 ? p.sub_slots - p.batch : p.sub_slots), block, 0, s>>>(p);
+        la_walk<KD, CT, NW, DT, HP, SB, true><<<grid(p.batch <= 64 ? p.sub_slots - p.cuts : p.sub_slots), block, 0, s>>>(p);
         // blocks for the card, or one for each head
-        const int64_t heads = (int64_t)p.batch * p.H;
+        const int64_t heads = (int64_t)p.cuts * p.H;
         const int most = p.tiles * VT * KD / 1024, split = (int)std::min<int64_t>(most, (4096 + heads - 1) / heads);
         const dim3 cg((unsigned)heads, (unsigned)p.nops, (unsigned)split);
         la_chain<SB><<<cg, dim3(256), 0, s>>>(p, KD, VT);
@@ -802,12 +842,13 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     h.seg = cut ? (int)seg : 0;
     h.sub = cut ? (int)sub : 0;
     h.slots = cut ? (int)(T / seg) + batch : batch;
-    h.sub_slots = cut ? (int)(T / sub) + batch : 0;
+    h.cuts = cut ? (int)std::min<int64_t>(batch, T / (seg + 1)) : 0;
+    h.sub_slots = cut ? (int)(T / sub) + h.cuts : 0;
     h.bytes = (size_t)nops * h.sub_slots * H * h.tiles * h.vt * h.kd * sizeof(float);
     // (in whole runs of the workgroups that share rows, on 8 XCDs)
     const int64_t each = (int64_t)(H / h.heads) * h.tiles * nops, run = (int64_t)8 * (share / h.heads) * h.tiles * nops;
     const int64_t blocks = (std::max(h.slots, h.sub_slots) * each + run - 1) / run * run;
-    h.threads = std::max(blocks * (h.kd == 256 && h.vt == 128 ? 512 : 256), cut ? (int64_t)batch * H * 256 : 0);
+    h.threads = std::max(blocks * (h.kd == 256 && h.vt == 128 ? 512 : 256), (int64_t)h.cuts * H * 256);
     return h;
 }
 
@@ -818,6 +859,7 @@ hipError_t launch_walk(Params &p, const Shape &h, int nops, hipStream_t s) {
     p.sub = h.sub;
     p.slots = h.slots;
     p.sub_slots = h.sub_slots;
+    p.cuts = h.cuts;
     return p.state_bf16 ? launch_any<true>(p, h, s) : launch_any<false>(p, h, s);
 }
 

@@ -62,7 +62,8 @@ struct Params {
     // the launch (set by launch_walk)
     int nops, tiles;  // tiles: workgroups along the value channels
     int seg, slots;   // tokens of a segment (0: whole sequences) and slots of segments
-    int sub, sub_slots;  // the same of the parts of segments (seg is a multiple of sub)
+    int sub, sub_slots;  // the same of the parts of segments (seg is a multiple of sub), of cut sequences alone
+    int cuts;         // most sequences of more than a segment
     float *parts;     // [nops][sub_slots][H][tiles * VT][KD] states of the parts, in register order
 };
 
@@ -70,7 +71,7 @@ struct Params {
 struct Shape {
     int kd, vt, tiles;  // kd rounded up; value channels of a workgroup, and workgroups along vd
     int heads;          // heads of a workgroup
-    int seg, slots, sub, sub_slots;
+    int seg, slots, sub, sub_slots, cuts;
     size_t bytes;       // of `parts`
     int64_t threads;    // of its largest grid, which 32 bits have to hold
 };

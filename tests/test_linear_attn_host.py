@@ -167,6 +167,24 @@ def test_workspace_refusals(lib):
     assert seen
 
 
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("total,batch,nheads,ngroups,K,V", [
+    (4096, 4096, 128, 128, 128, 64), (1536, 512, 128, 128, 128, 64), (4096, 1024, 64, 64, 128, 128),
+    (12000, 12000, 16, 16, 256, 16), (100_000, 512, 128, 128, 128, 64), (43898, 32, 128, 128, 128, 64),
+    (65536, 1, 16, 16, 128, 128), (1000, 3, 2, 2, 64, 64)])
+def test_workspace_is_for_sequences_that_can_be_cut(lib, total, batch, nheads, ngroups, K, V, backward):
+    """Only sequences of more than a segment (128 tokens at least) leave states in the workspace: two for each 128
+    tokens at most (whole segments', and one more for a sequence's end), however many sequences there are."""
+    need = binding.ssd_linear_attn_workspace_size(
+        prob(total_len=total, batch=batch, nheads=nheads, ngroups=ngroups, key_dim=K, value_dim=V), backward)
+
+    def pad(d):
+        return 64 if d <= 64 else 128 if d <= 128 else 256
+
+    state = nheads * 4 * (pad(max(K, V)) ** 2 * 3 if backward else pad(K) * pad(V))
+    assert need <= 2 * (total // 128) * state
+
+
 def cache(**kw):
     base = dict(count=2, nheads=4, head_dim=64, dstate=128, max_slots=8, max_entries=5, state_dtype=0, code_format=0)
     base.update(kw)
