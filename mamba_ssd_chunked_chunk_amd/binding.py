@@ -472,15 +472,16 @@ def _token_stride(t, name, shape, device):
 
 
 @functools.lru_cache(maxsize=256)
-def _linear_attn_sizes(*sizes):
-    """(reference to the problem of these sizes, its workspace bytes forward and backward)"""
+def _linear_attn_sizes(backward, *sizes):
+    """(reference to the problem of these sizes, workspace bytes); ``backward`` None: of single tokens, which need
+    none and have wider limits"""
     prob = make_linear_attn_problem(*sizes)
-    return (ctypes.byref(prob), ssd_linear_attn_workspace_size(prob), ssd_linear_attn_workspace_size(prob, True))
+    return ctypes.byref(prob), 0 if backward is None else ssd_linear_attn_workspace_size(prob, backward)
 
 
-def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
-    """What a linear-attention call goes by, its inputs checked: problem, workspace bytes (forward, backward),
-    device, shape of a state, addresses of q, k, v and log_decay."""
+def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale, backward):
+    """What a linear-attention call goes by, its inputs checked: problem and workspace bytes (of the direction, or
+    None for single tokens), device, shape of a state, addresses of q, k, v and log_decay."""
     if torch is None:
         _import_torch()
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
@@ -493,11 +494,11 @@ def _linear_attn(q, k, v, log_decay, batch, max_slots, state_dtype, scale):
     _, G, K = qk = q.shape
     if qk[0] != T:
         _refuse_tensor(q, "q", torch.bfloat16, (T, G, K), dev)
-    prob, forward, backward = _linear_attn_sizes(
-        T, batch, H, G, K, V, max_slots, state_dtype, K ** -0.5 if scale is None else float(scale),
+    prob, need = _linear_attn_sizes(
+        backward, T, batch, H, G, K, V, max_slots, state_dtype, K ** -0.5 if scale is None else float(scale),
         _token_stride(q, "q", qk, dev), _token_stride(k, "k", qk, dev), _token_stride(v, "v", (T, H, V), dev))
     decay = _dense(log_decay, "log_decay", torch.float32, (H,), dev)
-    return prob, forward, backward, dev, (H, V, K), (q.data_ptr(), k.data_ptr(), v.data_ptr(), decay)
+    return prob, need, dev, (H, V, K), (q.data_ptr(), k.data_ptr(), v.data_ptr(), decay)
 
 
 def _slots(cache_indices, has_initial_state, batch, dev):
@@ -561,7 +562,8 @@ def ssd_linear_attn_varlen_fwd_inplace(o, q, k, v, log_decay, pool, query_start_
     """
     batch = query_start_loc.numel() - 1
     slots = pool.shape[0]
-    prob, need, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
+    prob, need, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale,
+                                                  False)
     out = _dense(o, "o", torch.bfloat16, v.shape, dev)
     states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
     qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
@@ -580,8 +582,8 @@ def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_stat
     batch = query_start_loc.numel() - 1
     if final_states is None:
         raise ValueError("final_states is required")
-    prob, need, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
-                                             _state_dtype(final_states, "final_states"), scale)
+    prob, need, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
+                                                  _state_dtype(final_states, "final_states"), scale, False)
     out = _dense(o, "o", torch.bfloat16, v.shape, dev)
     first = _dense_or_none(initial_states, "initial_states", final_states.dtype, (batch, *state), dev)
     last = _dense(final_states, "final_states", final_states.dtype, (batch, *state), dev)
@@ -603,8 +605,8 @@ def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_d
     states = ((d_initial_states, "d_initial_states"), (initial_states, "initial_states"),
               (d_final_states, "d_final_states"))
     kind = next((t for t in states if t[0] is not None), None)
-    prob, _, need, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
-                                             STATE_F32 if kind is None else _state_dtype(*kind), scale)
+    prob, need, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
+                                                  STATE_F32 if kind is None else _state_dtype(*kind), scale, True)
     d_first, first, d_last = (None if t is None else _dense(t, n, kind[0].dtype, (batch, *state), dev)
                               for t, n in states)
     bf16 = torch.bfloat16
@@ -625,7 +627,8 @@ def ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, has_initial_state,
     """
     batch = v.shape[0]
     slots = pool.shape[0]
-    prob, _, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale)
+    prob, _, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, slots, _state_dtype(pool, "pool"), scale,
+                                               None)
     out = _dense(o, "o", torch.bfloat16, v.shape, dev)
     states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
     idx, flags = _slots(cache_indices, has_initial_state, batch, dev)

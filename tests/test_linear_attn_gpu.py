@@ -298,6 +298,34 @@ def test_step(K, V, dtype):
     assert torch.equal(pool.cpu()[rest], before[rest])
 
 
+def test_more_tokens_than_a_backward_pass_takes():
+    """5.6 million token heads: more than the backward pass's three walks of each have threads for, which is no matter
+    to prompts and single tokens."""
+    B, H, K, V = 44_000, 128, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(970)
+    q, k, v = (torch.randn(B, n, 8, generator=g, device="cuda").to(BF16) for n in (1, 1, H))
+    log_decay = torch.full((H,), -0.5, device="cuda")
+    idx = torch.arange(B, dtype=torch.int32, device="cuda")
+    prob = binding.make_linear_attn_problem(B, B, H, 1, K, V, B, binding.STATE_BF16)
+    with pytest.raises(binding.SsdError):
+        binding.ssd_linear_attn_workspace_size(prob, backward=True)
+    state = (v.float()[..., None] * k.float()[:, :, None, :]).to(BF16)  # exact products, rounded once
+    want = 0.25 * v.double() * (q.double() * k.double()).sum(-1, keepdim=True)
+    # K products, their sum and the scale in fp32, of a state that the prompt form rounds to bf16, as its scores
+    size = 0.25 * v.double().abs() * (q.double() * k.double()).abs().sum(-1, keepdim=True)
+    for step in (True, False):
+        pool = torch.zeros(B, H, V, K, dtype=BF16, device="cuda")
+        o = torch.empty_like(v)
+        if step:
+            binding.ssd_linear_attn_step_inplace(o, q, k, v, log_decay, pool, None, idx, scale=0.25)
+        else:
+            qsl = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+            binding.ssd_linear_attn_varlen_fwd_inplace(o, q, k, v, log_decay, pool, qsl, None, idx, scale=0.25)
+        assert torch.equal(pool, state)
+        bound = size * (2.0 ** -24 * (K + 8) + (0 if step else L.BF16)) + rounding(BF16) * want.abs()
+        assert bool(((o.double() - want).abs() <= bound + 2.0 ** -120).all())
+
+
 def test_step_continues_a_prompt():
     """A prompt of n tokens and m single steps are the prompt of n + m tokens."""
     n, m, H, G, K, V = 77, 5, 4, 2, 128, 128

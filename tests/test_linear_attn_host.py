@@ -233,6 +233,17 @@ def test_workspaces_refused_by_the_binding():
             binding._run("x", cpu, None, 512, bad, call)
 
 
+def test_sizes_that_only_the_backward_pass_refuses():
+    """A call of the binding goes by its own limits: single tokens by the step's, prompts by the forward pass's."""
+    wide = (12000, 12000, 128, 8, 256, 16, 12000, binding.STATE_BF16, 1.0)
+    long = ((1 << 31) - 1, 1, 2, 1, 16, 64, 1, binding.STATE_F32, 1.0)
+    for sizes in (wide, long):
+        assert binding._linear_attn_sizes(None, *sizes)[1] == 0
+        assert binding._linear_attn_sizes(False, *sizes)[1] > 0
+        with pytest.raises(binding.SsdError):
+            binding._linear_attn_sizes(True, *sizes)
+
+
 def test_binding_refusals():
     torch = pytest.importorskip("torch")
     bf = torch.bfloat16
