@@ -222,3 +222,29 @@ def test_counted_traffic_sums_the_call(monkeypatch):
         a = types.SimpleNamespace(**dict(vars(args), **kw))
         t = bench.counted_traffic("w", ks, a)
         assert all(v is None for v in t.values()), kw
+
+
+def test_counted_traffic_goes_by_the_scans_sources(tmp_path, monkeypatch):
+    """Counters of the scan's kernels hold until a source of theirs changes: neither comments nor the operators beside
+    the scan make them stale, new sources do."""
+    csrc = tmp_path / "mamba_ssd_chunked_chunk_amd" / "csrc"
+    csrc.mkdir(parents=True)
+    (csrc / "ssd_common.hpp").write_text("int a;  // one\n")
+    (csrc / "ssd_short.hip").write_text("int b;\n")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    h = bench.kernel_sources_hash()
+    for name in ("ssd_linear_attn.hip", "ssd_linear_attn.hpp", "ssd_linear_attn_step.hip", "ssd_state_cache.hip"):
+        (csrc / name).write_text("int c;\n")
+        assert bench.kernel_sources_hash() == h, name
+    (csrc / "ssd_common.hpp").write_text("int a; /* two */\n")
+    assert bench.kernel_sources_hash() == h
+    (csrc / "ssd_new.hip").write_text("int d;\n")
+    assert bench.kernel_sources_hash() != h
+
+
+def test_the_scans_sources_include_no_other_operator():
+    csrc = os.path.join(ROOT, "mamba_ssd_chunked_chunk_amd", "csrc")
+    for f in os.listdir(csrc):
+        if not f.startswith(bench.OTHER_SOURCES):
+            text = open(os.path.join(csrc, f), encoding="utf-8").read()
+            assert not any(f'#include "{name}' in text for name in bench.OTHER_SOURCES), f
