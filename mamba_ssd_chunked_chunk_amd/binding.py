@@ -107,6 +107,9 @@ def load_library():
             if lib.ssd_abi_version() != ABI_VERSION:
                 raise RuntimeError(f"{LIB_PATH} has ABI version {lib.ssd_abi_version()}, the binding "
                                    f"expects {ABI_VERSION}: rebuild it")
+            lacks = [name for name in EXPORTED if not hasattr(lib, name)]
+            if lacks:
+                raise RuntimeError(f"{LIB_PATH} lacks {', '.join(lacks)}: rebuild it")
             lib.ssd_status_string.restype = ctypes.c_char_p
             lib.ssd_status_string.argtypes = [ctypes.c_int]
             lib.ssd_workspace_size.restype = ctypes.c_int

@@ -43,6 +43,19 @@ def test_version_and_status_strings(lib):
     assert b"unknown" in lib.ssd_status_string(99)
 
 
+def test_a_library_from_before_the_newest_functions_is_refused(tmp_path, monkeypatch):
+    """Functions are added under one version: a library that lacks some says so when it is loaded."""
+    import subprocess
+    src, so = tmp_path / "old.c", tmp_path / "old.so"
+    src.write_text("int ssd_abi_version(void) { return %d; }\n" % binding.ABI_VERSION)
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "LIB_PATH", str(so))
+    with pytest.raises(RuntimeError, match="ssd_linear_attn_varlen_fwd.*rebuild"):
+        binding.load_library()
+    assert binding._lib is None
+
+
 def _prob(**kw):
     base = dict(total_len=1024, batch=4, nheads=16, head_dim=64, ngroups=1, dstate=256, max_slots=8)
     base.update(kw)
