@@ -102,21 +102,6 @@ __device__ __forceinline__ void read_state(const void *base, int64_t at, int64_t
         }
     }
 }
-template <bool SB>
-__device__ __forceinline__ void write_state(void *base, int64_t at, int64_t sk, const float (&f)[8]) {
-    if (sk == 1) {
-        store_state8<SB>(base, at, f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (SB)
-                static_cast<uint16_t *>(base)[at + e * sk] = float_to_bf16_bits(f[e]);
-            else
-                static_cast<float *>(base)[at + e * sk] = f[e];
-        }
-    }
-}
-
 __device__ __forceinline__ int clamp_row(const Params &p, int t) { return min(max(t, 0), (int)p.T); }
 
 // log2 of a head's decay; -infinity as a finite number, so that times 0 it is 0
@@ -643,7 +628,7 @@ __global__ __launch_bounds__(64 * NW, CT == 64 ? 2 : 3) void la_walk(Params p) {
                 float f[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = S[t][e / 4][d][e % 4];
-                write_state<SB>(op.state_out, state_at + vch(d) * op.sv + kc * op.sk, op.sk, f);
+                store_state8<SB>(op.state_out, state_at + vch(d) * op.sv + kc, f);
             }
     }
 }

@@ -35,7 +35,8 @@ struct Op {
     float scale_state;   // on out from the state that enters the chunk
     float scale_update;  // on v k^T as it enters the state
     // state element (v channel i, k channel j) of slot s, head h at
-    // ((s H + h) state_size + i sv + j sk); null in: zero, null out: dropped
+    // ((s H + h) state_size + i sv + j sk); null in: zero, null out: dropped (sk
+    // is 1 where there is an out)
     const void *state_in;
     void *state_out;
     int64_t sv, sk;
