@@ -218,6 +218,13 @@ def _opt(t, name, dtype, shape, device):
     return t
 
 
+def _need_workspace(t, need, device):
+    """A workspace has to hold its bytes itself (an expanded byte has their number, not their memory)."""
+    import torch
+    if t.dtype != torch.uint8 or t.numel() < need or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on {device}")
+
+
 def problem_from_tensors(x, B, ssm_pool, query_start_loc, dt_softplus=True,
                          short_path_max=SHORT_PATH_DEFAULT) -> ssd_problem:
     T, H, P = x.shape
@@ -278,8 +285,8 @@ def ssd_chunk_scan_varlen_fwd_inplace(y, x, dt, A, B, C, D, dt_bias, ssm_pool, q
     need = ssd_workspace_size(prob)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev:
-        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+    else:
+        _need_workspace(workspace, need, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev)
     status = load_library().ssd_chunk_scan_varlen_fwd_inplace(
         ctypes.byref(prob), _ptr(y), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -376,8 +383,8 @@ def ssd_chunk_scan_varlen_fwd(y, x, dt, A, B, C, D, dt_bias, initial_states, fin
     need = ssd_workspace_size(prob)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev:
-        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+    else:
+        _need_workspace(workspace, need, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev)
     status = load_library().ssd_chunk_scan_varlen_fwd(
         ctypes.byref(prob), _ptr(y), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -534,9 +541,7 @@ def _run(name, dev, stream, need, workspace, call):
     """The same for ``call(workspace address, bytes, stream)``.  A workspace that the caller does not give is
     allocated on the call's stream.  Returns the workspace (None where none was given and none is needed)."""
     if workspace is not None:
-        if (workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev
-                or not workspace.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on {dev}")
+        _need_workspace(workspace, need, dev)
     elif need:
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)

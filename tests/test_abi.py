@@ -56,6 +56,18 @@ def test_a_library_from_before_the_newest_functions_is_refused(tmp_path, monkeyp
     assert binding._lib is None
 
 
+def test_a_workspace_holds_its_bytes_itself():
+    """An expanded byte has as many elements, all of them one: every entry point would write past it."""
+    torch = pytest.importorskip("torch")
+    cpu, byte = torch.device("cpu"), torch.zeros(1, dtype=torch.uint8)
+    for good in (torch.zeros(512, dtype=torch.uint8), torch.zeros(16, 64, dtype=torch.uint8)):
+        binding._need_workspace(good, 512, cpu)
+    for bad in (byte.expand(512), torch.zeros(1024, dtype=torch.uint8)[::2], torch.zeros(511, dtype=torch.uint8),
+                torch.zeros(512, dtype=torch.int8)):
+        with pytest.raises(ValueError, match="workspace"):
+            binding._need_workspace(bad, 512, cpu)
+
+
 def _prob(**kw):
     base = dict(total_len=1024, batch=4, nheads=16, head_dim=64, ngroups=1, dstate=256, max_slots=8)
     base.update(kw)

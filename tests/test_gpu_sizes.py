@@ -136,3 +136,16 @@ def test_sizes_profiled_entry():
     assert torch.equal(run.d["y"].view(torch.int16), d["y"].view(torch.int16))
     assert torch.equal(run.d["pool"].view(torch.int32), d["pool"].view(torch.int32))
     assert hip.elapsed_ms(events[0], events[run.nk]) > 0.0
+
+
+def test_expanded_workspaces_are_refused():
+    """Both entry points of the scan that take a workspace, before anything is launched."""
+    from mamba_ssd_chunked_chunk_amd.workloads import make_problem
+    prob = make_problem([40, 300], nheads=4, head_dim=64, ngroups=2, dstate=64, max_slots=3, seed=3)
+    d = torch_io.upload(prob, "cuda:0")
+    need = binding.ssd_workspace_size(torch_io.problem_struct(d))
+    bad = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need)
+    with pytest.raises(ValueError, match="contiguous"):
+        torch_io.run(d, workspace=bad)
+    with pytest.raises(ValueError, match="contiguous"):
+        torch_io.run_fwd(d, None, torch.zeros(2, 4, 64, 64, device="cuda"), workspace=bad)
