@@ -584,7 +584,7 @@ def ssd_linear_attn_varlen_fwd_inplace(o, q, k, v, log_decay, pool, query_start_
 def ssd_linear_attn_varlen_fwd(o, q, k, v, log_decay, initial_states, final_states, query_start_loc, *, scale=None,
                                workspace=None, stream=None):
     """The same with separate states: sequence b starts from
-    ``initial_states[b]`` ([batch,H,V,K], or None for zero) and leaves
+    ``initial_states[b]`` ([batch,H,V,K], or None or empty for zero) and leaves
     ``final_states[b]``; both fp32 or both bf16.  Returns the workspace tensor.
     """
     batch = query_start_loc.numel() - 1
@@ -606,12 +606,12 @@ def ssd_linear_attn_varlen_bwd(dq, dk, dv, d_initial_states, q, k, v, d_o, log_d
     """Backward pass of ssd_linear_attn_varlen_fwd (see include/ssd.h): dq, dk
     bf16 [T,G,K] and dv bf16 [T,H,V] are written, and ``d_initial_states``
     where it is not None; ``initial_states`` and ``d_final_states`` may be None
-    (zero).  State tensors [batch,H,V,K], all fp32 or all bf16.  Returns the
+    or empty (zero).  State tensors [batch,H,V,K], all fp32 or all bf16.  Returns the
     workspace tensor.
     """
     batch = query_start_loc.numel() - 1
-    states = ((d_initial_states, "d_initial_states"), (initial_states, "initial_states"),
-              (d_final_states, "d_final_states"))
+    given = [None if t is None or t.numel() == 0 else t for t in (initial_states, d_final_states)]
+    states = ((d_initial_states, "d_initial_states"), (given[0], "initial_states"), (given[1], "d_final_states"))
     kind = next((t for t in states if t[0] is not None), None)
     prob, need, dev, state, inputs = _linear_attn(q, k, v, log_decay, batch, max(batch, 1),
                                                   STATE_F32 if kind is None else _state_dtype(*kind), scale, True)

@@ -687,6 +687,21 @@ def test_autograd_of_gradients_that_start_anywhere():
     assert all(torch.equal(a, b) for a, b in zip(want, torch.autograd.grad(outs, x, moved)))
 
 
+def test_autograd_of_empty_initial_states():
+    """Empty initial states stand for zero in the backward pass as in the forward pass; their type is the states'."""
+    from mamba_ssd_chunked_chunk_amd.linear_attention import linear_attention
+    c = cuda(L.draw([70, 33], 2, 2, 64, 64, 1650))
+    x = [c[n].clone().requires_grad_() for n in "qkv"]
+    got, want = [], []
+    for initial, results in ((torch.empty(0, dtype=BF16, device="cuda"), got), (None, want)):
+        o, final = linear_attention(*x, c["log_decay"], c["query_start_loc"], initial, state_dtype=BF16)
+        results += [o, final, *torch.autograd.grad([o, final], x, [c["d_o"], c["d_final"].bfloat16()])]
+    assert final.dtype == BF16 and all(torch.equal(a, b) for a, b in zip(got, want))
+    grads = [torch.empty_like(c[n]) for n in "qkv"]
+    empty = torch.empty(0, device="cuda")
+    binding.ssd_linear_attn_varlen_bwd(*grads, None, *x, c["d_o"], c["log_decay"], empty, empty, c["query_start_loc"])
+
+
 def test_autograd_refuses_a_learned_decay():
     from mamba_ssd_chunked_chunk_amd.linear_attention import linear_attention
     d = cuda(L.draw([5], 1, 1, 64, 64, 1620))
