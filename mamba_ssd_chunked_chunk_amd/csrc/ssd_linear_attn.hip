@@ -28,13 +28,13 @@
 //   - of 32 rows of q or scores, the first 16-row tile takes 0 .. 3, 8 .. 11,
 //     .., the second the others.
 //
-// What bounds it: 65536 tokens of 16 heads of 128 x 128: the walk 236 us (1.07 GB
-// at 4.5 TB/s, a copy's being 5.1), the pass for segments' states 132 us (0.54
-// GB at 4.1 TB/s): memory; the call takes 392 us, 370 with most products left
+// What bounds it: 65536 tokens of 16 heads of 128 x 128: the walk 233 us (1.11 GB
+// counted, 4.8 TB/s, a copy's being 5.1), the pass for segments' states 132 us
+// (0.55 GB, 4.2 TB/s): memory; the call takes 393 us, 370 with most products left
 // out and 241 with no rows moved after the first.  32 ragged prompts of 128 heads
-// that share q and k by 16: 527 us, 402 with most products left out, 328 with no
-// rows moved: with two workgroups a compute unit the two overlap only in part
-// (matrix cores busy 34% of the cycles, LDS 38%).
+// that share q and k by 16: 538 us (1.76 GB), 402 with most products left out, 328
+// with no rows moved: with two workgroups a compute unit the two overlap only in
+// part (matrix cores busy 35% of the cycles, LDS 38%).
 //
 // Rounding: scores and the state are rounded to bf16 once as operands of the
 // output, which is bf16 itself.  The weighted v of the state update is split
@@ -793,9 +793,14 @@ Shape shape_of(int64_t T, int batch, int H, int share, int kd, const int *vds, i
     const int64_t mean = (T + batch - 1) / batch;
     // Wide keys: one workgroup of 8 wavefronts and 128 value channels fills a
     // compute unit's LDS; where sequences are short, and their states most of the
-    // traffic, three with 64 channels and chunks of 32 tokens move them faster (20
-    // sequences of 27 tokens in the mean, backward: 76 -> 59 us; packed documents
-    // of 1700: 387 -> 503).
+    // traffic, three with 64 channels and chunks of 32 tokens move them faster.
+    // The border depends on the widths too (us with 64 / 128 channels for everything):
+    //   mean length                        27        66       ~200  265-282   ~1100
+    //   96 x 200, 12 heads, backward  1319/1371   809/761   562/487  564/455  484/392
+    //   256 x 256, 12 heads, backward 1911/2693 1134/1423   754/857  704/779  598/618
+    //   192 x 128, 4 heads, backward   136/227    96/128     66/92    69/92
+    //   200 x 128, 12 heads, prompts   468/609   262/301    170/190  171/176  200/173
+    // 256 tokens lose up to 15% below it (96 x 200) and a third above it (192 x 128).
     h.vt = vd <= 64 || (h.kd == 256 && mean <= 256) ? 64 : 128;
     h.heads = h.vt == 64 && h.kd < 256 && share % 2 == 0 && nops == 1 ? 2 : 1;
     const int64_t kAtOnce = h.kd < 256 ? 512 : h.vt == 64 ? 768 : 256;

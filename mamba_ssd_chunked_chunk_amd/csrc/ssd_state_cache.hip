@@ -2,9 +2,11 @@
 // and read back.  A row lies across the lanes that hold 16 bytes of its state
 // each (4 elements in fp32, 8 in bf16), so every state access of a wavefront is
 // one run of memory; a thread takes several rows so that enough of them are in
-// flight.  Both directions are bound by HBM: 4 (or 2) + 1 bytes an element.
-// 268 MB of fp32 state to int8: 87 us (3.9 TB/s); back: 56 us (6.0 TB/s, over a
-// large copy's 5.1); 1.07 GB from e4m3: 258 us (5.2 TB/s; medians).  Lanes of 8 elements of
+// flight.  Both directions are bound by memory: 4 (or 2) + 1 bytes an element.
+// 268 MB of fp32 state to int8: 87 us (338 MB counted, 3.9 TB/s); back: 57 us (338
+// MB, 5.9 TB/s: four bytes of five are written, and the codes, 67 MB and just
+// written, fit the 256 MB cache, so a copy's 5.1 is no bound here); 1.07 GB from
+// e4m3: 256 us (1.35 GB, 5.3 TB/s; medians).  Lanes of 8 elements of
 // fp32 and 4 rows a thread: 88 us, and 77 back; 16 rows a thread to int8: 103.
 #include <algorithm>
 
