@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kThreads) void la_step(StepParams p) {
         load_state8<true>(p.q, b * p.qs + (int64_t)(h / p.div) * p.K + c, q);
         load_state8<true>(p.k, b * p.ks + (int64_t)(h / p.div) * p.K + c, k);
     }
-    const float decay = expf(p.log_decay[h]);
+    const float decay = init ? expf(p.log_decay[h]) : 0.f;  // no state, nothing to decay: lambda may be infinite
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
         const bool row = r0 + n * RP < p.V;

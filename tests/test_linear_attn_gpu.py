@@ -298,6 +298,25 @@ def test_step(K, V, dtype):
     assert torch.equal(pool.cpu()[rest], before[rest])
 
 
+def test_a_first_token_needs_no_decay():
+    """A sequence that starts from zero leaves v k^T behind one token, also where lambda itself passes fp32."""
+    d = L.draw([1, 1], 4, 2, 64, 64, 960, slots=2)
+    d["log_decay"] = torch.tensor([100.0, 89.0, 2.0, -1.0])
+    c = cuda(d)
+    want, final = L.reference(dict(d, log_decay=torch.zeros(4)), [1, 1], 0.125)
+    bo, _ = L.forward_bounds(dict(d, log_decay=torch.zeros(4)), [1, 1], 0.125)
+    for step in (True, False):
+        pool, o = c["pool"].clone(), torch.full_like(c["v"], 7.0)
+        if step:
+            binding.ssd_linear_attn_step_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool, None,
+                                                 c["cache_indices"], scale=0.125)
+        else:
+            binding.ssd_linear_attn_varlen_fwd_inplace(o, c["q"], c["k"], c["v"], c["log_decay"], pool,
+                                                       c["query_start_loc"], None, c["cache_indices"], scale=0.125)
+        assert torch.equal(pool[c["cache_indices"].long()].cpu().double(), final)  # products of bf16, exact in fp32
+        assert L.worst(o, want, bo, rounding(BF16)) <= 1
+
+
 def test_more_tokens_than_a_backward_pass_takes():
     """5.6 million token heads: more than the backward pass's three walks of each have threads for, which is no matter
     to prompts and single tokens."""
