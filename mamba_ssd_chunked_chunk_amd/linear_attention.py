@@ -57,8 +57,9 @@ def linear_attention(q, k, v, log_decay, query_start_loc, initial_states=None, *
 
     q, k bf16 [T,G,K], v bf16 [T,H,V] (slices of one projection will do), log_decay fp32 [H] (a constant of the
     layer: it gets no gradient), query_start_loc int32 [batch+1], initial_states [batch,H,V,K] in fp32 or bf16, or
-    None for zero (or an empty tensor; the final states are then of ``state_dtype``).  ``scale``: None for K ** -0.5.  Returns o bf16
-    [T,H,V] and the final states [batch,H,V,K]; both are differentiable in q, k, v and initial_states.
+    None for zero (the final states are then of ``state_dtype``; an empty tensor stands for zero too, in its own
+    type).  ``scale``: None for K ** -0.5.  Returns o bf16 [T,H,V] and the final states [batch,H,V,K]; both are
+    differentiable in q, k, v and initial_states.
 
     Rows behind query_start_loc[-1] need ``padded=True``: their outputs and gradients are then zero (otherwise they
     are not written).
