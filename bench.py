@@ -168,7 +168,8 @@ def roofline_entry(name, alg, t_us, traffic=None):
 
 
 # sources of the operators beside the scan: no workload here runs them
-OTHER_SOURCES = ("ssd_linear_attn", "ssd_state_cache")
+OTHER_SOURCES = ("ssd_linear_attn", "ssd_state_cache", "ssd_layer", "ssd_rms_norm", "ssd_causal_conv",
+                 "ssd_selective")
 
 
 def kernel_sources_hash():

@@ -504,6 +504,195 @@ ssd_status ssd_state_dequantize(const ssd_state_cache_problem *prob, void *pool,
                                 const float *scales, const uint32_t *pool_indices,
                                 const uint32_t *entry_indices, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What stands around a mixer of these kinds: the norm ahead of it with the
+ * residual's addition, and the short convolution ahead of its scan.
+ *
+ * Norm.  Of each row, with r the residual stream in its own type:
+ *     r = residual + x     y = r / sqrt(mean(r^2) + eps) * weight
+ * (r = x without a residual).  y is bf16, or 8 bits with one fp32 scale a row
+ * by the rule of the parked states above (SSD_CODE_I8, SSD_CODE_E4M3), a row
+ * of y in place of a row of a state.  Sums are fp32; r is rounded once, to the
+ * residual's type, and y is the norm of what is stored.                    */
+#define SSD_NORM_MAX_WIDTH 32768
+#define SSD_OUT_BF16 2  /* beside SSD_CODE_I8 and SSD_CODE_E4M3 */
+typedef struct ssd_norm_problem {
+    int64_t rows;           /* >= 0                                           */
+    int32_t width;          /* multiple of 8, 8 .. SSD_NORM_MAX_WIDTH         */
+    int32_t residual_dtype; /* SSD_STATE_F32 or SSD_STATE_BF16: of residual, residual_out, r, d_r */
+    int32_t out_format;     /* SSD_OUT_BF16, SSD_CODE_I8 or SSD_CODE_E4M3 (forward only) */
+    float eps;              /* >= 0, finite                                   */
+    int64_t x_stride;       /* elements from one row of x to the next: a multiple of 8, at least width, or 0 for dense */
+} ssd_norm_problem;
+
+/*   y            OUT  bf16, or 8-bit codes, [rows,width]
+ *   scales       OUT  fp32 [rows] (8-bit codes only; NULL for bf16)
+ *   residual_out OUT  [rows,width], or NULL without a residual; may be the
+ *                     same buffer as residual
+ *   x            IN   bf16 [rows,width]
+ *   residual     IN   [rows,width], or NULL
+ *   weight       IN   fp32 [width]                                        */
+ssd_status ssd_rms_norm_fwd(const ssd_norm_problem *prob, void *y, float *scales, void *residual_out,
+                            const void *x, const void *residual, const float *weight, void *stream);
+
+/* Workspace of the backward pass, 256-byte aligned.  Host only.           */
+ssd_status ssd_rms_norm_workspace_size(const ssd_norm_problem *prob, size_t *bytes);
+
+/* Backward pass, of y in bf16.  With r what the forward pass stored (x where
+ * there was no residual), s = 1 / sqrt(mean(r^2) + eps), u = weight d_y:
+ *     d = s u - s^3 r mean(u r) + d_r       dweight = sum over rows of s r d_y
+ *   dx           OUT  bf16 [rows,width]: d
+ *   d_residual   OUT  the residual's type [rows,width]: d, or NULL (dx serves
+ *                     both where the residual is bf16)
+ *   dweight      OUT  fp32 [width]
+ *   r            IN   the residual's type [rows,width]
+ *   d_y          IN   bf16 [rows,width]
+ *   d_r          IN   the residual's type [rows,width]: gradient of
+ *                     residual_out, or NULL (zero); may be d_residual's buffer */
+ssd_status ssd_rms_norm_bwd(const ssd_norm_problem *prob, void *dx, void *d_residual, float *dweight,
+                            const void *r, const float *weight, const void *d_y, const void *d_r,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Short causal depthwise convolution over a ragged batch.  For channel d:
+ *     p_t = bias[d] + sum_j weight[d][j] x_{t - (width - 1) + j}
+ *     y_t = p_t sigmoid(p_t) with silu, p_t without
+ * where the inputs ahead of a sequence are its state (zero where it has none).
+ * The state of a sequence is its last width - 1 inputs, oldest first:
+ * [width - 1, channels] in bf16, bit for bit the inputs.  query_start_loc,
+ * has_initial_state, cache_indices, rows behind the last sequence and padding
+ * entries as for linear attention.  Sums are fp32.                         */
+#define SSD_CONV_MAX_WIDTH 4
+typedef struct ssd_conv_problem {
+    int64_t total_len;  /* rows of x and y; >= 0, fits int32                  */
+    int32_t batch;      /* number of sequences; >= 1                          */
+    int32_t channels;   /* multiple of 8                                      */
+    int32_t width;      /* taps: 2 .. SSD_CONV_MAX_WIDTH                      */
+    int32_t max_slots;  /* leading dimension of the pool; >= 1 (in-place only) */
+    int32_t silu;       /* nonzero: silu behind the sum                       */
+    int64_t x_stride;   /* elements from one token of x to the next: a multiple of 8, at least channels, or 0 for dense */
+} ssd_conv_problem;
+
+/*   y        OUT  bf16 [T,channels]
+ *   x        IN   bf16 [T,channels]
+ *   weight   IN   fp32 [channels,width]
+ *   bias     IN   fp32 [channels], or NULL
+ *   pool     IN/OUT bf16 [max_slots,width - 1,channels]                   */
+ssd_status ssd_causal_conv_varlen_fwd_inplace(
+    const ssd_conv_problem *prob, void *y, const void *x, const float *weight, const float *bias, void *pool,
+    const int32_t *query_start_loc, const uint8_t *has_initial_state, const uint32_t *cache_indices, void *stream);
+
+/* The same with separate states [batch,width - 1,channels]: initial_states
+ * may be NULL (zero) or the same buffer as final_states.                   */
+ssd_status ssd_causal_conv_varlen_fwd(
+    const ssd_conv_problem *prob, void *y, const void *x, const float *weight, const float *bias,
+    const void *initial_states, void *final_states, const int32_t *query_start_loc, void *stream);
+
+/* Workspace of the backward pass, 256-byte aligned.  Host only.           */
+ssd_status ssd_causal_conv_workspace_size(const ssd_conv_problem *prob, size_t *bytes);
+
+/* Backward pass of ssd_causal_conv_varlen_fwd.
+ *   dx        OUT  bf16 [T,channels] (dense)
+ *   dweight   OUT  fp32 [channels,width]
+ *   dbias     OUT  fp32 [channels], or NULL
+ *   d_initial OUT  bf16 [batch,width - 1,channels], or NULL
+ *   d_y       IN   bf16 [T,channels] (dense)
+ *   d_final   IN   bf16 [batch,width - 1,channels], or NULL (zero)
+ * No output may overlap an input.                                          */
+ssd_status ssd_causal_conv_varlen_bwd(
+    const ssd_conv_problem *prob, void *dx, float *dweight, float *dbias, void *d_initial, const void *x,
+    const float *weight, const float *bias, const void *d_y, const void *initial_states, const void *d_final,
+    const int32_t *query_start_loc, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Single tokens: sequence b is the one token in row b (total_len == batch). */
+ssd_status ssd_causal_conv_step_inplace(
+    const ssd_conv_problem *prob, void *y, const void *x, const float *weight, const float *bias, void *pool,
+    const uint8_t *has_initial_state, const uint32_t *cache_indices, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Selective scan: a decay per channel and state, a time step per channel.
+ * For channel d of group g = d / (channels / ngroups):
+ *     dts = softplus(dt[t,d] + dt_bias[d])     (dt + dt_bias when dt_softplus is 0)
+ *     h[n] = exp(dts A[d,n]) h[n] + dts x[t,d] B[t,g,n]
+ *     s[t,d] = sum_n C[t,g,n] h[n] + D[d] x[t,d]
+ *     y[t,d] = s[t,d] z[t,d] sigmoid(z[t,d])   (s where there is no z)
+ * with the state reset at every query_start_loc boundary, as in the scan.
+ * query_start_loc, has_initial_state, cache_indices, rows behind the last
+ * sequence and padding entries as for linear attention.  x, dt, z, B and C
+ * may have a stride between tokens (slices of projections); everything else is
+ * dense.  Activations are bf16; A, D, dt_bias, the states and all sums are
+ * fp32.  A is normally negative; powers of decays above 1 have to be finite in
+ * fp32 over a whole sequence.  Results are deterministic (bitwise run to run). */
+#define SSD_SELECTIVE_MAX_DSTATE 64
+typedef struct ssd_selective_problem {
+    int64_t total_len;   /* rows of x, dt, z, B, C, y; >= 0, fits int32        */
+    int32_t batch;       /* number of sequences; >= 1                         */
+    int32_t channels;    /* multiple of 8 ngroups                             */
+    int32_t ngroups;     /* G                                                 */
+    int32_t dstate;      /* N: multiple of 4, 4 .. SSD_SELECTIVE_MAX_DSTATE    */
+    int32_t max_slots;   /* leading dimension of the pool; >= 1 (in-place only) */
+    int32_t dt_softplus; /* nonzero: softplus                                 */
+    int32_t state_dtype; /* SSD_STATE_F32 or SSD_STATE_BF16                   */
+    /* elements from one token to the next, or 0 for dense: of x, dt and z a
+     * multiple of 8, at least channels; of B and C even, at least ngroups dstate */
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+} ssd_selective_problem;
+
+/* Workspace of the prompt forms (backward 0) or of the backward pass
+ * (backward not 0), 256-byte aligned; 0 bytes need none.  Host only.      */
+ssd_status ssd_selective_scan_workspace_size(const ssd_selective_problem *prob, int backward, size_t *bytes);
+
+/* Prompts, pool updated in place.
+ *   y         OUT  bf16 [T,channels]
+ *   x, dt     IN   bf16 [T,channels]
+ *   A         IN   fp32 [channels,N]
+ *   B, C      IN   bf16 [T,G,N] (from a 4-byte boundary on)
+ *   D         IN   fp32 [channels], or NULL (0)
+ *   z         IN   bf16 [T,channels], or NULL (no gate)
+ *   dt_bias   IN   fp32 [channels], or NULL (0)
+ *   pool      IN/OUT fp32 or bf16 (state_dtype) [max_slots,channels,N]: the
+ *             layout of a scan's pool with nheads 1 (or any split of the
+ *             channels into heads), so ssd_state_quantize parks it where N is
+ *             a multiple of 8                                              */
+ssd_status ssd_selective_scan_varlen_fwd_inplace(
+    const ssd_selective_problem *prob, void *y, const void *x, const void *dt, const float *A, const void *B,
+    const void *C, const float *D, const void *z, const float *dt_bias, void *pool, const int32_t *query_start_loc,
+    const uint8_t *has_initial_state, const uint32_t *cache_indices, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/* The same with separate states [batch,channels,N]: initial_states may be
+ * NULL (zero) or the same buffer as final_states.                          */
+ssd_status ssd_selective_scan_varlen_fwd(
+    const ssd_selective_problem *prob, void *y, const void *x, const void *dt, const float *A, const void *B,
+    const void *C, const float *D, const void *z, const float *dt_bias, const void *initial_states,
+    void *final_states, const int32_t *query_start_loc, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of ssd_selective_scan_varlen_fwd.  With e = d_y silu(z), U the
+ * gradient of h and a = exp(dts A):
+ *     U_t = C_t e_t + a_{t+1} U_{t+1}  (+ d_final for the last token)
+ *     dC_t = sum_d e_t h_t,  dB_t = sum_d U_t dts x_t  (over a group's channels)
+ *     dx_t = dts U_t.B_t + D e_t,  dz = d_y s silu'(z),  dD = sum_t e_t x_t
+ *     q = a_t h_{t-1} U_t,  dA = sum_t dts q,  d_dts = q.A + x_t U_t.B_t
+ *     ddt = d_dts softplus'(dt + dt_bias),  ddt_bias = sum_t ddt,  d_initial = a_1 U_1
+ *   dx, ddt, dz OUT bf16 [T,channels] (dense; dz NULL exactly where z is)
+ *   dB, dC      OUT bf16 [T,G,N] (dense)
+ *   dA          OUT fp32 [channels,N];  dD, ddt_bias OUT fp32 [channels] or NULL
+ *   d_initial   OUT state_dtype [batch,channels,N], or NULL
+ *   d_y         IN  bf16 [T,channels] (dense)
+ *   d_final     IN  state_dtype [batch,channels,N], or NULL (zero)
+ * No output may overlap an input.                                          */
+ssd_status ssd_selective_scan_varlen_bwd(
+    const ssd_selective_problem *prob, void *dx, void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz,
+    float *ddt_bias, void *d_initial, const void *x, const void *dt, const float *A, const void *B, const void *C,
+    const float *D, const void *z, const float *dt_bias, const void *d_y, const void *initial_states,
+    const void *d_final, const int32_t *query_start_loc, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Single tokens: sequence b is the one token in row b (total_len == batch),
+ * pool updated in place.  One kernel, no workspace.                        */
+ssd_status ssd_selective_scan_step_inplace(
+    const ssd_selective_problem *prob, void *y, const void *x, const void *dt, const float *A, const void *B,
+    const void *C, const float *D, const void *z, const float *dt_bias, void *pool,
+    const uint8_t *has_initial_state, const uint32_t *cache_indices, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,7 +30,12 @@ EXPORTED = ("ssd_abi_version", "ssd_status_string", "ssd_workspace_size",
             "ssd_chunk_scan_varlen_fwd_inplace_noalloc",
             "ssd_linear_attn_workspace_size", "ssd_linear_attn_varlen_fwd_inplace", "ssd_linear_attn_varlen_fwd",
             "ssd_linear_attn_varlen_bwd", "ssd_linear_attn_step_inplace", "ssd_state_quantize",
-            "ssd_state_dequantize")
+            "ssd_state_dequantize",
+            "ssd_rms_norm_fwd", "ssd_rms_norm_workspace_size", "ssd_rms_norm_bwd",
+            "ssd_causal_conv_varlen_fwd_inplace", "ssd_causal_conv_varlen_fwd", "ssd_causal_conv_workspace_size",
+            "ssd_causal_conv_varlen_bwd", "ssd_causal_conv_step_inplace",
+            "ssd_selective_scan_workspace_size", "ssd_selective_scan_varlen_fwd_inplace",
+            "ssd_selective_scan_varlen_fwd", "ssd_selective_scan_varlen_bwd", "ssd_selective_scan_step_inplace")
 
 
 class SsdError(RuntimeError):
@@ -61,6 +66,25 @@ class ssd_state_cache_problem(ctypes.Structure):
                 ("state_dtype", ctypes.c_int32), ("code_format", ctypes.c_int32)]
 
 
+class ssd_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("out_format", ctypes.c_int32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64)]
+
+
+class ssd_conv_problem(ctypes.Structure):
+    _fields_ = [("total_len", ctypes.c_int64), ("batch", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("max_slots", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64)]
+
+
+class ssd_selective_problem(ctypes.Structure):
+    _fields_ = [("total_len", ctypes.c_int64), ("batch", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("ngroups", ctypes.c_int32), ("dstate", ctypes.c_int32), ("max_slots", ctypes.c_int32),
+                ("dt_softplus", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("c_stride", ctypes.c_int64)]
+
+
 class ssd_workspace_layout(ctypes.Structure):
     _fields_ = [("total_bytes", ctypes.c_size_t), ("nchunks_max", ctypes.c_int64),
                 ("meta", ctypes.c_size_t), ("chunk_off", ctypes.c_size_t),
@@ -85,6 +109,10 @@ SHORT_PATH_LIMIT = 128  # SSD_SHORT_PATH_LIMIT
 MAX_DSTATE, MAX_HEAD_DIM = 256, 1024  # SSD_MAX_DSTATE, SSD_MAX_HEAD_DIM
 LINEAR_ATTN_MAX_DIM = 256  # SSD_LINEAR_ATTN_MAX_DIM
 CODE_I8, CODE_E4M3 = 0, 1  # SSD_CODE_I8, SSD_CODE_E4M3
+OUT_BF16 = 2  # SSD_OUT_BF16
+NORM_MAX_WIDTH = 32768  # SSD_NORM_MAX_WIDTH
+CONV_MAX_WIDTH = 4  # SSD_CONV_MAX_WIDTH
+SELECTIVE_MAX_DSTATE = 64  # SSD_SELECTIVE_MAX_DSTATE
 SHORT_PATH_DEFAULT = -1  # ssd_problem.short_path_max: any negative value selects SHORT_PATH_LIMIT
 
 
@@ -136,6 +164,7 @@ def load_library():
             lib.ssd_validate_inputs.argtypes = [PP, V, V, V]
             PL = ctypes.POINTER(ssd_linear_attn_problem)
             PC = ctypes.POINTER(ssd_state_cache_problem)
+            PN, PV, PS = (ctypes.POINTER(s) for s in (ssd_norm_problem, ssd_conv_problem, ssd_selective_problem))
             for name, args in (
                     ("ssd_linear_attn_workspace_size", [PL, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
                     ("ssd_linear_attn_varlen_fwd_inplace", [PL] + [V] * 10 + [ctypes.c_size_t, V]),
@@ -143,7 +172,20 @@ def load_library():
                     ("ssd_linear_attn_varlen_bwd", [PL] + [V] * 13 + [ctypes.c_size_t, V]),
                     ("ssd_linear_attn_step_inplace", [PL] + [V] * 9),
                     ("ssd_state_quantize", [PC] + [V] * 6),
-                    ("ssd_state_dequantize", [PC] + [V] * 6)):
+                    ("ssd_state_dequantize", [PC] + [V] * 6),
+                    ("ssd_rms_norm_fwd", [PN] + [V] * 7),
+                    ("ssd_rms_norm_workspace_size", [PN, ctypes.POINTER(ctypes.c_size_t)]),
+                    ("ssd_rms_norm_bwd", [PN] + [V] * 8 + [ctypes.c_size_t, V]),
+                    ("ssd_causal_conv_varlen_fwd_inplace", [PV] + [V] * 9),
+                    ("ssd_causal_conv_varlen_fwd", [PV] + [V] * 8),
+                    ("ssd_causal_conv_workspace_size", [PV, ctypes.POINTER(ctypes.c_size_t)]),
+                    ("ssd_causal_conv_varlen_bwd", [PV] + [V] * 12 + [ctypes.c_size_t, V]),
+                    ("ssd_causal_conv_step_inplace", [PV] + [V] * 8),
+                    ("ssd_selective_scan_workspace_size", [PS, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+                    ("ssd_selective_scan_varlen_fwd_inplace", [PS] + [V] * 14 + [ctypes.c_size_t, V]),
+                    ("ssd_selective_scan_varlen_fwd", [PS] + [V] * 13 + [ctypes.c_size_t, V]),
+                    ("ssd_selective_scan_varlen_bwd", [PS] + [V] * 22 + [ctypes.c_size_t, V]),
+                    ("ssd_selective_scan_step_inplace", [PS] + [V] * 13)):
                 getattr(lib, name).restype = ctypes.c_int
                 getattr(lib, name).argtypes = args
             _lib = lib
@@ -696,3 +738,331 @@ def ssd_state_dequantize(pool, codes, scales, pool_indices, entry_indices, *, st
     prob, dev, (p, c, f, i, j) = _state_cache(pool, codes, scales, pool_indices, entry_indices)
     fn = load_library().ssd_state_dequantize
     _launch("ssd_state_dequantize", dev, stream, lambda st: fn(prob, p, c, f, i, j, st))
+
+
+# ---------------------------------------------------------------------------
+# the norm, the short convolution and the selective scan, checked in the same way
+
+def ssd_rms_norm_workspace_size(prob: ssd_norm_problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().ssd_rms_norm_workspace_size(ctypes.byref(prob), ctypes.byref(n)),
+           "ssd_rms_norm_workspace_size")
+    return n.value
+
+
+def ssd_causal_conv_workspace_size(prob: ssd_conv_problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().ssd_causal_conv_workspace_size(ctypes.byref(prob), ctypes.byref(n)),
+           "ssd_causal_conv_workspace_size")
+    return n.value
+
+
+def ssd_selective_scan_workspace_size(prob: ssd_selective_problem, backward=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().ssd_selective_scan_workspace_size(ctypes.byref(prob), 1 if backward else 0,
+                                                            ctypes.byref(n)), "ssd_selective_scan_workspace_size")
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_sizes(backward, *sizes):
+    prob = ssd_norm_problem(*sizes)
+    return ctypes.byref(prob), ssd_rms_norm_workspace_size(prob) if backward else 0
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_sizes(backward, *sizes):
+    prob = ssd_conv_problem(*sizes)
+    return ctypes.byref(prob), ssd_causal_conv_workspace_size(prob) if backward else 0
+
+
+@functools.lru_cache(maxsize=256)
+def _selective_sizes(backward, *sizes):
+    """``backward`` None: of single tokens, which need no workspace and have wider limits"""
+    prob = ssd_selective_problem(*sizes)
+    return ctypes.byref(prob), 0 if backward is None else ssd_selective_scan_workspace_size(prob, backward)
+
+
+def _hip_device(t, name, dims):
+    if torch is None:
+        _import_torch()
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != len(dims):
+        raise ValueError(f"{name} must be [{', '.join(dims)}]")
+    if t.device.type != "cuda":
+        raise ValueError("libssd runs on a HIP device; got tensors on " + str(t.device))
+    return t.device
+
+
+def _row_stride(t, name, shape, device, step):
+    """Elements between the rows of a bf16 tensor whose rows are dense (a slice of a wider projection is one), a
+    multiple of ``step``; 0 for a dense tensor."""
+    if t is None or t.dtype != torch.bfloat16 or t.shape != shape or t.device != device:
+        _refuse_tensor(t, name, torch.bfloat16, shape, device)
+    if t.is_contiguous():
+        return 0
+    row = 1
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != row:
+            raise ValueError(f"{name}: the elements of a row must be dense")
+        row *= n
+    if shape[0] > 1 and (t.stride(0) < row or t.stride(0) % step != 0):
+        raise ValueError(f"{name}: the stride between rows must be a multiple of {step} elements, at least {row}")
+    return t.stride(0) if shape[0] > 1 else 0
+
+
+def ssd_rms_norm_fwd(y, scales, residual_out, x, residual, weight, *, eps=1e-5, stream=None):
+    """Root-mean-square norm with the residual's addition (see include/ssd.h):
+    r = residual + x, y = r / sqrt(mean(r^2) + eps) * weight.
+
+    x bf16 [rows,width] (rows may have a stride, a multiple of 8); residual and
+    residual_out fp32 or bf16 [rows,width] (one buffer will do), or both None;
+    weight fp32 [width].  y bf16 with ``scales`` None, or int8 or
+    float8_e4m3fn codes with ``scales`` fp32 [rows].
+    """
+    dev = _hip_device(x, "x", ("rows", "width"))
+    shape = rows, width = x.shape
+    kinds = {torch.bfloat16: OUT_BF16, torch.int8: CODE_I8, torch.float8_e4m3fn: CODE_E4M3}
+    if y is None or y.dtype not in kinds:
+        raise TypeError("y: expected bfloat16, int8 or float8_e4m3fn, got " + str(None if y is None else y.dtype))
+    form = kinds[y.dtype]
+    if (scales is None) != (form == OUT_BF16):
+        raise ValueError("scales go with 8-bit codes, and with them only")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    kind = STATE_BF16 if residual is None else _state_dtype(residual, "residual")
+    prob, _ = _norm_sizes(False, rows, width, kind, form, float(eps), _row_stride(x, "x", shape, dev, 8))
+    out = _dense(y, "y", y.dtype, shape, dev)
+    s = None if scales is None else _dense(scales, "scales", torch.float32, (rows,), dev)
+    r = r_out = None
+    if residual is not None:
+        r = _dense(residual, "residual", residual.dtype, shape, dev)
+        r_out = _dense(residual_out, "residual_out", residual.dtype, shape, dev)
+    w = _dense(weight, "weight", torch.float32, (width,), dev)
+    f = load_library().ssd_rms_norm_fwd
+    _launch("ssd_rms_norm_fwd", dev, stream, lambda st: f(prob, out, s, r_out, x.data_ptr(), r, w, st))
+
+
+def ssd_rms_norm_bwd(dx, d_residual, dweight, r, weight, d_y, d_r, *, eps=1e-5, workspace=None, stream=None):
+    """Backward pass of ssd_rms_norm_fwd with y in bf16 (see include/ssd.h):
+    dx bf16 [rows,width], d_residual (the type of ``r``, or None: dx serves both
+    where that is bf16) and dweight fp32 [width] are written.  ``r`` is the forward
+    pass's residual_out (its x where there was no residual), ``d_r`` the gradient
+    of residual_out or None.  Returns the workspace tensor.
+    """
+    dev = _hip_device(r, "r", ("rows", "width"))
+    shape = rows, width = r.shape
+    kind = _state_dtype(r, "r")
+    prob, need = _norm_sizes(True, rows, width, kind, OUT_BF16, float(eps), 0)
+    out = _dense(dx, "dx", torch.bfloat16, shape, dev)
+    d_res = None if d_residual is None else _dense(d_residual, "d_residual", r.dtype, shape, dev)
+    dw = _dense(dweight, "dweight", torch.float32, (width,), dev)
+    a = _dense(r, "r", r.dtype, shape, dev)
+    w = _dense(weight, "weight", torch.float32, (width,), dev)
+    g = _dense(d_y, "d_y", torch.bfloat16, shape, dev)
+    gr = None if d_r is None else _dense(d_r, "d_r", r.dtype, shape, dev)
+    f = load_library().ssd_rms_norm_bwd
+    return _run("ssd_rms_norm_bwd", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, out, d_res, dw, a, w, g, gr, ws, n, st))
+
+
+def _causal_conv(x, weight, bias, batch, slots, silu, backward):
+    """Problem and workspace bytes of a convolution call, device, shape of a state, addresses of x, weight and bias."""
+    dev = _hip_device(x, "x", ("T", "channels"))
+    T, D = x.shape
+    if weight is None or weight.dim() != 2:
+        raise ValueError("weight must be [channels, width]")
+    W = weight.shape[1]
+    prob, need = _conv_sizes(backward, T, batch, D, W, slots, 1 if silu else 0, _row_stride(x, "x", (T, D), dev, 8))
+    w = _dense(weight, "weight", torch.float32, (D, W), dev)
+    b = None if bias is None else _dense(bias, "bias", torch.float32, (D,), dev)
+    return prob, need, dev, (W - 1, D), (x.data_ptr(), w, b)
+
+
+def ssd_causal_conv_varlen_fwd_inplace(y, x, weight, bias, pool, query_start_loc, has_initial_state, cache_indices, *,
+                                       silu=True, stream=None):
+    """Short causal depthwise convolution over a ragged batch, pool of last
+    inputs updated in place (see include/ssd.h).
+
+    y, x bf16 [T,channels] (x may be a slice of a projection: a stride between
+    tokens that is a multiple of 8); weight fp32 [channels,width], width 2 to 4;
+    bias fp32 [channels] or None; pool bf16 [S,width-1,channels];
+    query_start_loc, has_initial_state and cache_indices as for
+    ssd_linear_attn_varlen_fwd_inplace.
+    """
+    batch, slots = query_start_loc.numel() - 1, pool.shape[0]
+    prob, _, dev, state, inputs = _causal_conv(x, weight, bias, batch, slots, silu, False)
+    out = _dense(y, "y", torch.bfloat16, x.shape, dev)
+    states = _dense(pool, "pool", torch.bfloat16, (slots, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
+    f = load_library().ssd_causal_conv_varlen_fwd_inplace
+    _launch("ssd_causal_conv_varlen_fwd_inplace", dev, stream, lambda st: f(
+        prob, out, *inputs, states, qsl, flags, idx, st))
+
+
+def ssd_causal_conv_varlen_fwd(y, x, weight, bias, initial_states, final_states, query_start_loc, *, silu=True,
+                               stream=None):
+    """The same with separate states bf16 [batch,width-1,channels]: sequence b
+    follows ``initial_states[b]`` (None or empty: zeros) and leaves
+    ``final_states[b]``."""
+    batch = query_start_loc.numel() - 1
+    prob, _, dev, state, inputs = _causal_conv(x, weight, bias, batch, max(batch, 1), silu, False)
+    out = _dense(y, "y", torch.bfloat16, x.shape, dev)
+    first = _dense_or_none(initial_states, "initial_states", torch.bfloat16, (batch, *state), dev)
+    last = _dense(final_states, "final_states", torch.bfloat16, (batch, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    f = load_library().ssd_causal_conv_varlen_fwd
+    _launch("ssd_causal_conv_varlen_fwd", dev, stream, lambda st: f(prob, out, *inputs, first, last, qsl, st))
+
+
+def ssd_causal_conv_varlen_bwd(dx, dweight, dbias, d_initial_states, x, weight, bias, d_y, initial_states,
+                               d_final_states, query_start_loc, *, silu=True, workspace=None, stream=None):
+    """Backward pass of ssd_causal_conv_varlen_fwd (see include/ssd.h): dx bf16
+    [T,channels], dweight fp32 [channels,width], dbias fp32 [channels] (or None)
+    and ``d_initial_states`` (or None) are written.  Returns the workspace tensor.
+    """
+    batch = query_start_loc.numel() - 1
+    prob, need, dev, state, inputs = _causal_conv(x, weight, bias, batch, max(batch, 1), silu, True)
+    bf16, f32 = torch.bfloat16, torch.float32
+    out = _dense(dx, "dx", bf16, x.shape, dev)
+    dw = _dense(dweight, "dweight", f32, weight.shape, dev)
+    db = None if dbias is None else _dense(dbias, "dbias", f32, (x.shape[1],), dev)
+    d_first = None if d_initial_states is None else _dense(d_initial_states, "d_initial_states", bf16,
+                                                           (batch, *state), dev)
+    g = _dense(d_y, "d_y", bf16, x.shape, dev)
+    first = _dense_or_none(initial_states, "initial_states", bf16, (batch, *state), dev)
+    d_last = _dense_or_none(d_final_states, "d_final_states", bf16, (batch, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    f = load_library().ssd_causal_conv_varlen_bwd
+    return _run("ssd_causal_conv_varlen_bwd", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, out, dw, db, d_first, *inputs, g, first, d_last, qsl, ws, n, st))
+
+
+def ssd_causal_conv_step_inplace(y, x, weight, bias, pool, has_initial_state, cache_indices, *, silu=True,
+                                 stream=None):
+    """One token per sequence (see include/ssd.h): row b of y and x is sequence
+    b's token; other arguments as for ssd_causal_conv_varlen_fwd_inplace."""
+    batch, slots = x.shape[0], pool.shape[0]
+    prob, _, dev, state, inputs = _causal_conv(x, weight, bias, batch, slots, silu, False)
+    out = _dense(y, "y", torch.bfloat16, x.shape, dev)
+    states = _dense(pool, "pool", torch.bfloat16, (slots, *state), dev)
+    idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
+    f = load_library().ssd_causal_conv_step_inplace
+    _launch("ssd_causal_conv_step_inplace", dev, stream, lambda st: f(prob, out, *inputs, states, flags, idx, st))
+
+
+def _selective(x, dt, A, B, C, D, z, dt_bias, batch, slots, state_dtype, dt_softplus, backward):
+    """Problem and workspace bytes of a selective-scan call, device, shape of a state, addresses of x, dt, A, B, C,
+    D, z and dt_bias."""
+    dev = _hip_device(x, "x", ("T", "channels"))
+    tokens = T, ch = x.shape
+    if B is None or B.dim() != 3:
+        raise ValueError("B must be [T, groups, dstate]")
+    _, G, N = bc = B.shape
+    if bc[0] != T:
+        _refuse_tensor(B, "B", torch.bfloat16, (T, G, N), dev)
+    prob, need = _selective_sizes(
+        backward, T, batch, ch, G, N, slots, 1 if dt_softplus else 0, state_dtype,
+        _row_stride(x, "x", tokens, dev, 8), _row_stride(dt, "dt", tokens, dev, 8),
+        0 if z is None else _row_stride(z, "z", tokens, dev, 8), _row_stride(B, "B", bc, dev, 2),
+        _row_stride(C, "C", bc, dev, 2))
+    f32 = torch.float32
+    return prob, need, dev, (ch, N), (
+        x.data_ptr(), dt.data_ptr(), _dense(A, "A", f32, (ch, N), dev), B.data_ptr(), C.data_ptr(),
+        None if D is None else _dense(D, "D", f32, (ch,), dev), None if z is None else z.data_ptr(),
+        None if dt_bias is None else _dense(dt_bias, "dt_bias", f32, (ch,), dev))
+
+
+def ssd_selective_scan_varlen_fwd_inplace(y, x, dt, A, B, C, D, z, dt_bias, pool, query_start_loc, has_initial_state,
+                                          cache_indices, *, dt_softplus=True, workspace=None, stream=None):
+    """Selective scan (a decay per channel and state) over a ragged batch, pool
+    updated in place (see include/ssd.h).
+
+    y bf16 [T,channels]; x, dt, z bf16 [T,channels] and B, C bf16 [T,G,N]
+    (slices of projections will do: a stride between tokens that is a multiple of
+    8, of B and C even); A fp32 [channels,N]; D, dt_bias fp32 [channels] or None;
+    z None for no gate; pool fp32 or bf16 [S,channels,N]; query_start_loc,
+    has_initial_state and cache_indices as for
+    ssd_linear_attn_varlen_fwd_inplace.  Returns the workspace tensor (None where
+    none is needed).
+    """
+    batch, slots = query_start_loc.numel() - 1, pool.shape[0]
+    prob, need, dev, state, inputs = _selective(x, dt, A, B, C, D, z, dt_bias, batch, slots,
+                                                _state_dtype(pool, "pool"), dt_softplus, False)
+    out = _dense(y, "y", torch.bfloat16, x.shape, dev)
+    states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
+    f = load_library().ssd_selective_scan_varlen_fwd_inplace
+    return _run("ssd_selective_scan_varlen_fwd_inplace", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, out, *inputs, states, qsl, flags, idx, ws, n, st))
+
+
+def ssd_selective_scan_varlen_fwd(y, x, dt, A, B, C, D, z, dt_bias, initial_states, final_states, query_start_loc, *,
+                                  dt_softplus=True, workspace=None, stream=None):
+    """The same with separate states [batch,channels,N]: sequence b starts from
+    ``initial_states[b]`` (None or empty: zero) and leaves ``final_states[b]``;
+    both fp32 or both bf16.  Returns the workspace tensor."""
+    batch = query_start_loc.numel() - 1
+    if final_states is None:
+        raise ValueError("final_states is required")
+    prob, need, dev, state, inputs = _selective(x, dt, A, B, C, D, z, dt_bias, batch, max(batch, 1),
+                                                _state_dtype(final_states, "final_states"), dt_softplus, False)
+    out = _dense(y, "y", torch.bfloat16, x.shape, dev)
+    first = _dense_or_none(initial_states, "initial_states", final_states.dtype, (batch, *state), dev)
+    last = _dense(final_states, "final_states", final_states.dtype, (batch, *state), dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    f = load_library().ssd_selective_scan_varlen_fwd
+    return _run("ssd_selective_scan_varlen_fwd", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, out, *inputs, first, last, qsl, ws, n, st))
+
+
+def ssd_selective_scan_varlen_bwd(dx, ddt, dA, dB, dC, dD, dz, ddt_bias, d_initial_states, x, dt, A, B, C, D, z,
+                                  dt_bias, d_y, initial_states, d_final_states, query_start_loc, *, dt_softplus=True,
+                                  workspace=None, stream=None):
+    """Backward pass of ssd_selective_scan_varlen_fwd (see include/ssd.h): dx,
+    ddt, dz bf16 [T,channels] (dz None where z is), dB, dC bf16 [T,G,N], dA fp32
+    [channels,N] are written, and dD, ddt_bias fp32 [channels] and
+    ``d_initial_states`` where they are not None.  State tensors
+    [batch,channels,N], all fp32 or all bf16.  Returns the workspace tensor.
+    """
+    batch = query_start_loc.numel() - 1
+    given = [None if t is None or t.numel() == 0 else t for t in (initial_states, d_final_states)]
+    states = ((d_initial_states, "d_initial_states"), (given[0], "initial_states"), (given[1], "d_final_states"))
+    kind = next((t for t in states if t[0] is not None), None)
+    prob, need, dev, state, inputs = _selective(x, dt, A, B, C, D, z, dt_bias, batch, max(batch, 1),
+                                                STATE_F32 if kind is None else _state_dtype(*kind), dt_softplus, True)
+    if (z is None) != (dz is None):
+        raise ValueError("dz goes with z, and with it only")
+    d_first, first, d_last = (None if t is None else _dense(t, n, kind[0].dtype, (batch, *state), dev)
+                              for t, n in states)
+    bf16, f32 = torch.bfloat16, torch.float32
+    rows, ch = [None if t is None else _dense(t, n, bf16, x.shape, dev)
+                for t, n in ((dx, "dx"), (ddt, "ddt"), (dz, "dz"))], (x.shape[1],)
+    if dx is None or ddt is None:
+        raise ValueError("dx and ddt are required")
+    a = _dense(dA, "dA", f32, A.shape, dev)
+    b, c = (_dense(t, n, bf16, B.shape, dev) for t, n in ((dB, "dB"), (dC, "dC")))
+    d, e = (None if t is None else _dense(t, n, f32, ch, dev) for t, n in ((dD, "dD"), (ddt_bias, "ddt_bias")))
+    g = _dense(d_y, "d_y", bf16, x.shape, dev)
+    qsl = _dense(query_start_loc, "query_start_loc", torch.int32, (batch + 1,), dev)
+    f = load_library().ssd_selective_scan_varlen_bwd
+    return _run("ssd_selective_scan_varlen_bwd", dev, stream, need, workspace, lambda ws, n, st: f(
+        prob, rows[0], rows[1], a, b, c, d, rows[2], e, d_first, *inputs, g, first, d_last, qsl, ws, n, st))
+
+
+def ssd_selective_scan_step_inplace(y, x, dt, A, B, C, D, z, dt_bias, pool, has_initial_state, cache_indices, *,
+                                    dt_softplus=True, stream=None):
+    """One token per sequence by the recurrence (see include/ssd.h): row b of y,
+    x, dt, B, C, z is sequence b's token; other arguments as for
+    ssd_selective_scan_varlen_fwd_inplace.  One kernel, no workspace."""
+    batch, slots = x.shape[0], pool.shape[0]
+    prob, _, dev, state, inputs = _selective(x, dt, A, B, C, D, z, dt_bias, batch, slots,
+                                             _state_dtype(pool, "pool"), dt_softplus, None)
+    out = _dense(y, "y", torch.bfloat16, x.shape, dev)
+    states = _dense(pool, "pool", pool.dtype, (slots, *state), dev)
+    idx, flags = _slots(cache_indices, has_initial_state, batch, dev)
+    f = load_library().ssd_selective_scan_step_inplace
+    _launch("ssd_selective_scan_step_inplace", dev, stream, lambda st: f(prob, out, *inputs, states, flags, idx, st))

@@ -1,0 +1,193 @@
+// Shared definitions of the operators around and beside the scan: the norm,
+// the short convolution and the selective scan.
+#pragma once
+
+#include "ssd_common.hpp"
+
+namespace ssd {
+namespace layer {
+
+// ---------------------------------------------------------------- pieces
+
+// 8 consecutive bf16 as floats, and back (16 bytes)
+__device__ __forceinline__ void widen8(const u32x4 &v, float (&o)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        o[2 * k] = bf16x2_lo(v[k]);
+        o[2 * k + 1] = bf16x2_hi(v[k]);
+    }
+}
+__device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
+    return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// 1 / (1 + e^-x) with the hardware's exponential and reciprocal: 0 and 1 at the
+// ends of the range.
+__device__ __forceinline__ float sigmoid_f(float x) {
+    return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * x));
+}
+
+// sums over a wavefront, in every lane
+__device__ __forceinline__ float wave_sum(float v) {
+    v = dpp_add_all<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_add_all<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_add_all<0x141>(v);  // row_half_mirror
+    v = dpp_add_all<0x140>(v);  // row_mirror
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+    return v;
+}
+
+// ---------------------------------------------------------------- ragged batches
+
+// Where a sequence lies: rows begin .. begin + len - 1.  Boundaries are clamped
+// to 0 .. T, so a wrong table never leads outside the tensors.
+struct Seq {
+    int b, begin, len;
+};
+__device__ __forceinline__ int clamp_row(int v, int T) { return v < 0 ? 0 : v > T ? T : v; }
+__device__ __forceinline__ Seq seq_at(const int32_t *qsl, int b, int T) {
+    const int begin = clamp_row(qsl[b], T), end = clamp_row(qsl[b + 1], T);
+    return Seq{b, begin, end > begin ? end - begin : 0};
+}
+
+// Sequences are cut into pieces of `piece` tokens.  Piece s of sequence b has
+// the place begin / piece + b + s: begin / piece bounds the whole pieces ahead
+// and b the partial ones, so places never meet, and T / piece + batch of them
+// hold all (some stay empty).  Finds the sequence and the piece of a place;
+// false where it is empty (a sequence without tokens has one piece, 0).  All
+// lanes of a wavefront search together, 64 boundaries at a time.
+__device__ __forceinline__ bool find_piece(const int32_t *qsl, int batch, int T, int piece, int place, Seq &seq,
+                                           int &s) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = batch - 1;  // the last b with begin / piece + b <= place
+    while (hi > lo) {
+        const int step = (hi - lo + 63) / 64;
+        const int b = lo + (lane + 1) * step;
+        const bool ahead = b <= hi && clamp_row(qsl[b], T) / piece + b <= place;
+        const uint64_t m = __ballot(ahead);
+        const int k = ~m == 0 ? 64 : __builtin_ctzll(~m);
+        lo += k * step;
+        hi = hi < lo + step - 1 ? hi : lo + step - 1;
+    }
+    seq = seq_at(qsl, lo, T);
+    s = place - (seq.begin / piece + lo);
+    return s >= 0 && (s == 0 || (int64_t)s * piece < seq.len);
+}
+
+// ---------------------------------------------------------------- norm
+
+struct NormParams {
+    int64_t rows, xs;
+    int width;
+    float eps;
+    int res_bf16, out;  // out: SSD_OUT_BF16, SSD_CODE_I8 or SSD_CODE_E4M3
+    void *y;
+    float *scales;
+    void *res_out;
+    const uint16_t *x;
+    const void *res;
+    const float *weight;
+};
+// threads of the launch, which 32 bits have to hold
+int64_t norm_threads(int64_t rows, int width);
+hipError_t launch_norm(const NormParams &p, hipStream_t s);
+
+struct NormGradParams {
+    int64_t rows;
+    int width;
+    float eps;
+    int res_bf16;
+    uint16_t *dx;
+    void *d_res;
+    const void *r;
+    const float *weight;
+    const uint16_t *dy;
+    const void *d_r;
+    float *part;  // [parts][width]
+    float *dweight;
+    int parts;
+};
+int norm_grad_parts(int64_t rows, int width);
+hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s);
+
+// out[j] = sum over i < n of part[i * stride + j], j < width (a multiple of 4,
+// as is the stride)
+hipError_t launch_sum_parts(const float *part, int n, int64_t stride, int64_t width, float *out, hipStream_t s);
+
+// ---------------------------------------------------------------- convolution
+
+struct ConvParams {
+    int T, batch, D;
+    int64_t xs;
+    int silu;
+    uint16_t *y;
+    const uint16_t *x;
+    const float *weight, *bias;
+    const uint16_t *state_in;
+    uint16_t *state_out;
+    const int32_t *qsl;
+    const uint8_t *has_init;
+    const uint32_t *cache_idx;
+    int init_all;
+    uint32_t max_slots;
+    // backward
+    const uint16_t *dy, *d_final;
+    uint16_t *dx, *d_init;
+    float *part;  // [parts][width + 1][D]
+    float *dweight, *dbias;
+    int tile;        // tokens of a piece
+    int64_t places;  // of pieces
+};
+// Tokens of a piece and places, of either direction
+void conv_shape(ConvParams &p, bool backward);
+int64_t conv_parts(const ConvParams &p);
+int64_t conv_threads(const ConvParams &p);
+hipError_t launch_conv(const ConvParams &p, int width, hipStream_t s);
+hipError_t launch_conv_step(const ConvParams &p, int width, hipStream_t s);
+hipError_t launch_conv_grad(const ConvParams &p, int width, hipStream_t s);
+
+// ---------------------------------------------------------------- selective scan
+
+struct ScanParams {
+    int T, batch, D, G, N, Dg;  // Dg: channels of a group
+    int blocks;                 // of 64 channels: G times those of a group
+    int64_t xs, dts, zs, bs, cs;
+    int softplus;
+    uint16_t *y;
+    const uint16_t *x, *dt, *z, *B, *C;
+    const float *A, *Dskip, *bias;
+    const void *state_in;
+    void *state_out;
+    int state_bf16;
+    const int32_t *qsl;
+    const uint8_t *has_init;
+    const uint32_t *cache_idx;
+    int init_all;
+    uint32_t max_slots;
+    // sequences of more than `seg` tokens are cut into segments of that many
+    int seg;
+    int64_t places;  // of segments
+    int64_t cut_places, cuts;  // of segments of cut sequences; most of those sequences
+    float *parts;    // [cut_places][D][N]: the states that segments leave, from zero but the first
+    float *steps;    // [cut_places][D]: sums of their time steps
+    // backward
+    const uint16_t *dy;
+    const void *d_final;
+    uint16_t *dx, *ddt, *dz, *dB, *dC;
+    void *d_init;
+    float *dA, *dD, *dbias;
+    float *adj;      // [cut_places][D][N]: the same of the gradient, backwards, from zero but the last
+    float *marks;    // [tiles][N / 4][D][4]: the state ahead of each tile of kGradTile tokens
+    float *bc;       // [blocks][T][2][N]: dC and dB of 64 channels
+    float *dA_part, *dD_part;  // [places][D][N], [places][2][D]
+};
+constexpr int kGradTile = 8;
+void scan_shape(ScanParams &p, bool backward);
+int64_t scan_threads(const ScanParams &p, bool backward);
+hipError_t launch_scan(const ScanParams &p, hipStream_t s);
+hipError_t launch_scan_grad(const ScanParams &p, hipStream_t s);
+hipError_t launch_scan_step(const ScanParams &p, hipStream_t s);
+
+}  // namespace layer
+}  // namespace ssd

@@ -1,0 +1,303 @@
+// Root-mean-square norm with the residual's addition, its 8-bit outputs and
+// its backward pass.  A row lies in the registers of 64, 256 or 1024 threads, 8
+// consecutive elements each, so it is read once; the sums over it are fp32.
+#include "ssd.h"
+#include "ssd_layer.hpp"
+#include "ssd_state_cache.hpp"
+
+namespace ssd {
+namespace layer {
+namespace {
+
+// ROWS rows of TPR threads each in a block
+template <int TPR>
+struct Team {
+    static constexpr int kRows = TPR == 64 ? 4 : 1;
+    static constexpr int kThreads = TPR * kRows;
+    static constexpr int kWaves = TPR / 64;
+};
+
+// sums over the threads of a row, in all of them; `buf` holds a float a wave
+// (for each of the sums), and a barrier has to pass before it is used again
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 v, float2 *buf) {
+    v.x = wave_sum(v.x);
+    v.y = wave_sum(v.y);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) buf[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) {
+            v.x += buf[w].x;
+            v.y += buf[w].y;
+        }
+    }
+    return v;
+}
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *buf) {
+    v = wave_max_u32(v);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) buf[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) v = v > buf[w] ? v : buf[w];
+    }
+    return v;
+}
+
+__device__ __forceinline__ void load8(const void *base, int64_t at, bool bf16, float (&o)[8]) {
+    if (bf16)
+        load_state8<true>(base, at, o);
+    else
+        load_state8<false>(base, at, o);
+}
+
+template <int TPR, int VPT>
+__global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm(NormParams p) {
+    __shared__ float2 sums[16];
+    __shared__ uint32_t tops[16];
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * Team<TPR>::kRows + threadIdx.x / TPR;
+    const bool live = row < p.rows;
+    float r[VPT][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * TPR) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] = 0.f;
+        if (live && c < p.width) load_state8<true>(p.x, row * p.xs + c, r[v]);
+    }
+    if (p.res != nullptr) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * TPR) * 8;
+            if (!live || c >= p.width) continue;
+            const int64_t at = row * p.width + c;
+            float a[8];
+            load8(p.res, at, p.res_bf16, a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[v][e] += a[e];
+            if (p.res_bf16) {
+                // the stream is held in bf16: what is normed is what is held
+                const u32x4 w = narrow8(r[v]);
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.res_out) + at) = w;
+                widen8(w, r[v]);
+            } else {
+                store_state8<false>(p.res_out, at, r[v]);
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(r[v][e], r[v][e], sum);
+    sum = row_sum<TPR>(make_float2(sum, 0.f), sums).x;
+    const float s = 1.f / sqrtf(sum / (float)p.width + p.eps);
+    uint32_t top = 0;  // magnitudes order as their bits, infinities and NaN last
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * TPR) * 8;
+        if (c >= p.width) continue;
+        float w[8];
+        load_state8<false>(p.weight, c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            r[v][e] *= s * w[e];
+            const uint32_t m = __float_as_uint(r[v][e]) & 0x7FFFFFFFu;
+            top = top > m ? top : m;
+        }
+    }
+    if (p.out == SSD_OUT_BF16) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * TPR) * 8;
+            if (live && c < p.width)
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.y) + row * p.width + c) = narrow8(r[v]);
+        }
+        return;
+    }
+    top = row_max<TPR>(top, tops);
+    const bool finite = top < 0x7F800000u;
+    float scale, inv;
+    if (p.out == SSD_CODE_E4M3) {
+        const int k = e4m3_scale_exponent(top);
+        scale = top == 0 ? 0.f : __uint_as_float((uint32_t)k << 23);
+        inv = __uint_as_float((uint32_t)(254 - k) << 23);  // exact
+    } else {
+        scale = code_scale(__uint_as_float(top));
+        if (scale < 1.17549435e-38f) scale = 0.f;
+        inv = __builtin_amdgcn_rcpf(scale);
+    }
+    const bool codes = scale > 0.f && finite;
+    if (!finite) scale = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * TPR) * 8;
+        if (!live || c >= p.width) continue;
+        uint32_t q[2] = {};
+        if (codes && p.out == SSD_CODE_E4M3) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(r[v][4 * i] * inv, r[v][4 * i + 1] * inv, 0, false);
+                q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(r[v][4 * i + 2] * inv, r[v][4 * i + 3] * inv, q[i], true);
+            }
+        } else if (codes) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                q[e / 4] |= (uint32_t)(nearest_code(r[v][e], scale, inv) & 0xFF) << (8 * (e % 4));
+        }
+        *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(p.y) + row * p.width + c) = u32x2{q[0], q[1]};
+    }
+    if (live && t == 0) p.scales[row] = scale;
+}
+
+// Gradient: with u = w dy, d = s u - s^3 r mean(u r) + d_r.  Each row's team walks
+// over rows and keeps its share of sum s r dy in registers.
+template <int TPR, int VPT>
+__global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradParams p) {
+    __shared__ float2 sums[2][16];
+    const int t = threadIdx.x % TPR;
+    const int team = blockIdx.x * Team<TPR>::kRows + threadIdx.x / TPR;
+    const int teams = gridDim.x * Team<TPR>::kRows;
+    float w[VPT][8], dw[VPT][8];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * TPR) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[v][e] = dw[v][e] = 0.f;
+        if (c < p.width) load_state8<false>(p.weight, c, w[v]);
+    }
+    const float share = 1.f / (float)p.width;
+    // every team of a block takes as many turns (they share barriers)
+    const int64_t turns = (p.rows + teams - 1) / teams;
+    for (int64_t n = 0; n < turns; ++n) {
+        const int64_t row = n * teams + team;
+        const bool live = row < p.rows;
+        float r[VPT][8], u[VPT][8];
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * TPR) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[v][e] = u[v][e] = 0.f;
+            if (live && c < p.width) {
+                load8(p.r, row * p.width + c, p.res_bf16, r[v]);
+                load_state8<true>(p.dy, row * p.width + c, u[v]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sum.x = __builtin_fmaf(r[v][e], r[v][e], sum.x);
+                sum.y = __builtin_fmaf(u[v][e] * w[v][e], r[v][e], sum.y);
+            }
+        sum = row_sum<TPR>(sum, sums[n & 1]);
+        const float s = 1.f / sqrtf(sum.x * share + p.eps);
+        const float k = s * s * s * (sum.y * share);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * TPR) * 8;
+            if (!live || c >= p.width) continue;
+            const int64_t at = row * p.width + c;
+            float d[8] = {};
+            if (p.d_r != nullptr) load8(p.d_r, at, p.res_bf16, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[v][e] = __builtin_fmaf(s * r[v][e], u[v][e], dw[v][e]);
+                d[e] += s * (u[v][e] * w[v][e]) - k * r[v][e];
+            }
+            *reinterpret_cast<u32x4 *>(p.dx + at) = narrow8(d);
+            if (p.d_res != nullptr) {
+                if (p.res_bf16)
+                    store_state8<true>(p.d_res, at, d);
+                else
+                    store_state8<false>(p.d_res, at, d);
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * TPR) * 8;
+        if (c < p.width) store_state8<false>(p.part, (int64_t)team * p.width + c, dw[v]);
+    }
+}
+
+// Sums of parts: 16 threads of 4 columns each, 16 parts at a time.
+__global__ __launch_bounds__(256) void sum_parts(const float *part, int n, int64_t stride, int64_t width, float *out) {
+    __shared__ f32x4 buf[16][16];
+    const int col = threadIdx.x % 16, first = threadIdx.x / 16;
+    const int64_t j = ((int64_t)blockIdx.x * 16 + col) * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (j < width)
+#pragma unroll 4
+        for (int i = first; i < n; i += 16) s += *reinterpret_cast<const f32x4 *>(part + i * stride + j);
+    buf[first][col] = s;
+    __syncthreads();
+    if (first == 0 && j < width) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += buf[i][col];
+        *reinterpret_cast<f32x4 *>(out + j) = s;
+    }
+}
+
+template <int TPR, int VPT>
+hipError_t norm_as(const NormParams &p, hipStream_t s) {
+    constexpr int rows = Team<TPR>::kRows;
+    rms_norm<TPR, VPT><<<dim3((unsigned)((p.rows + rows - 1) / rows)), Team<TPR>::kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+template <int TPR, int VPT>
+hipError_t norm_grad_as(const NormGradParams &p, hipStream_t s) {
+    rms_norm_grad<TPR, VPT><<<dim3((unsigned)(p.parts / Team<TPR>::kRows)), Team<TPR>::kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+constexpr int kWide = 2048;  // above this width a row has 256 threads
+}  // namespace
+
+int64_t norm_threads(int64_t rows, int width) {
+    if (rows > UINT32_MAX) return rows;
+    return rows * (width <= kWide ? 64 : width <= 16384 ? 256 : 1024) + 255;
+}
+
+hipError_t launch_norm(const NormParams &p, hipStream_t s) {
+    if (p.width <= 512) return norm_as<64, 1>(p, s);
+    if (p.width <= 1024) return norm_as<64, 2>(p, s);
+    if (p.width <= kWide) return norm_as<64, 4>(p, s);
+    if (p.width <= 4096) return norm_as<256, 2>(p, s);
+    if (p.width <= 8192) return norm_as<256, 4>(p, s);
+    if (p.width <= 16384) return norm_as<256, 8>(p, s);
+    return norm_as<1024, 4>(p, s);
+}
+
+int norm_grad_parts(int64_t rows, int width) {
+    const int per_block = width <= 1024 ? 4 : 1;
+    const int64_t blocks = (rows + per_block - 1) / per_block;
+    return (int)(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024) * per_block;
+}
+
+hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s) {
+    hipError_t e;
+    if (p.width <= 512) e = norm_grad_as<64, 1>(p, s);
+    else if (p.width <= 1024) e = norm_grad_as<64, 2>(p, s);
+    else if (p.width <= 2048) e = norm_grad_as<256, 1>(p, s);
+    else if (p.width <= 4096) e = norm_grad_as<256, 2>(p, s);
+    else if (p.width <= 8192) e = norm_grad_as<256, 4>(p, s);
+    else if (p.width <= 16384) e = norm_grad_as<1024, 2>(p, s);
+    else e = norm_grad_as<1024, 4>(p, s);
+    if (e != hipSuccess) return e;
+    return launch_sum_parts(p.part, p.parts, p.width, p.width, p.dweight, s);
+}
+
+hipError_t launch_sum_parts(const float *part, int n, int64_t stride, int64_t width, float *out, hipStream_t s) {
+    sum_parts<<<dim3((unsigned)((width + 63) / 64)), 256, 0, s>>>(part, n, stride, width, out);
+    return hipGetLastError();
+}
+
+}  // namespace layer
+}  // namespace ssd

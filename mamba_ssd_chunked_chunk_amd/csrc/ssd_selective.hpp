@@ -1,0 +1,99 @@
+// What the kernels of the selective scan share.
+#pragma once
+
+#include "ssd_layer.hpp"
+
+namespace ssd {
+namespace layer {
+
+constexpr int kTile = 16;  // tokens between two hand-overs of a walk
+
+// What a workgroup works on.
+struct Span {
+    int g, c0, ch0;  // group, first channel in it and in all
+    int nch;         // channels, up to 64
+};
+__device__ __forceinline__ Span span_of(const ScanParams &p, int block) {
+    const int per = p.blocks / p.G;
+    Span w;
+    w.g = block / per;
+    w.c0 = (block % per) * 64;
+    w.ch0 = w.g * p.Dg + w.c0;
+    w.nch = min(64, p.Dg - w.c0);
+    return w;
+}
+
+__device__ __forceinline__ void widen4(const u32x2 &v, float (&o)[4]) {
+    o[0] = bf16x2_lo(v[0]);
+    o[1] = bf16x2_hi(v[0]);
+    o[2] = bf16x2_lo(v[1]);
+    o[3] = bf16x2_hi(v[1]);
+}
+
+__device__ __forceinline__ float time_step(const ScanParams &p, float raw, int ch) {
+    if (p.bias != nullptr) raw += p.bias[ch];
+    return p.softplus ? softplus_f(raw) : raw;
+}
+
+// 4 bf16 at an address that is the same in all lanes: a scalar load (the
+// constant address space says that nothing writes there during the kernel) and
+// the scalar unit's shifts.
+struct Quad {
+    float v[4];
+};
+__device__ __forceinline__ Quad quad_at(const uint16_t *ptr) {
+    typedef const __attribute__((address_space(4))) uint32_t *Scalar;
+    const Scalar s = (Scalar)(uintptr_t)ptr;
+    const uint32_t a = s[0], b = s[1];
+    return Quad{{bf16x2_lo(a), bf16x2_hi(a), bf16x2_lo(b), bf16x2_hi(b)}};
+}
+
+// First place of a cut sequence's segments among those of all cut sequences: at
+// most begin / (seg + 1) of them lie ahead of it, each with at most one partial
+// segment.
+__device__ __forceinline__ int64_t cut_place(const ScanParams &p, const Seq &q) {
+    return q.begin / p.seg + min(q.b, q.begin / (p.seg + 1));
+}
+
+// The state that enters segment s > 0 from the states that the segments ahead
+// of it leave (all but the first from zero).  A: times log2(e).
+__device__ __forceinline__ void chain_states(const ScanParams &p, int64_t first, int s, int64_t at, int ch,
+                                             const float (&A)[4], float (&h)[4]) {
+    const float *part = p.parts + first * p.D * p.N + at;
+    const float *steps = p.steps + first * p.D + ch;
+    const int64_t row = (int64_t)p.D * p.N;
+#pragma unroll 4
+    for (int j = 0; j < s; ++j) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + j * row);
+        const float d = steps[(int64_t)j * p.D];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = j == 0 ? v[i] : __builtin_fmaf(fast_exp2(d * A[i]), h[i], v[i]);
+    }
+}
+
+// Where the state ahead of token t (a multiple of kGradTile) of a sequence is
+// kept for the backward pass, 4 states of a channel together.
+__device__ __forceinline__ float *mark_at(const ScanParams &p, const Seq &q, int t, int n0, int ch) {
+    const int64_t tile = q.begin / kGradTile + q.b + t / kGradTile;
+    return p.marks + ((tile * (p.N / 4) + n0 / 4) * p.D + ch) * 4;
+}
+
+// wavefronts that hold N states, 4 each
+inline int waves_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 12 ? 3 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+template <typename F>
+void by_waves(int n, F f) {
+    switch (n) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 8: return f(std::integral_constant<int, 8>{});
+    default: return f(std::integral_constant<int, 16>{});
+    }
+}
+
+hipError_t launch_scan_states(const ScanParams &p, hipStream_t s);
+hipError_t launch_scan_marks(const ScanParams &p, hipStream_t s);
+
+}  // namespace layer
+}  // namespace ssd

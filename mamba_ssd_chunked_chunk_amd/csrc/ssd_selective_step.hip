@@ -1,0 +1,111 @@
+// Selective scan, one token per sequence, by the recurrence itself.  A thread
+// holds 4 consecutive states of a channel (16 bytes in fp32) of several
+// sequences, so the decays are read once for all of them; the lanes of a channel
+// add their shares of C.h.  The states are read once and written once, and that
+// is the bound.
+#include "ssd_selective.hpp"
+
+namespace ssd {
+namespace layer {
+namespace {
+constexpr int kThreads = 256;
+
+// sum over each aligned group of LANES lanes
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (LANES >= 2) v = dpp_add_all<0xB1>(v);   // quad_perm [1,0,3,2]
+    if constexpr (LANES >= 4) v = dpp_add_all<0x4E>(v);   // quad_perm [2,3,0,1]
+    if constexpr (LANES >= 8) v = dpp_add_all<0x141>(v);  // row_half_mirror
+    if constexpr (LANES >= 16) v = dpp_add_all<0x140>(v); // row_mirror
+    return v;
+}
+
+// 4 bf16 from a 4-byte boundary on
+__device__ __forceinline__ void load_quad(const uint16_t *ptr, float (&o)[4]) {
+    const uint32_t *s = reinterpret_cast<const uint32_t *>(ptr);
+    widen4(u32x2{s[0], s[1]}, o);
+}
+
+template <int LANES, int SEQS, bool SB>
+__global__ __launch_bounds__(kThreads) void scan_step(ScanParams p, int cblocks) {
+    const int cb = blockIdx.x % cblocks, b0 = blockIdx.x / cblocks * SEQS;
+    const int ch = cb * (kThreads / LANES) + threadIdx.x / LANES, n0 = threadIdx.x % LANES * 4;
+    const bool in = ch < p.D && n0 < p.N;
+    const int64_t at = (int64_t)ch * p.N + n0;
+    float h[SEQS][4];
+    int64_t slot[SEQS];
+#pragma unroll
+    for (int k = 0; k < SEQS; ++k) {
+        const int b = b0 + k;
+        slot[k] = b < p.batch ? (int64_t)p.cache_idx[b] : (int64_t)p.max_slots;  // max_slots or more: nothing
+        const bool init = b < p.batch && p.has_init != nullptr && p.has_init[b] != 0;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (in && init && slot[k] < (int64_t)p.max_slots)
+            v = load_state4<SB>(p.state_in, slot[k] * p.D * p.N + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[k][i] = v[i];
+    }
+    float A[4] = {};
+    if (in) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(p.A + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A[i] = v[i] * kLog2e;
+    }
+    const int g = ch / p.Dg;
+#pragma unroll
+    for (int k = 0; k < SEQS; ++k) {
+        const int64_t b = b0 + k;
+        if (slot[k] >= (int64_t)p.max_slots) continue;
+        float B[4] = {}, C[4] = {}, y = 0.f, x = 0.f;
+        if (in) {
+            load_quad(p.B + b * p.bs + g * p.N + n0, B);
+            load_quad(p.C + b * p.cs + g * p.N + n0, C);
+            x = bf16_bits_to_float(p.x[b * p.xs + ch]);
+            const float step = time_step(p, bf16_bits_to_float(p.dt[b * p.dts + ch]), ch);
+            const float u = step * x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[k][i] = __builtin_fmaf(fast_exp2(step * A[i]), h[k][i], u * B[i]);
+                y = __builtin_fmaf(C[i], h[k][i], y);
+            }
+            store_state4<SB>(p.state_out, slot[k] * p.D * p.N + at, f32x4{h[k][0], h[k][1], h[k][2], h[k][3]});
+        }
+        y = lanes_sum<LANES>(y);
+        if (!in || n0 != 0) continue;
+        if (p.Dskip != nullptr) y = __builtin_fmaf(p.Dskip[ch], x, y);
+        if (p.z != nullptr) {
+            const float z = bf16_bits_to_float(p.z[b * p.zs + ch]);
+            y *= z * sigmoid_f(z);
+        }
+        p.y[b * p.D + ch] = float_to_bf16_bits(y);
+    }
+}
+
+template <int LANES, int SEQS>
+hipError_t launch_as(const ScanParams &p, hipStream_t s) {
+    constexpr int chans = kThreads / LANES;
+    const int cblocks = (p.D + chans - 1) / chans;
+    const dim3 grid((unsigned)((int64_t)cblocks * ((p.batch + SEQS - 1) / SEQS)));
+    if (p.state_bf16)
+        scan_step<LANES, SEQS, true><<<grid, kThreads, 0, s>>>(p, cblocks);
+    else
+        scan_step<LANES, SEQS, false><<<grid, kThreads, 0, s>>>(p, cblocks);
+    return hipGetLastError();
+}
+template <int LANES>
+hipError_t launch_lanes(const ScanParams &p, hipStream_t s) {
+    return p.batch >= 16 ? launch_as<LANES, 4>(p, s) : launch_as<LANES, 1>(p, s);
+}
+}  // namespace
+
+hipError_t launch_scan_step(const ScanParams &p, hipStream_t s) {
+    const int need = p.N / 4;
+    if (need <= 1) return launch_lanes<1>(p, s);
+    if (need <= 2) return launch_lanes<2>(p, s);
+    if (need <= 4) return launch_lanes<4>(p, s);
+    if (need <= 8) return launch_lanes<8>(p, s);
+    return launch_lanes<16>(p, s);
+}
+
+}  // namespace layer
+}  // namespace ssd

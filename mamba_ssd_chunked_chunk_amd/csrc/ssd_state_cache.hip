@@ -12,6 +12,7 @@
 
 #include "ssd_common.hpp"
 #include "ssd_linear_attn.hpp"
+#include "ssd_state_cache.hpp"
 
 namespace ssd {
 namespace {
@@ -36,28 +37,6 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
         v = v > o ? v : o;
     }
     return v;
-}
-
-// x / s to the nearest integer, ties to even, decided on the true quotient:
-// the product with the rounded reciprocal is within one of it, and the
-// remainder x - c s is exact in fp32 (a multiple of half a unit of s's last
-// place, below s in size).
-__device__ __forceinline__ int nearest_code(float x, float s, float inv) {
-    float c = rintf(x * inv);
-    const float r = 2.f * __builtin_fmaf(-c, s, x);
-    const float a = fabsf(r);
-    const bool odd = ((int)c & 1) != 0;
-    if (a > s || (a == s && odd)) c += r > 0.f ? 1.f : -1.f;
-    return (int)c;
-}
-
-// top / 127, correctly rounded: by Markstein's theorem one step from a product
-// with the rounded reciprocal gives it, away from the subnormal range.
-__device__ __forceinline__ float code_scale(float top) {
-    constexpr float inv = 1.f / 127.f;
-    if (top < 0x1p-100f) return top / 127.f;
-    const float q = top * inv;
-    return __builtin_fmaf(__builtin_fmaf(-127.f, q, top), inv, q);
 }
 
 // Where a block works: the pair it moves (or none) and its first row.
@@ -126,9 +105,7 @@ __global__ __launch_bounds__(kThreads) void state_quantize(CacheParams p, const 
         float s;
         uint32_t q[E / 4] = {};
         if constexpr (E4M3) {
-            // top = m 2^e: 448 = 1.75 2^8 holds m <= 1.75 with 2^(e-8)
-            int k = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-            k = k < 1 ? 1 : k;
+            const int k = e4m3_scale_exponent(top);
             s = top == 0 ? 0.f : __uint_as_float((uint32_t)k << 23);
             if (top != 0 && finite) {
                 const float inv = __uint_as_float((uint32_t)(254 - k) << 23);  // exact
