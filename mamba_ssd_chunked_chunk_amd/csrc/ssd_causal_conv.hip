@@ -343,9 +343,9 @@ hipError_t launch_conv_grad(const ConvParams &p, int width, hipStream_t s) {
     hipError_t e = by_width(width, [&](auto w) { conv_grad<decltype(w)::value><<<grid, 256, 0, s>>>(p); });
     if (e != hipSuccess) return e;
     const int64_t row = (int64_t)(width + 1) * p.D;
-    e = launch_sum_parts(p.part, (int)quads, row, (int64_t)width * p.D, p.dweight, s);
-    if (e != hipSuccess || p.dbias == nullptr) return e;
-    return launch_sum_parts(p.part + (int64_t)width * p.D, (int)quads, row, p.D, p.dbias, s);
+    return launch_sums(Sums{{Sum{p.part, (int)quads, row, (int64_t)width * p.D, p.dweight},
+                             Sum{p.part + (int64_t)width * p.D, (int)quads, row, p.D, p.dbias}}},
+                       s);
 }
 
 }  // namespace layer

@@ -112,8 +112,41 @@ int norm_grad_parts(int64_t rows, int width);
 hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s);
 
 // out[j] = sum over i < n of part[i * stride + j], j < width (a multiple of 4,
-// as is the stride)
-hipError_t launch_sum_parts(const float *part, int n, int64_t stride, int64_t width, float *out, hipStream_t s);
+// as is the stride), or nothing where out is null.
+struct Sum {
+    const float *part;
+    int n;
+    int64_t stride, width;
+    float *out;
+};
+struct Sums {
+    Sum s[3];
+};
+constexpr int kSumThreads = 256, kSumColumns = 64;
+inline __host__ __device__ int64_t sum_blocks(const Sum &s) {
+    return s.out == nullptr ? 0 : (s.width + kSumColumns - 1) / kSumColumns;
+}
+// The block-th block of the sums: 16 threads of 4 columns each, 16 parts at a
+// time, in their order.
+__device__ __forceinline__ void add_parts(const Sums &all, int64_t block, f32x4 (&buf)[16][16]) {
+    int k = 0;
+    while (k < 2 && block >= sum_blocks(all.s[k])) block -= sum_blocks(all.s[k++]);
+    const Sum &a = all.s[k];
+    const int col = threadIdx.x % 16, first = threadIdx.x / 16;
+    const int64_t j = block * kSumColumns + col * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (j < a.width)
+#pragma unroll 4
+        for (int i = first; i < a.n; i += 16) s += *reinterpret_cast<const f32x4 *>(a.part + i * a.stride + j);
+    buf[first][col] = s;
+    __syncthreads();
+    if (first == 0 && j < a.width) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += buf[i][col];
+        *reinterpret_cast<f32x4 *>(a.out + j) = s;
+    }
+}
+hipError_t launch_sums(const Sums &sums, hipStream_t s);
 
 // ---------------------------------------------------------------- convolution
 
@@ -165,8 +198,8 @@ struct ScanParams {
     const uint32_t *cache_idx;
     int init_all;
     uint32_t max_slots;
-    // sequences of more than `seg` tokens are cut into segments of that many
-    int seg;
+    // sequences of more than `cut` tokens are cut into segments of `seg`
+    int seg, cut;
     int64_t places;  // of segments
     int64_t cut_places, cuts;  // of segments of cut sequences; most of those sequences
     float *parts;    // [cut_places][D][N]: the states that segments leave, from zero but the first

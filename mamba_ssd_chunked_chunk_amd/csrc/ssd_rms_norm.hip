@@ -227,22 +227,9 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
     }
 }
 
-// Sums of parts: 16 threads of 4 columns each, 16 parts at a time.
-__global__ __launch_bounds__(256) void sum_parts(const float *part, int n, int64_t stride, int64_t width, float *out) {
+__global__ __launch_bounds__(kSumThreads) void sum_parts(Sums sums) {
     __shared__ f32x4 buf[16][16];
-    const int col = threadIdx.x % 16, first = threadIdx.x / 16;
-    const int64_t j = ((int64_t)blockIdx.x * 16 + col) * 4;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (j < width)
-#pragma unroll 4
-        for (int i = first; i < n; i += 16) s += *reinterpret_cast<const f32x4 *>(part + i * stride + j);
-    buf[first][col] = s;
-    __syncthreads();
-    if (first == 0 && j < width) {
-#pragma unroll
-        for (int i = 1; i < 16; ++i) s += buf[i][col];
-        *reinterpret_cast<f32x4 *>(out + j) = s;
-    }
+    add_parts(sums, blockIdx.x, buf);
 }
 
 template <int TPR, int VPT>
@@ -291,11 +278,12 @@ hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s) {
     else if (p.width <= 16384) e = norm_grad_as<1024, 2>(p, s);
     else e = norm_grad_as<1024, 4>(p, s);
     if (e != hipSuccess) return e;
-    return launch_sum_parts(p.part, p.parts, p.width, p.width, p.dweight, s);
+    return launch_sums(Sums{{Sum{p.part, p.parts, p.width, p.width, p.dweight}}}, s);
 }
 
-hipError_t launch_sum_parts(const float *part, int n, int64_t stride, int64_t width, float *out, hipStream_t s) {
-    sum_parts<<<dim3((unsigned)((width + 63) / 64)), 256, 0, s>>>(part, n, stride, width, out);
+hipError_t launch_sums(const Sums &sums, hipStream_t s) {
+    const int64_t blocks = sum_blocks(sums.s[0]) + sum_blocks(sums.s[1]) + sum_blocks(sums.s[2]);
+    sum_parts<<<dim3((unsigned)blocks), kSumThreads, 0, s>>>(sums);
     return hipGetLastError();
 }
 

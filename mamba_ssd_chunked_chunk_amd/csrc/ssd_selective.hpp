@@ -30,9 +30,18 @@ __device__ __forceinline__ void widen4(const u32x2 &v, float (&o)[4]) {
     o[3] = bf16x2_hi(v[1]);
 }
 
-__device__ __forceinline__ float time_step(const ScanParams &p, float raw, int ch) {
-    if (p.bias != nullptr) raw += p.bias[ch];
-    return p.softplus ? softplus_f(raw) : raw;
+// softplus without a branch or a division: with z = e^-|v| and u = 1 + z
+// rounded, log1p(z) = log(u) + (z - (u - 1)) / u but for terms of the second
+// order, and the quotient by u in [1, 2] moves the last summand, at most half a
+// unit of u's last place, by less than 2^-24 z.
+__device__ __forceinline__ float softplus_fast(float v) {
+    const float z = fast_exp2(-fabsf(v) * kLog2e);  // in (0, 1]
+    const float u = 1.f + z;
+    const float l = __builtin_fmaf(__builtin_amdgcn_logf(u), kLn2, z - (u - 1.f));
+    return __builtin_amdgcn_fmed3f(v, 0.f, __builtin_inff()) + l;
+}
+__device__ __forceinline__ float time_step(const ScanParams &p, float raw) {
+    return p.softplus ? softplus_fast(raw) : raw;
 }
 
 // 4 bf16 at an address that is the same in all lanes: a scalar load (the
@@ -41,18 +50,56 @@ __device__ __forceinline__ float time_step(const ScanParams &p, float raw, int c
 struct Quad {
     float v[4];
 };
-__device__ __forceinline__ Quad quad_at(const uint16_t *ptr) {
+struct Words {
+    uint32_t b[2], c[2];  // 4 of B and of C
+};
+__device__ __forceinline__ void words_at(const uint16_t *ptr, uint32_t (&w)[2]) {
     typedef const __attribute__((address_space(4))) uint32_t *Scalar;
     const Scalar s = (Scalar)(uintptr_t)ptr;
-    const uint32_t a = s[0], b = s[1];
+    w[0] = s[0];
+    w[1] = s[1];
+}
+__device__ __forceinline__ Quad quad_of(uint32_t a, uint32_t b) {
     return Quad{{bf16x2_lo(a), bf16x2_hi(a), bf16x2_lo(b), bf16x2_hi(b)}};
+}
+__device__ __forceinline__ Quad quad_at(const uint16_t *ptr) {
+    uint32_t w[2];
+    words_at(ptr, w);
+    return quad_of(w[0], w[1]);
 }
 
 // First place of a cut sequence's segments among those of all cut sequences: at
-// most begin / (seg + 1) of them lie ahead of it, each with at most one partial
+// most begin / (cut + 1) of them lie ahead of it, each with at most one partial
 // segment.
 __device__ __forceinline__ int64_t cut_place(const ScanParams &p, const Seq &q) {
-    return q.begin / p.seg + min(q.b, q.begin / (p.seg + 1));
+    return q.begin / p.seg + min(q.b, q.begin / (p.cut + 1));
+}
+
+__device__ __forceinline__ int segments_of(const ScanParams &p, const Seq &q) {
+    return q.len > p.cut ? (q.len + p.seg - 1) / p.seg : 1;
+}
+// The cut sequence and its segment at one of these places; false where none is.
+// (Places never meet, so the sequence is the last whose first place is not
+// behind it.)
+__device__ __forceinline__ bool find_cut(const ScanParams &p, int place, Seq &q, int &s) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = p.batch - 1;
+    while (hi > lo) {
+        const int step = (hi - lo + 63) / 64;
+        const int b = lo + (lane + 1) * step;
+        bool ahead = b <= hi;
+        if (ahead) {
+            const int begin = clamp_row(p.qsl[b], p.T);
+            ahead = begin / p.seg + min(b, begin / (p.cut + 1)) <= place;
+        }
+        const uint64_t m = __ballot(ahead);
+        const int k = ~m == 0 ? 64 : __builtin_ctzll(~m);
+        lo += k * step;
+        hi = hi < lo + step - 1 ? hi : lo + step - 1;
+    }
+    q = seq_at(p.qsl, lo, p.T);
+    s = place - (int)cut_place(p, q);
+    return q.len > p.cut && s >= 0 && (int64_t)s * p.seg < q.len;
 }
 
 // The state that enters segment s > 0 from the states that the segments ahead
@@ -92,7 +139,6 @@ void by_waves(int n, F f) {
     }
 }
 
-hipError_t launch_scan_states(const ScanParams &p, hipStream_t s);
 hipError_t launch_scan_marks(const ScanParams &p, hipStream_t s);
 
 }  // namespace layer

@@ -11,6 +11,8 @@
 // gradients, become one a lane in 6 steps, each of which adds what two lanes
 // hold of half the values.  They leave as fp32 for each 64 channels, and a last
 // kernel adds the blocks of a group, in their order.
+#include <type_traits>
+
 #include "ssd_selective.hpp"
 
 namespace ssd {
@@ -34,15 +36,8 @@ __device__ __forceinline__ float fold_dpp(float a, float b, bool bit) {
     return keep + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(give), CTRL, 0xF, 0xF, false));
 }
 
-// 4 bf16 of a token, or zeros where there is none
-__device__ __forceinline__ Quad quad_or_zero(const uint16_t *row0, int64_t stride, int t, int last) {
-    Quad r = quad_at(row0 + (int64_t)min(t, last) * stride);
-    if (t > last) r = Quad{{0.f, 0.f, 0.f, 0.f}};
-    return r;
-}
-
 // The gradient of the state that leaves segment s, from what the segments
-// behind it pass on from zero (the last one from d_final).
+// behind it pass on: the last one in full, the others from zero.
 __device__ __forceinline__ void chain_back(const ScanParams &p, int64_t first, int s, int nseg, int64_t at, int ch,
                                            const float (&A)[4], float (&u)[4]) {
     const int64_t row = (int64_t)p.D * p.N;
@@ -61,39 +56,39 @@ __device__ __forceinline__ f32x4 final_grad(const ScanParams &p, int64_t at) {
     return p.state_bf16 ? load_state4<true>(p.d_final, at) : load_state4<false>(p.d_final, at);
 }
 
-// What the segments of cut sequences pass on to those ahead of them, from zero
-// but the last: U_t = (U_{t+1} + C_t e_t) a_t down to their first tokens.
 template <int NW>
-__global__ __launch_bounds__(NW * 64) void scan_adjoint(ScanParams p) {
+union Shared {
+    struct {
+        float2 sx[kGradTile][64];      // time step, and times x
+        f32x4 B[kGradTile][NW], C[kGradTile][NW];
+        float e[kGradTile][64];
+        float y[NW][kGradTile][64];    // a wavefront's shares of C.h
+        float2 uq[NW][kGradTile][64];  // and of U.B and q.A
+    };
+    float2 adjoint[kTile][64];  // time step and e
+};
+
+// What a segment between the first and the last passes on to those ahead of it,
+// from zero: U_t = (U_{t+1} + C_t e_t) a_t down to its first token.
+template <int NW>
+__device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, const Seq &q, int s, const Span &w) {
     constexpr int NT = NW * 64, kItems = (kTile * 16 + NT - 1) / NT;
-    __shared__ float2 sin[kTile][64];  // time step and e
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    Seq q;
-    int s;
-    if (!find_piece(p.qsl, p.batch, p.T, p.seg, blockIdx.x / p.blocks, q, s)) return;
-    const int nseg = q.len > p.seg ? (q.len + p.seg - 1) / p.seg : 1;
-    if (s == 0) return;
-    const Span w = span_of(p, blockIdx.x % p.blocks);
-    const int t0 = s * p.seg, t1 = min(q.len, t0 + p.seg), n0 = wave * 4;
+    const int t0 = s * p.seg, n0 = wave * 4;
     const bool mine = lane < w.nch && n0 < p.N;
     const int ch = w.ch0 + (lane < w.nch ? lane : 0);
     const int64_t at = (int64_t)ch * p.N + n0;
     float A[4] = {}, u[4] = {};
-    if (mine) {
-        const f32x4 v = s == nseg - 1 ? final_grad(p, (int64_t)q.b * p.D * p.N + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+    if (mine)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            A[i] = p.A[at + i] * kLog2e;
-            u[i] = v[i];
-        }
-    }
+        for (int i = 0; i < 4; ++i) A[i] = p.A[at + i] * kLog2e;
     const uint16_t *Cp = p.C + (int64_t)q.begin * p.cs + w.g * p.N + n0;
-    for (int t = t0 + (t1 - 1 - t0) / kTile * kTile; t >= t0; t -= kTile) {
+    for (int t = t0 + p.seg - kTile; t >= t0; t -= kTile) {  // (a whole number of tiles)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int i = threadIdx.x + k * NT, r = i / 16, c = (i % 16) * 4;
-            if (i >= kTile * 16 || t + r >= t1 || c >= w.nch) continue;
+            if (i >= kTile * 16 || c >= w.nch) continue;
             const int64_t row = q.begin + t + r;
             float d[4], e[4], z[4];
             widen4(*reinterpret_cast<const u32x2 *>(p.dt + row * p.dts + w.ch0 + c), d);
@@ -104,12 +99,15 @@ __global__ __launch_bounds__(NW * 64) void scan_adjoint(ScanParams p) {
                 for (int j = 0; j < 4; ++j) e[j] *= z[j] * sigmoid_f(z[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sin[r][c + j] = make_float2(time_step(p, d[j], w.ch0 + c + j), e[j]);
+            for (int j = 0; j < 4; ++j)
+                lds.adjoint[r][c + j] = make_float2(
+                    time_step(p, d[j] + (p.bias != nullptr ? p.bias[w.ch0 + c + j] : 0.f)), e[j]);
         }
         __syncthreads();
         if (n0 >= p.N) continue;
-        for (int i = min(kTile, t1 - t) - 1; i >= 0; --i) {
-            const float2 e = sin[i][lane];
+#pragma unroll 4
+        for (int i = kTile - 1; i >= 0; --i) {
+            const float2 e = lds.adjoint[i][lane];
             const Quad C = quad_at(Cp + (int64_t)(t + i) * p.cs);
 #pragma unroll
             for (int j = 0; j < 4; ++j) u[j] = __builtin_fmaf(C.v[j], e.y, u[j]) * fast_exp2(e.x * A[j]);
@@ -119,30 +117,34 @@ __global__ __launch_bounds__(NW * 64) void scan_adjoint(ScanParams p) {
         *reinterpret_cast<f32x4 *>(p.adj + (cut_place(p, q) + s) * p.D * p.N + at) = f32x4{u[0], u[1], u[2], u[3]};
 }
 
+// Adds to a pointer that is the same in all lanes.
+template <typename T>
+__device__ __forceinline__ T *moved(T *base, int64_t bytes) {
+    typedef std::conditional_t<std::is_const<T>::value, const char, char> Byte;
+    return reinterpret_cast<T *>(reinterpret_cast<Byte *>(base) + bytes);
+}
+// ... and reads or writes at a lane's own offset from it, in bytes.
+template <typename V, typename T>
+__device__ __forceinline__ V at_offset(const T *base, uint32_t bytes) {
+    return *reinterpret_cast<const V *>(reinterpret_cast<const char *>(base) + bytes);
+}
+template <typename V, typename T>
+__device__ __forceinline__ void put_offset(T *base, uint32_t bytes, const V &v) {
+    *reinterpret_cast<V *>(reinterpret_cast<char *>(base) + bytes) = v;
+}
+
+// One segment of a sequence (or all of it) and 64 channels.
 template <int NW>
-__global__ __launch_bounds__(NW * 64) void scan_grad(ScanParams p) {
-    constexpr int NT = NW * 64, K = kGradTile, kItems = (K * 32 + NT - 1) / NT;
-    constexpr int kTeams = NT < 256 ? NT / 32 : 8;  // threads that finish the same channels
-    __shared__ float4 sin[K][64];        // time step, times x, e, x
-    __shared__ float part[3][NW][K][64];  // a wavefront's shares of C.h, U.B and q.A
+__device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const Seq &q, int s, int nseg, int block) {
+    constexpr int NT = NW * 64, K = kGradTile, kItems = (K * 32 + NT - 1) / NT, kStep = NT / 32;
+    constexpr int kTeams = NT < 256 ? kStep : 8;  // threads that finish the same channels
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    const int place = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
     const Span w = span_of(p, block);
     const int n0 = wave * 4;
     const bool mine = lane < w.nch && n0 < p.N;
     const int ch = w.ch0 + (lane < w.nch ? lane : 0);
     const int64_t at = (int64_t)ch * p.N + n0;
-    float *dA_to = p.dA_part + (int64_t)place * p.D * p.N + at;
-    float *dD_to = p.dD_part + (int64_t)place * 2 * p.D + w.ch0;
-    Seq q;
-    int s;
-    if (!find_piece(p.qsl, p.batch, p.T, p.seg, place, q, s)) {  // an empty place adds nothing
-        if (mine) *reinterpret_cast<f32x4 *>(dA_to) = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (threadIdx.x < w.nch) dD_to[threadIdx.x] = dD_to[p.D + threadIdx.x] = 0.f;
-        return;
-    }
-    const int nseg = q.len > p.seg ? (q.len + p.seg - 1) / p.seg : 1;
-    const int t0 = s * p.seg, t1 = min(q.len, t0 + p.seg), last = q.len - 1;
+    const int t0 = s * p.seg, t1 = nseg > 1 ? min(q.len, t0 + p.seg) : q.len;
     const int64_t state = (int64_t)q.b * p.D * p.N + at;
 
     float A[4] = {}, u[4] = {}, dA[4] = {};  // u: the gradient of the state behind the walk
@@ -157,9 +159,15 @@ __global__ __launch_bounds__(NW * 64) void scan_grad(ScanParams p) {
             chain_back(p, cut_place(p, q), s, nseg, at, ch, A, u);
         }
     }
-    // the tokens and channels this thread prepares and finishes: 2 channels of a token an item
-    const int c = (threadIdx.x % 32) * 2;
-    const int64_t row0 = q.begin;
+    if (n0 >= p.N) {  // no states, no share
+        for (int i = 0; i < K; ++i) {
+            lds.y[wave][i][lane] = 0.f;
+            lds.uq[wave][i][lane] = make_float2(0.f, 0.f);
+        }
+    }
+    // the tokens and channels this thread prepares and finishes: 2 channels of a token an item, the same ones in
+    // every item
+    const int c = (threadIdx.x % 32) * 2, r0 = threadIdx.x / 32;
     const bool in = c < w.nch;
     float bias[2] = {}, skip[2] = {}, dD[2] = {}, db[2] = {};
 #pragma unroll
@@ -167,154 +175,216 @@ __global__ __launch_bounds__(NW * 64) void scan_grad(ScanParams p) {
         if (in && p.bias != nullptr) bias[e] = p.bias[w.ch0 + c + e];
         if (in && p.Dskip != nullptr) skip[e] = p.Dskip[w.ch0 + c + e];
     }
-    const uint16_t *Bp = p.B + row0 * p.bs + w.g * p.N + n0, *Cp = p.C + row0 * p.cs + w.g * p.N + n0;
+    // pointers to the first row of the tile that is worked on (or, of inputs, fetched next), and bytes from there
+    const int tiles = (t1 - t0 + K - 1) / K;
+    const int64_t row = q.begin + t0 + (int64_t)(tiles - 1) * K;
+    const bool gate = p.z != nullptr;
+    const uint16_t *xp = p.x + row * p.xs + w.ch0, *tp = p.dt + row * p.dts + w.ch0, *yp = p.dy + row * p.D + w.ch0;
+    const uint16_t *zp = gate ? p.z + row * p.zs + w.ch0 : nullptr;
+    uint16_t *dxp = p.dx + row * p.D + w.ch0, *dtp = p.ddt + row * p.D + w.ch0;
+    uint16_t *dzp = gate ? p.dz + row * p.D + w.ch0 : nullptr;
+    const int xs = (int)p.xs * 2, ts = (int)p.dts * 2, zs = (int)p.zs * 2, ys = p.D * 2;  // bytes between rows
+    const uint32_t xo = r0 * xs + c * 2, to = r0 * ts + c * 2, zo = r0 * zs + c * 2, yo = r0 * ys + c * 2;
+    // two elements of B or of C of a token of the tile, by the first K N threads
+    const int bt = threadIdx.x / p.N, bj = threadIdx.x % p.N * 2;
+    const bool ofC = bj >= p.N;
+    const int64_t bcs = ofC ? p.cs : p.bs;
+    const uint16_t *Wp = (ofC ? p.C + (bj - p.N) : p.B + bj) + (row + bt) * bcs + w.g * p.N;
+    float *Wl = reinterpret_cast<float *>(ofC ? &lds.C[bt < K ? bt : 0][0] : &lds.B[bt < K ? bt : 0][0]) +
+                (ofC ? bj - p.N : bj);
+    uint32_t nw = 0;
+    const float *mp = p.marks + ((q.begin / K + q.b + t0 / K + (int64_t)(tiles - 1)) * (p.N / 4) + wave) * p.D * 4;
+    // value (gradient, token, state) of a lane's bits (5), (4, 3, 2), (1, 0)
+    float *bcp = p.bc + ((int64_t)block * p.T + row) * 2 * p.N + n0;
+    const int bi = (lane >> 2) & 7;
+    const uint32_t bo = ((bi * 2 + (lane >> 5)) * p.N + (lane & 3)) * 4;
+
     uint32_t nx[kItems], nd[kItems], nz[kItems], ny[kItems];
     f32x4 mark = {0.f, 0.f, 0.f, 0.f};
-    auto fetch = [&](int t) {
+    auto fetch = [&](int n) {  // n: tokens of the tile
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int r = t + (threadIdx.x + k * NT) / 32;
             nx[k] = nd[k] = nz[k] = ny[k] = 0;
-            if (r >= t + K || r >= t1 || !in) continue;
-            const int64_t row = row0 + r;
-            nx[k] = *reinterpret_cast<const uint32_t *>(p.x + row * p.xs + w.ch0 + c);
-            nd[k] = *reinterpret_cast<const uint32_t *>(p.dt + row * p.dts + w.ch0 + c);
-            ny[k] = *reinterpret_cast<const uint32_t *>(p.dy + row * p.D + w.ch0 + c);
-            if (p.z != nullptr) nz[k] = *reinterpret_cast<const uint32_t *>(p.z + row * p.zs + w.ch0 + c);
+            if (r0 + k * kStep >= n || !in) continue;
+            nx[k] = at_offset<uint32_t>(xp, xo + k * kStep * xs);
+            nd[k] = at_offset<uint32_t>(tp, to + k * kStep * ts);
+            ny[k] = at_offset<uint32_t>(yp, yo + k * kStep * ys);
+            if (gate) nz[k] = at_offset<uint32_t>(zp, zo + k * kStep * zs);
         }
-        if (mine) mark = *reinterpret_cast<const f32x4 *>(mark_at(p, q, t, n0, ch));
+        if (mine) mark = at_offset<f32x4>(mp, (uint32_t)ch * 16);
+        nw = bt < n ? *reinterpret_cast<const uint32_t *>(Wp) : 0;
+        Wp -= K * bcs;
+        xp = moved(xp, -(int64_t)K * xs);
+        tp = moved(tp, -(int64_t)K * ts);
+        yp = moved(yp, -(int64_t)K * ys);
+        if (gate) zp = moved(zp, -(int64_t)K * zs);
+        mp -= (int64_t)p.N * p.D;
     };
-    const int tiles = (t1 - t0 + K - 1) / K;
-    if (tiles > 0) fetch(t0 + (tiles - 1) * K);
+    if (tiles > 0) fetch(t1 - t0 - (tiles - 1) * K);
+    const float still = p.softplus ? -__builtin_inff() : 0.f;  // what makes a step of 0
+    // (loads that have to be here before the loop: a wait inside it would be for the last tile's stores too)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) asm volatile("" : "+v"(bias[e]), "+v"(skip[e]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(A[e]), "+v"(u[e]));
     for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int t = t0 + tile * K, n = min(K, t1 - t);
-        uint32_t rd[kItems], rz[kItems], ry[kItems];
+        const int n = min(K, t1 - t0 - tile * K);
+        if (bt < K) *reinterpret_cast<float2 *>(Wl) = make_float2(bf16x2_lo(nw), bf16x2_hi(nw));
+        float step[kItems][2], x[kItems][2], e[kItems][2], slope[kItems][2], wz[kItems][2];
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int i = threadIdx.x + k * NT, r = i / 32;
-            rd[k] = nd[k];
-            rz[k] = nz[k];
-            ry[k] = ny[k];
-            if (i >= K * 32) continue;
-            const bool live = r < n && in;  // elsewhere nothing happens: no step, no gradient
+            const int r = r0 + k * kStep;
+            if (r >= K) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float x = e ? bf16x2_hi(nx[k]) : bf16x2_lo(nx[k]), z = e ? bf16x2_hi(nz[k]) : bf16x2_lo(nz[k]);
-                const float raw = (e ? bf16x2_hi(nd[k]) : bf16x2_lo(nd[k])) + bias[e];
-                const float step = p.softplus ? softplus_f(raw) : raw;
-                float g = e ? bf16x2_hi(ny[k]) : bf16x2_lo(ny[k]);
-                if (p.z != nullptr) g *= z * sigmoid_f(z);
-                sin[r][c + e] = live ? make_float4(step, step * x, g, x) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 2; ++i) {
+                x[k][i] = i ? bf16x2_hi(nx[k]) : bf16x2_lo(nx[k]);
+                const float g = i ? bf16x2_hi(ny[k]) : bf16x2_lo(ny[k]);
+                float raw = (i ? bf16x2_hi(nd[k]) : bf16x2_lo(nd[k])) + bias[i];
+                raw = r < n ? raw : still;
+                step[k][i] = raw;
+                slope[k][i] = 1.f;
+                if (p.softplus) {
+                    const float v = fast_exp2(-fabsf(raw) * kLog2e);  // softplus_fast, and its slope beside it
+                    const float m = 1.f + v;
+                    step[k][i] = __builtin_amdgcn_fmed3f(raw, 0.f, __builtin_inff()) +
+                                 __builtin_fmaf(__builtin_amdgcn_logf(m), kLn2, v - (m - 1.f));
+                    slope[k][i] = __builtin_amdgcn_rcpf(m) * (raw >= 0.f ? 1.f : v);
+                }
+                e[k][i] = g;
+                wz[k][i] = 0.f;
+                if (gate) {
+                    const float z = i ? bf16x2_hi(nz[k]) : bf16x2_lo(nz[k]), o = sigmoid_f(z), zo_ = z * o;
+                    e[k][i] = g * zo_;
+                    wz[k][i] = g * __builtin_fmaf(zo_, 1.f - o, o);
+                }
+                lds.sx[r][c + i] = make_float2(step[k][i], step[k][i] * x[k][i]);
+                lds.e[r][c + i] = e[k][i];
             }
         }
         const f32x4 h0 = mark;
-        if (tile > 0) fetch(t - K);
+        if (tile > 0) fetch(K);
         __syncthreads();
         if (n0 < p.N) {
+            // a token's numbers are read while the one ahead of it is worked on (the compiler, which takes the stores
+            // between for a hindrance, would read and wait)
+            struct Token {
+                float2 v;
+                float e;
+                f32x4 B, C;
+            };
+            auto read = [&](int i, bool back) {
+                return Token{lds.sx[i][lane], back ? lds.e[i][lane] : 0.f, lds.B[i][wave], lds.C[i][wave]};
+            };
             float h[K][4], a[K][4];
+            Token next = read(0, false);
 #pragma unroll
             for (int i = 0; i < K; ++i) {
-                const float4 v = sin[i][lane];
-                const Quad B = quad_or_zero(Bp, p.bs, t + i, last), C = quad_or_zero(Cp, p.cs, t + i, last);
+                const Token m = next;
+                next = i < K - 1 ? read(i + 1, false) : read(K - 1, true);
+                __builtin_amdgcn_sched_barrier(0);
                 float y = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    a[i][j] = fast_exp2(v.x * A[j]);
-                    h[i][j] = __builtin_fmaf(a[i][j], i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j], v.y * B.v[j]);
-                    y = __builtin_fmaf(C.v[j], h[i][j], y);
+                    a[i][j] = fast_exp2(m.v.x * A[j]);
+                    h[i][j] = __builtin_fmaf(a[i][j], i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j], m.v.y * m.B[j]);
+                    y = j == 0 ? m.C[j] * h[i][j] : __builtin_fmaf(m.C[j], h[i][j], y);
                 }
-                part[0][wave][i][lane] = y;
+                if (gate) lds.y[wave][i][lane] = y;
+                __builtin_amdgcn_sched_barrier(0);
             }
             float dAt[4] = {}, f[K][4];
 #pragma unroll
             for (int i = K - 1; i >= 0; --i) {
-                const float4 v = sin[i][lane];
-                const Quad B = quad_or_zero(Bp, p.bs, t + i, last), C = quad_or_zero(Cp, p.cs, t + i, last);
-                float uB = 0.f, qA = 0.f;
+                const Token m = next;
+                if (i > 0) next = read(i - 1, true);
+                __builtin_amdgcn_sched_barrier(0);
+                float uB = 0.f, qA = 0.f, forB[4], forC[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    u[j] = __builtin_fmaf(C.v[j], v.z, u[j]);
-                    // (lanes without a channel hold zeros: no share in the sums over channels)
-                    f[i][j] = fold32(v.z * h[i][j], u[j] * v.y);
-                    uB = __builtin_fmaf(u[j], B.v[j], uB);
+                    u[j] = __builtin_fmaf(m.C[j], m.e, u[j]);
+                    forC[j] = m.e * h[i][j];
+                    forB[j] = u[j] * m.v.y;
+                    uB = j == 0 ? u[j] * m.B[j] : __builtin_fmaf(u[j], m.B[j], uB);
                     u[j] *= a[i][j];
                     const float qq = u[j] * (i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j]);
-                    qA = __builtin_fmaf(qq, A[j], qA);
-                    dAt[j] = __builtin_fmaf(qq, v.x, dAt[j]);
+                    qA = j == 0 ? qq * A[j] : __builtin_fmaf(qq, A[j], qA);
+                    dAt[j] = i == K - 1 ? qq * m.v.x : __builtin_fmaf(qq, m.v.x, dAt[j]);
                 }
-                part[1][wave][i][lane] = uB;
-                part[2][wave][i][lane] = qA;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // (lanes without a channel hold zeros: no share in the sums over channels)
+                    f[i][j] = fold32(forC[j], forB[j]);
+                    if (i < 4) f[i][j] = fold16(f[i][j], f[i + 4][j]);
+                    if (i < 2) f[i][j] = fold_dpp<0x128>(f[i][j], f[i + 2][j], lane & 8);  // row_ror:8
+                }
+                lds.uq[wave][i][lane] = make_float2(uB, qA);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) dA[j] += dAt[j];
-            // value (gradient, token, state) of lane bits (5), (4, 3, 2), (1, 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[i][j] = fold16(f[i][j], f[i + 4][j]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[i][j] = fold_dpp<0x128>(f[i][j], f[i + 2][j], lane & 8);  // row_ror:8
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[0][j] = fold_dpp<0x141>(f[0][j], f[1][j], lane & 4);  // row_half_mirror
             f[0][0] = fold_dpp<0x4E>(f[0][0], f[0][2], lane & 2);  // quad_perm [2,3,0,1]
             f[0][1] = fold_dpp<0x4E>(f[0][1], f[0][3], lane & 2);
             f[0][0] = fold_dpp<0xB1>(f[0][0], f[0][1], lane & 1);  // quad_perm [1,0,3,2]
-            const int i = (lane >> 2) & 7;
-            if (i < n) {
-                const int64_t row = (int64_t)block * p.T + row0 + t + i;
-                p.bc[(row * 2 + (lane >> 5)) * p.N + n0 + (lane & 3)] = f[0][0];
-            }
+            if (bi < n) put_offset(bcp, bo, f[0][0]);
         }
+        bcp -= (int64_t)K * 2 * p.N;
         __syncthreads();
+        uint32_t ox[kItems], od[kItems], oz[kItems];
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int i = threadIdx.x + k * NT, r = i / 32;
-            if (i >= K * 32 || r >= n || !in) continue;
-            float2 y = make_float2(0.f, 0.f), uB = y, qA = y;
+            const int r = min(r0 + k * kStep, K - 1);
+            float2 y = make_float2(0.f, 0.f), uB, qA;
 #pragma unroll
             for (int v = 0; v < NW; ++v) {
-                if (v * 4 >= p.N) continue;
-                const float2 a = *reinterpret_cast<const float2 *>(&part[0][v][r][c]);
-                const float2 b = *reinterpret_cast<const float2 *>(&part[1][v][r][c]);
-                const float2 d = *reinterpret_cast<const float2 *>(&part[2][v][r][c]);
-                y.x += a.x;
-                y.y += a.y;
-                uB.x += b.x;
-                uB.y += b.y;
-                qA.x += d.x;
-                qA.y += d.y;
-            }
-            float dx[2], ddt[2], dz[2] = {};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float4 v = sin[r][c + e];
-                const float b = e ? uB.y : uB.x;
-                const float raw = (e ? bf16x2_hi(rd[k]) : bf16x2_lo(rd[k])) + bias[e];
-                dx[e] = __builtin_fmaf(v.x, b, skip[e] * v.z);
-                ddt[e] = __builtin_fmaf(e ? qA.y : qA.x, kLn2, v.w * b);
-                if (p.softplus) ddt[e] *= sigmoid_f(raw);
-                dD[e] = __builtin_fmaf(v.z, v.w, dD[e]);
-                db[e] += ddt[e];
-                if (p.z != nullptr) {
-                    const float z = e ? bf16x2_hi(rz[k]) : bf16x2_lo(rz[k]), o = sigmoid_f(z);
-                    const float g = e ? bf16x2_hi(ry[k]) : bf16x2_lo(ry[k]);
-                    const float out = __builtin_fmaf(skip[e], v.w, e ? y.y : y.x);
-                    dz[e] = g * out * __builtin_fmaf(z * o, 1.f - o, o);
+                const float4 b = *reinterpret_cast<const float4 *>(&lds.uq[v][r][c]);
+                uB = v == 0 ? make_float2(b.x, b.z) : make_float2(uB.x + b.x, uB.y + b.z);
+                qA = v == 0 ? make_float2(b.y, b.w) : make_float2(qA.x + b.y, qA.y + b.w);
+                if (gate) {
+                    const float2 a = *reinterpret_cast<const float2 *>(&lds.y[v][r][c]);
+                    y = make_float2(y.x + a.x, y.y + a.y);
                 }
             }
-            const int64_t to = (row0 + t + r) * p.D + w.ch0 + c;
-            *reinterpret_cast<uint32_t *>(p.dx + to) = pack_bf16x2(dx[0], dx[1]);
-            *reinterpret_cast<uint32_t *>(p.ddt + to) = pack_bf16x2(ddt[0], ddt[1]);
-            if (p.z != nullptr) *reinterpret_cast<uint32_t *>(p.dz + to) = pack_bf16x2(dz[0], dz[1]);
+            float dx[2], dt[2], dz[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float b = i ? uB.y : uB.x;
+                dx[i] = __builtin_fmaf(step[k][i], b, skip[i] * e[k][i]);
+                dt[i] = __builtin_fmaf(i ? qA.y : qA.x, kLn2, x[k][i] * b) * slope[k][i];
+                dz[i] = wz[k][i] * __builtin_fmaf(skip[i], x[k][i], i ? y.y : y.x);
+                if (r0 + k * kStep < n) {
+                    dD[i] = __builtin_fmaf(e[k][i], x[k][i], dD[i]);
+                    db[i] += dt[i];
+                }
+            }
+            ox[k] = pack_bf16x2(dx[0], dx[1]);
+            od[k] = pack_bf16x2(dt[0], dt[1]);
+            oz[k] = pack_bf16x2(dz[0], dz[1]);
         }
-        __syncthreads();
+        // the next tile's rows are waited for here, ahead of the stores
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) asm volatile("" : "+v"(nx[k]), "+v"(nd[k]), "+v"(ny[k]), "+v"(nz[k]));
+        asm volatile("" : "+v"(mark), "+v"(nw));
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            if (r0 + k * kStep >= n || !in) continue;
+            const uint32_t o = yo + k * kStep * ys;
+            put_offset(dxp, o, ox[k]);
+            put_offset(dtp, o, od[k]);
+            if (gate) put_offset(dzp, o, oz[k]);
+        }
+        dxp = moved(dxp, -(int64_t)K * ys);
+        dtp = moved(dtp, -(int64_t)K * ys);
+        if (gate) dzp = moved(dzp, -(int64_t)K * ys);
     }
+    const int64_t place = q.begin / p.seg + q.b + s;
     if (mine) {
-        *reinterpret_cast<f32x4 *>(dA_to) = f32x4{dA[0], dA[1], dA[2], dA[3]};
-        if (s == 0 && p.d_init != nullptr) {
-            const f32x4 v = {u[0], u[1], u[2], u[3]};
+        const f32x4 v = {u[0], u[1], u[2], u[3]};
+        *reinterpret_cast<f32x4 *>(p.dA_part + place * p.D * p.N + at) = f32x4{dA[0], dA[1], dA[2], dA[3]};
+        if (s > 0) {
+            if (s == nseg - 1) *reinterpret_cast<f32x4 *>(p.adj + (cut_place(p, q) + s) * p.D * p.N + at) = v;
+        } else if (p.d_init != nullptr) {
             if (p.state_bf16)
                 store_state4<true>(p.d_init, state, v);
             else
@@ -322,28 +392,65 @@ __global__ __launch_bounds__(NW * 64) void scan_grad(ScanParams p) {
         }
     }
     // sums over tokens of what belongs to channels
-    float2 *sums = reinterpret_cast<float2 *>(&sin[0][0]);  // [kTeams][64]
-    const int team = threadIdx.x / 32;
-    if (team < kTeams)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) sums[team * 64 + c + e] = make_float2(dD[e], db[e]);
     __syncthreads();
+    if (r0 < kTeams)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) lds.sx[r0][c + i] = make_float2(dD[i], db[i]);
+    __syncthreads();
+    float *dD_to = p.dD_part + place * 2 * p.D + w.ch0;
     for (int i = threadIdx.x; i < w.nch; i += NT) {
         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kTeams; ++k) {
-            v.x += sums[k * 64 + i].x;
-            v.y += sums[k * 64 + i].y;
+            v.x += lds.sx[k][i].x;
+            v.y += lds.sx[k][i].y;
         }
         dD_to[i] = v.x;
         dD_to[p.D + i] = v.y;
     }
 }
 
-// dB and dC: the blocks of a group, added in their order.
-__global__ __launch_bounds__(256) void sum_blocks(ScanParams p) {
+// Whole sequences and last segments; what the segments between pass on.
+template <int NW>
+__global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_first(ScanParams p) {
+    __shared__ Shared<NW> lds;
+    const int place = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
+    Seq q;
+    int s;
+    const bool found = find_piece(p.qsl, p.batch, p.T, p.seg, place, q, s);
+    const int nseg = found ? segments_of(p, q) : 0;
+    if (!found || s >= nseg) {  // an empty place adds nothing
+        const Span w = span_of(p, block);
+        const int lane = threadIdx.x & 63, n0 = threadIdx.x / 64 * 4;
+        if (lane < w.nch && n0 < p.N)
+            *reinterpret_cast<f32x4 *>(p.dA_part + ((int64_t)place * p.D + w.ch0 + lane) * p.N + n0) =
+                f32x4{0.f, 0.f, 0.f, 0.f};
+        float *dD = p.dD_part + (int64_t)place * 2 * p.D + w.ch0;
+        if (threadIdx.x < w.nch) dD[threadIdx.x] = dD[p.D + threadIdx.x] = 0.f;
+        return;
+    }
+    if (s == nseg - 1)
+        grad<NW>(p, lds, q, s, nseg, block);
+    else if (s > 0)
+        adjoint<NW>(p, lds, q, s, span_of(p, block));
+}
+template <int NW>
+__global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_rest(ScanParams p) {
+    __shared__ Shared<NW> lds;
+    Seq q;
+    int s;
+    if (!find_cut(p, blockIdx.x / p.blocks, q, s)) return;
+    const int nseg = segments_of(p, q);
+    if (s < nseg - 1) grad<NW>(p, lds, q, s, nseg, blockIdx.x % p.blocks);
+}
+
+// The sums over blocks and places: dB and dC, the blocks of a group added in
+// their order, by the first bc_blocks workgroups, and dA, dD, dbias.
+__global__ __launch_bounds__(kSumThreads) void scan_sums(ScanParams p, int64_t bc_blocks, Sums sums) {
+    __shared__ f32x4 buf[16][16];
+    if (blockIdx.x >= bc_blocks) return add_parts(sums, blockIdx.x - bc_blocks, buf);
     const int quads = p.N / 4;
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
     const int j = (int)(i % quads);
     i /= quads;
     const int which = (int)(i & 1);
@@ -363,27 +470,23 @@ __global__ __launch_bounds__(256) void sum_blocks(ScanParams p) {
 }  // namespace
 
 hipError_t launch_scan_grad(const ScanParams &p, hipStream_t s) {
-    const dim3 grid((unsigned)(p.places * p.blocks));
-    hipError_t e = launch_scan_states(p, s);
+    hipError_t e = launch_scan_marks(p, s);
     if (e != hipSuccess) return e;
-    if (p.cut_places > 0)
-        by_waves(waves_of(p.N), [&](auto n) {
-            constexpr int NW = decltype(n)::value;
-            scan_adjoint<NW><<<grid, NW * 64, 0, s>>>(p);
-        });
-    if ((e = launch_scan_marks(p, s)) != hipSuccess) return e;
     by_waves(waves_of(p.N), [&](auto n) {
         constexpr int NW = decltype(n)::value;
-        scan_grad<NW><<<grid, NW * 64, 0, s>>>(p);
+        scan_grad_first<NW><<<dim3((unsigned)(p.places * p.blocks)), NW * 64, 0, s>>>(p);
+        if (p.cut_places > 0)
+            scan_grad_rest<NW><<<dim3((unsigned)(p.cut_places * p.blocks)), NW * 64, 0, s>>>(p);
     });
-    const int64_t sums = (int64_t)p.T * p.G * 2 * (p.N / 4);
-    if (sums > 0) sum_blocks<<<dim3((unsigned)((sums + 255) / 256)), 256, 0, s>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t DN = (int64_t)p.D * p.N, n = p.places;
-    if ((e = launch_sum_parts(p.dA_part, (int)n, DN, DN, p.dA, s)) != hipSuccess) return e;
-    if (p.dD != nullptr && (e = launch_sum_parts(p.dD_part, (int)n, 2 * p.D, p.D, p.dD, s)) != hipSuccess) return e;
-    if (p.dbias != nullptr) e = launch_sum_parts(p.dD_part + p.D, (int)n, 2 * p.D, p.D, p.dbias, s);
-    return e;
+    const int64_t bc_blocks = ((int64_t)p.T * p.G * (p.N / 2) + kSumThreads - 1) / kSumThreads;
+    const int64_t DN = (int64_t)p.D * p.N;
+    const int n = (int)p.places;
+    const Sums sums = {{{p.dA_part, n, DN, DN, p.dA}, {p.dD_part, n, 2 * p.D, p.D, p.dD},
+                        {p.dD_part + p.D, n, 2 * p.D, p.D, p.dbias}}};
+    const int64_t blocks = bc_blocks + sum_blocks(sums.s[0]) + sum_blocks(sums.s[1]) + sum_blocks(sums.s[2]);
+    scan_sums<<<dim3((unsigned)blocks), kSumThreads, 0, s>>>(p, bc_blocks, sums);
+    return hipGetLastError();
 }
 
 }  // namespace layer

@@ -1,8 +1,7 @@
 // Selective scan over ragged batches: h = exp(dts A) h + dts x B, y = C.h + D x,
 // gated by silu(z).  Every channel and state decays on its own, so there is no
 // matrix product in it: a token costs each (channel, state) an exponential, two
-// products and two fused adds, about 8 issue slots with the exponential at a
-// quarter of the rate, and this, not memory, is what bounds it.
+// products and two fused adds, and this, not memory, is what bounds it.
 //
 // A workgroup takes 64 channels of a sequence (or of one of its segments) and a
 // wavefront 4 states of them, a channel a lane: B and C are then the same for
@@ -10,10 +9,15 @@
 // channel alone (softplus, gate, input and output) is done once, by all threads
 // together, for a tile of 16 tokens at a time, and handed over through LDS.
 //
-// Sequences longer than a share of the card are cut into segments: a pass over
-// all but their last ones leaves the states that each would from zero, with the
-// sum of its time steps, and a segment's workgroup chains those ahead of it
-// before it starts.
+// Sequences longer than a share of the card are cut into segments, in two
+// launches: the first walks whole sequences and first segments, which leave
+// their states, and forms the states that the segments between the first and the
+// last would leave from zero, with the sums of their time steps; the second
+// walks the other segments, each after chaining what lies ahead of it.
+#include <math.h>
+
+#include <algorithm>
+
 #include "ssd.h"
 #include "ssd_layer.hpp"
 #include "ssd_selective.hpp"
@@ -22,27 +26,26 @@ namespace ssd {
 namespace layer {
 namespace {
 
-// kOutputs: the scan itself.  kStates: the pass that leaves the segments' states
-// of cut sequences.  kMarks: the state ahead of every kGradTile tokens, for the
-// backward pass.
-enum Walk { kOutputs, kStates, kMarks };
+constexpr int kGroup = 4;  // tokens whose B, C and steps are on their way while as many are worked on
+
+// kOutputs: the scan itself.  kMarks: the state ahead of every kGradTile tokens,
+// for the backward pass.  kStates: the state a segment leaves from zero.
+enum Walk { kOutputs, kMarks, kStates };
+
+template <int NW>
+struct Shared {
+    float2 step[kTile][64];  // time step, and times x
+    float y[NW][kTile][64];  // a wavefront's share of C.h
+};
+
+// One segment of a sequence (or all of it) and 64 channels.
 template <int NW, Walk WALK>
-__global__ __launch_bounds__(NW * 64) void scan_walk(ScanParams p) {
+__device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const Seq &q, int s, int nseg,
+                                     const Span &w) {
     constexpr int NT = NW * 64, kItems = (kTile * 16 + NT - 1) / NT;
     constexpr bool OUT = WALK == kOutputs, STATES = WALK == kStates;
-    __shared__ float2 sdt[kTile][64];                   // time step, and times x
-    __shared__ float sy[OUT ? NW : 1][kTile][64];    // a wavefront's share of C.h
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    const int place = blockIdx.x / p.blocks;
-    Seq q;
-    int s;
-    if (!find_piece(p.qsl, p.batch, p.T, p.seg, place, q, s)) return;
-    const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[q.b] : q.b;
-    if (slot >= (int64_t)p.max_slots) return;  // padding
-    const int nseg = q.len > p.seg ? (q.len + p.seg - 1) / p.seg : 1;
-    if (STATES && s >= nseg - 1) return;
-    const Span w = span_of(p, blockIdx.x % p.blocks);
-    const int t0 = s * p.seg, t1 = min(q.len, t0 + p.seg);
+    const int t0 = s * p.seg, t1 = nseg > 1 ? min(q.len, t0 + p.seg) : q.len;
     const bool init = p.state_in != nullptr && (p.init_all || (p.has_init != nullptr && p.has_init[q.b] != 0));
 
     // this lane's channel, and this wavefront's states
@@ -50,124 +53,171 @@ __global__ __launch_bounds__(NW * 64) void scan_walk(ScanParams p) {
     const bool mine = lane < w.nch && n0 < p.N;
     const int ch = w.ch0 + (lane < w.nch ? lane : 0);
     const int64_t at = (int64_t)ch * p.N + n0;
+    const int64_t slot = p.cache_idx != nullptr ? (int64_t)p.cache_idx[q.b] : q.b;
     const int64_t state = slot * p.D * p.N + at;
+    const int64_t first = nseg > 1 ? cut_place(p, q) : 0;  // of this sequence's segments' states
     float A[4] = {}, h[4] = {};
     if (mine) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) A[i] = p.A[at + i] * kLog2e;
-    }
-    const int64_t first = nseg > 1 ? cut_place(p, q) : 0;  // of this sequence's segments' states
-    if (mine && s == 0) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (nseg > 1 && !STATES) {
-            // the pass kept what the pool held, which the last segment may have replaced by now
-            v = *reinterpret_cast<const f32x4 *>(p.parts + (first + nseg - 1) * p.D * p.N + at);
-        } else if (init) {
-            v = p.state_bf16 ? load_state4<true>(p.state_in, state) : load_state4<false>(p.state_in, state);
-        }
-        if (STATES) *reinterpret_cast<f32x4 *>(p.parts + (first + nseg - 1) * p.D * p.N + at) = v;
+        if (!STATES && s == 0 && init) {
+            const f32x4 v = p.state_bf16 ? load_state4<true>(p.state_in, state) : load_state4<false>(p.state_in, state);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = v[i];
+            for (int i = 0; i < 4; ++i) h[i] = v[i];
+        }
+        if (!STATES && s > 0) chain_states(p, first, s, at, ch, A, h);
     }
-    if (mine && !STATES && s > 0) chain_states(p, first, s, at, ch, A, h);
+    if (OUT && n0 >= p.N)  // no states, no share
+        for (int i = 0; i < kTile; ++i) lds.y[wave][i][lane] = 0.f;
 
-    // the tokens and channels this thread prepares and finishes: 4 channels of a token an item
-    const uint16_t *xp = p.x + (int64_t)q.begin * p.xs + w.ch0, *dtp = p.dt + (int64_t)q.begin * p.dts + w.ch0;
-    const uint16_t *zp = p.z != nullptr ? p.z + (int64_t)q.begin * p.zs + w.ch0 : nullptr;
-    const uint16_t *Bp = p.B + (int64_t)q.begin * p.bs + w.g * p.N + n0;
-    const uint16_t *Cp = p.C + (int64_t)q.begin * p.cs + w.g * p.N + n0;
+    // the tokens and channels this thread prepares and finishes: 4 channels of a token an item, the same ones in
+    // every item
+    const int c = (threadIdx.x % 16) * 4, r0 = threadIdx.x / 16;
+    const bool in = c < w.nch;
+    float bias[4] = {}, skip[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (in && p.bias != nullptr) bias[e] = p.bias[w.ch0 + c + e];
+        if (OUT && in && p.Dskip != nullptr) skip[e] = p.Dskip[w.ch0 + c + e];
+    }
+    const int64_t row0 = q.begin + t0 + r0;
+    const uint16_t *xp = p.x + row0 * p.xs + w.ch0 + c, *dp = p.dt + row0 * p.dts + w.ch0 + c;
+    const bool gate = OUT && p.z != nullptr;
+    const uint16_t *zp = gate ? p.z + row0 * p.zs + w.ch0 + c : nullptr;
+    uint16_t *yp = OUT ? p.y + row0 * p.D + w.ch0 + c : nullptr;
+    const uint16_t *Bp = p.B + (int64_t)(q.begin + t0) * p.bs + w.g * p.N + n0;
+    const uint16_t *Cp = p.C + (int64_t)(q.begin + t0) * p.cs + w.g * p.N + n0;
     u32x2 nx[kItems], nd[kItems], nz[kItems];
     auto fetch = [&](int t) {
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int i = threadIdx.x + k * NT, r = t + i / 16, c = (i % 16) * 4;
             nx[k] = nd[k] = nz[k] = u32x2{0, 0};
-            if (i >= kTile * 16 || r >= t1 || c >= w.nch) continue;
-            nx[k] = *reinterpret_cast<const u32x2 *>(xp + (int64_t)r * p.xs + c);
-            nd[k] = *reinterpret_cast<const u32x2 *>(dtp + (int64_t)r * p.dts + c);
-            if (OUT && zp != nullptr) nz[k] = *reinterpret_cast<const u32x2 *>(zp + (int64_t)r * p.zs + c);
+            const int r = r0 + k * (NT / 16);
+            if (r >= kTile || t + r >= t1 || !in) continue;
+            nx[k] = *reinterpret_cast<const u32x2 *>(xp + k * (NT / 16) * p.xs);
+            nd[k] = *reinterpret_cast<const u32x2 *>(dp + k * (NT / 16) * p.dts);
+            if (gate) nz[k] = *reinterpret_cast<const u32x2 *>(zp + k * (NT / 16) * p.zs);
         }
+        xp += kTile * p.xs;
+        dp += kTile * p.dts;
+        if (gate) zp += kTile * p.zs;
     };
-    float steps = 0.f;  // sum of this lane's channel's time steps (first wavefront)
+    float steps = 0.f;  // sum of this lane's channel's time steps
     fetch(t0);
+    // (loads that have to be here before the loop: a wait inside it would be for the last tile's stores too)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(bias[e]), "+v"(skip[e]), "+v"(A[e]), "+v"(h[e]));
     for (int t = t0; t < t1; t += kTile) {
         u32x2 rx[kItems], rz[kItems];
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int i = threadIdx.x + k * NT, r = i / 16, c = (i % 16) * 4;
+            const int r = r0 + k * (NT / 16);
             rx[k] = nx[k];
             rz[k] = nz[k];
-            if (i >= kTile * 16 || c >= w.nch) continue;
+            if (r >= kTile) continue;
             float x[4], d[4];
             widen4(nx[k], x);
             widen4(nd[k], d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float step = time_step(p, d[e], w.ch0 + c + e);
-                sdt[r][c + e] = make_float2(step, step * x[e]);
+                const float step = time_step(p, d[e] + bias[e]);
+                lds.step[r][c + e] = make_float2(step, step * x[e]);
             }
         }
         if (t + kTile < t1) fetch(t + kTile);
         __syncthreads();
         if (n0 < p.N) {
             const int n = min(kTile, t1 - t);
-            auto token = [&](int i) {
+            auto token = [&](int i, const float2 &e, const Words &m) {
                 if (WALK == kMarks && i % kGradTile == 0 && mine)
                     *reinterpret_cast<f32x4 *>(mark_at(p, q, t + i, n0, ch)) = f32x4{h[0], h[1], h[2], h[3]};
-                const float2 e = sdt[i][lane];
-                const Quad B = quad_at(Bp + (int64_t)(t + i) * p.bs);
+                const Quad B = quad_of(m.b[0], m.b[1]), C = quad_of(m.c[0], m.c[1]);
                 float y = 0.f;
-                Quad C = {};
-                if (OUT) C = quad_at(Cp + (int64_t)(t + i) * p.cs);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     h[j] = __builtin_fmaf(fast_exp2(e.x * A[j]), h[j], e.y * B.v[j]);
-                    if (OUT) y = __builtin_fmaf(C.v[j], h[j], y);
+                    if (OUT) y = j == 0 ? C.v[j] * h[j] : __builtin_fmaf(C.v[j], h[j], y);
                 }
                 if (STATES) steps += e.x;
-                if (OUT) sy[wave][i][lane] = y;
+                if (OUT) lds.y[wave][i][lane] = y;
             };
             if (n == kTile) {
+                Words next[kGroup], now[kGroup];
+                float2 en[kGroup], ee[kGroup];
+                auto ahead = [&](int g) {
 #pragma unroll
-                for (int i = 0; i < kTile; ++i) token(i);
+                    for (int i = 0; i < kGroup; ++i) {
+                        words_at(Bp, next[i].b);
+                        Bp += p.bs;
+                        if (OUT) {
+                            words_at(Cp, next[i].c);
+                            Cp += p.cs;
+                        }
+                        en[i] = lds.step[g + i][lane];
+                    }
+                };
+                ahead(0);
+#pragma unroll
+                for (int g = 0; g < kTile; g += kGroup) {
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) {
+                        now[i] = next[i];
+                        ee[i] = en[i];
+                    }
+                    if (g + kGroup < kTile) ahead(g + kGroup);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) token(g + i, ee[i], now[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             } else {
 #pragma unroll 1
-                for (int i = 0; i < n; ++i) token(i);
+                for (int i = 0; i < n; ++i) {
+                    Words m;
+                    words_at(Bp + (int64_t)i * p.bs, m.b);
+                    words_at(Cp + (int64_t)i * p.cs, m.c);
+                    token(i, lds.step[i][lane], m);
+                }
             }
         }
         __syncthreads();
         if constexpr (OUT) {
+            u32x2 out[kItems];
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
-                const int i = threadIdx.x + k * NT, r = i / 16, c = (i % 16) * 4;
-                if (i >= kTile * 16 || t + r >= t1 || c >= w.nch) continue;
-                f32x4 y = {0.f, 0.f, 0.f, 0.f};
+                const int r = min(r0 + k * (NT / 16), kTile - 1);
+                f32x4 y = *reinterpret_cast<const f32x4 *>(&lds.y[0][r][c]);
 #pragma unroll
-                for (int v = 0; v < NW; ++v)
-                    if (v * 4 < p.N) y += *reinterpret_cast<const f32x4 *>(&sy[v][r][c]);
-                if (p.Dskip != nullptr) {
-                    float x[4];
-                    widen4(rx[k], x);
+                for (int v = 1; v < NW; ++v) y += *reinterpret_cast<const f32x4 *>(&lds.y[v][r][c]);
+                float x[4];
+                widen4(rx[k], x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p.Dskip[w.ch0 + c + e], x[e], y[e]);
-                }
-                if (zp != nullptr) {
+                for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(skip[e], x[e], y[e]);
+                if (gate) {
                     float z[4];
                     widen4(rz[k], z);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) y[e] *= z[e] * sigmoid_f(z[e]);
                 }
-                *reinterpret_cast<u32x2 *>(p.y + (int64_t)(q.begin + t + r) * p.D + w.ch0 + c) =
-                    u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+                out[k] = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
             }
+            // the next tile's rows are waited for here, ahead of the stores
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) asm volatile("" : "+v"(nx[k]), "+v"(nd[k]), "+v"(nz[k]));
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int r = r0 + k * (NT / 16);
+                if (r < kTile && t + r < t1 && in) *reinterpret_cast<u32x2 *>(yp + k * (NT / 16) * p.D) = out[k];
+            }
+            yp += (int64_t)kTile * p.D;
         }
     }
     if (!mine) return;
     const f32x4 v = {h[0], h[1], h[2], h[3]};
-    if constexpr (STATES) {
+    if (s < nseg - 1) {
         *reinterpret_cast<f32x4 *>(p.parts + (first + s) * p.D * p.N + at) = v;
-        if (wave == 0) p.steps[(first + s) * p.D + ch] = steps;
-    } else if (OUT && s == nseg - 1) {
+        if (STATES && wave == 0) p.steps[(first + s) * p.D + ch] = steps;
+    } else if (OUT) {
         if (p.state_bf16)
             store_state4<true>(p.state_out, state, v);
         else
@@ -175,12 +225,41 @@ __global__ __launch_bounds__(NW * 64) void scan_walk(ScanParams p) {
     }
 }
 
+__device__ __forceinline__ bool padding(const ScanParams &p, int b) {
+    return p.cache_idx != nullptr && p.cache_idx[b] >= p.max_slots;
+}
+
+template <int NW, Walk WALK>
+__global__ __launch_bounds__(NW * 64) void scan_first(ScanParams p) {
+    __shared__ Shared<NW> lds;
+    Seq q;
+    int s;
+    if (!find_piece(p.qsl, p.batch, p.T, p.seg, blockIdx.x / p.blocks, q, s)) return;
+    const int nseg = segments_of(p, q);
+    if (padding(p, q.b) || (s > 0 && s >= nseg - 1)) return;
+    const Span w = span_of(p, blockIdx.x % p.blocks);
+    if (s == 0)
+        walk<NW, WALK>(p, lds, q, s, nseg, w);
+    else
+        walk<NW, kStates>(p, lds, q, s, nseg, w);
+}
+
+template <int NW, Walk WALK>
+__global__ __launch_bounds__(NW * 64) void scan_rest(ScanParams p) {
+    __shared__ Shared<NW> lds;
+    Seq q;
+    int s;
+    if (!find_cut(p, blockIdx.x / p.blocks, q, s) || s == 0 || padding(p, q.b)) return;
+    walk<NW, WALK>(p, lds, q, s, segments_of(p, q), span_of(p, blockIdx.x % p.blocks));
+}
+
 template <Walk WALK>
-hipError_t walk(const ScanParams &p, hipStream_t s) {
-    const dim3 grid((unsigned)(p.places * p.blocks));
+hipError_t launch_walk(const ScanParams &p, hipStream_t s) {
     by_waves(waves_of(p.N), [&](auto n) {
         constexpr int NW = decltype(n)::value;
-        scan_walk<NW, WALK><<<grid, NW * 64, 0, s>>>(p);
+        scan_first<NW, WALK><<<dim3((unsigned)(p.places * p.blocks)), NW * 64, 0, s>>>(p);
+        if (p.cut_places > 0)
+            scan_rest<NW, WALK><<<dim3((unsigned)(p.cut_places * p.blocks)), NW * 64, 0, s>>>(p);
     });
     return hipGetLastError();
 }
@@ -189,31 +268,27 @@ hipError_t walk(const ScanParams &p, hipStream_t s) {
 void scan_shape(ScanParams &p, bool backward) {
     p.Dg = p.D / p.G;
     p.blocks = p.G * ((p.Dg + 63) / 64);
-    // A workgroup's share of the card: four wavefronts a SIMD, 1024 workgroups of 4
-    const int64_t share = (int64_t)p.T * p.blocks / 1024;
-    int64_t seg = (share + kTile - 1) / kTile * kTile;
-    seg = seg < 256 ? 256 : seg;
+    // SEGMENT_RULE
+    const int64_t waves = (int64_t)p.blocks * waves_of(p.N), fill = backward ? 2048 : 4096;
+    int64_t seg = std::max<int64_t>(backward ? 32 : 64, (int64_t)sqrt((double)p.T));
+    seg = std::max(seg, (int64_t)p.T * waves / (backward ? 2048 : 16384));
+    if (p.batch * waves >= fill) seg = std::max<int64_t>(seg, p.T / p.batch / (backward ? 1 : 2));
+    seg = (seg + kTile - 1) / kTile * kTile;
     p.seg = (int)seg;
+    p.cut = (int)std::min<int64_t>(2 * seg, INT32_MAX);
     p.places = p.T / seg + p.batch;
-    p.cuts = p.T / (seg + 1) < p.batch ? p.T / (seg + 1) : p.batch;
+    p.cuts = std::min<int64_t>(p.T / ((int64_t)p.cut + 1), p.batch);
     p.cut_places = p.cuts > 0 ? p.T / seg + p.cuts : 0;
-    (void)backward;
 }
 
 int64_t scan_threads(const ScanParams &p, bool backward) {
     const int64_t walk = p.places * p.blocks * 64 * waves_of(p.N);
-    const int64_t sums = backward ? (int64_t)p.T * p.G * (p.N / 2) + 255 : 0;
+    const int64_t sums = backward ? (int64_t)p.T * p.G * (p.N / 2) + 4 * ((int64_t)p.D * (p.N + 2)) + 1024 : 0;
     return walk > sums ? walk : sums;
 }
 
-hipError_t launch_scan_states(const ScanParams &p, hipStream_t s) {
-    return p.cut_places > 0 ? walk<kStates>(p, s) : hipSuccess;
-}
-hipError_t launch_scan_marks(const ScanParams &p, hipStream_t s) { return walk<kMarks>(p, s); }
-hipError_t launch_scan(const ScanParams &p, hipStream_t s) {
-    const hipError_t e = launch_scan_states(p, s);
-    return e != hipSuccess ? e : walk<kOutputs>(p, s);
-}
+hipError_t launch_scan_marks(const ScanParams &p, hipStream_t s) { return launch_walk<kMarks>(p, s); }
+hipError_t launch_scan(const ScanParams &p, hipStream_t s) { return launch_walk<kOutputs>(p, s); }
 
 }  // namespace layer
 }  // namespace ssd

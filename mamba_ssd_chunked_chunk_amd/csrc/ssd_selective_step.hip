@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void scan_step(ScanParams p, int cblocks)
             load_quad(p.B + b * p.bs + g * p.N + n0, B);
             load_quad(p.C + b * p.cs + g * p.N + n0, C);
             x = bf16_bits_to_float(p.x[b * p.xs + ch]);
-            const float step = time_step(p, bf16_bits_to_float(p.dt[b * p.dts + ch]), ch);
+            const float step = time_step(p, bf16_bits_to_float(p.dt[b * p.dts + ch]) + (p.bias != nullptr ? p.bias[ch] : 0.f));
             const float u = step * x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
