@@ -142,7 +142,7 @@ def test_rows_of_a_step_are_its_sequences(lib):
 
 def test_workspace_sizes(lib):
     """Short sequences need none in the forward pass; the backward pass of the scan keeps a state for every 8 tokens."""
-    assert binding.ssd_selective_scan_workspace_size(scan(total_len=200)) == 0
+    assert binding.ssd_selective_scan_workspace_size(scan(total_len=128)) == 0
     assert binding.ssd_selective_scan_workspace_size(scan(total_len=0)) == 0
     cut = binding.ssd_selective_scan_workspace_size(scan(total_len=100_000, batch=1))
     assert cut >= 512 * 17 * 4 * 2
