@@ -1,53 +1,90 @@
 // Short causal depthwise convolution over ragged batches, its step for single
-// tokens and its backward pass.  A wavefront takes a piece of one sequence and
-// 512 channels, 8 consecutive ones a lane, and walks along the tokens with the
-// last width - 1 inputs in registers, so a row is read once but for the few
-// ahead of a piece.  Only the first piece of a sequence, which alone reads its
-// state, writes the one that it leaves, so the pool needs no second launch.
+// tokens and its backward pass.  A lane takes 8 consecutive channels (4 in the
+// backward pass) of a piece of one sequence and walks along the tokens, the last
+// `width` inputs in a ring of registers and the next rows on their way in others,
+// so a row is read once but for the few ahead of a piece.  Only the first piece of
+// a sequence, which alone reads its state, writes the one that it leaves, so the
+// pool needs no second launch.
 #include "ssd_layer.hpp"
 
 namespace ssd {
 namespace layer {
 namespace {
 
-constexpr int kAhead = 8;  // rows in flight
-
-// weights [channels][W] of 8 channels
+// Rows in flight, a multiple of the width, so that a token's place in the ring
+// is known when the walk is unrolled.
 template <int W>
-__device__ __forceinline__ void load_taps(const float *weight, int c, float (&w)[W][8]) {
-    const float *at = weight + (int64_t)c * W;
-    float f[8 * W];
+constexpr int kAhead = W == 3 ? 6 : 8;
+
+// E consecutive bf16 as they lie in memory, and as floats
+template <int E>
+using Raw = uint32_t __attribute__((ext_vector_type(E / 2)));
+template <int E>
+__device__ __forceinline__ Raw<E> row_of(const uint16_t *base, int64_t at) {
+    return *reinterpret_cast<const Raw<E> *>(base + at);
+}
+template <int E>
+__device__ __forceinline__ void put_row(uint16_t *base, int64_t at, const Raw<E> &v) {
+    *reinterpret_cast<Raw<E> *>(base + at) = v;
+}
+template <int E>
+__device__ __forceinline__ void widen(const Raw<E> &v, float (&o)[E]) {
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i) {
-        const f32x4 v = reinterpret_cast<const f32x4 *>(at)[i];
+    for (int k = 0; k < E / 2; ++k) {
+        o[2 * k] = bf16x2_lo(v[k]);
+        o[2 * k + 1] = bf16x2_hi(v[k]);
+    }
+}
+template <int E>
+__device__ __forceinline__ Raw<E> narrow(const float (&v)[E]) {
+    Raw<E> r;
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) r[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    return r;
+}
+
+// weights [channels][W] and bias of E channels
+template <int W, int E>
+__device__ __forceinline__ void load_taps(const float *weight, int c, float (&w)[W][E]) {
+    const f32x4 *at = reinterpret_cast<const f32x4 *>(weight + (int64_t)c * W);
+    float f[E * W];
+#pragma unroll
+    for (int i = 0; i < E * W / 4; ++i) {
+        const f32x4 v = at[i];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[4 * i + e] = v[e];
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j][e] = f[e * W + j];
 }
-__device__ __forceinline__ u32x4 row8(const uint16_t *base, int64_t at) {
-    return *reinterpret_cast<const u32x4 *>(base + at);
-}
-__device__ __forceinline__ void put8(uint16_t *base, int64_t at, const u32x4 &v) {
-    *reinterpret_cast<u32x4 *>(base + at) = v;
+template <int E>
+__device__ __forceinline__ void load_bias(const float *bias, int c, float (&b)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) b[e] = 0.f;
+    if (bias == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+        const f32x4 v = reinterpret_cast<const f32x4 *>(bias + c)[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[4 * i + e] = v[e];
+    }
 }
 
 // The W - 1 inputs ahead of token `t` of a sequence, as they are stored: of the
 // sequence, of its state ahead of it, or zero.  `state`: its rows, or null.
-template <int W>
+template <int W, int E>
 __device__ __forceinline__ void load_window(const ConvParams &p, const Seq &q, int t, const uint16_t *state, int c,
-                                            u32x4 (&win)[W - 1]) {
+                                            Raw<E> (&win)[W - 1]) {
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
         const int i = t - (W - 1) + r;
-        win[r] = u32x4{0, 0, 0, 0};
+        win[r] = Raw<E>(0);
         if (i >= 0)
-            win[r] = row8(p.x, (int64_t)(q.begin + i) * p.xs + c);
+            win[r] = row_of<E>(p.x, (int64_t)(q.begin + i) * p.xs + c);
         else if (state != nullptr)
-            win[r] = row8(state, (int64_t)(W - 1 + i) * p.D + c);
+            win[r] = row_of<E>(state, (int64_t)(W - 1 + i) * p.D + c);
     }
 }
 
@@ -69,17 +106,18 @@ __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
     const uint16_t *state = init ? p.state_in + at : nullptr;
     const int t0 = s * p.tile, t1 = min(q.len, t0 + p.tile);
 
-    u32x4 win[W - 1];
-    load_window<W>(p, q, t0, state, c, win);
+    constexpr int E = 8, R = kAhead<W>;
+    Raw<E> win[W - 1];
+    load_window<W, E>(p, q, t0, state, c, win);
     if (s == 0) {
         // the state that the sequence leaves
-        u32x4 last[W - 1];
+        Raw<E> last[W - 1];
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
             const int i = q.len - (W - 1) + r;
-            last[r] = u32x4{0, 0, 0, 0};
+            last[r] = Raw<E>(0);
             if (i >= 0)
-                last[r] = row8(p.x, (int64_t)(q.begin + i) * p.xs + c);
+                last[r] = row_of<E>(p.x, (int64_t)(q.begin + i) * p.xs + c);
             else {
 #pragma unroll
                 for (int m = 0; m < W - 1; ++m)
@@ -87,44 +125,45 @@ __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
             }
         }
 #pragma unroll
-        for (int r = 0; r < W - 1; ++r) put8(p.state_out, at + (int64_t)r * p.D + c, last[r]);
+        for (int r = 0; r < W - 1; ++r) put_row<E>(p.state_out, at + (int64_t)r * p.D + c, last[r]);
     }
     if (t0 >= t1) return;
-    float w[W][8], bias[8] = {}, v[W][8];
-    load_taps<W>(p.weight, c, w);
-    if (p.bias != nullptr) load_state8<false>(p.bias, c, bias);
+    float w[W][E], bias[E], v[W][E];  // v: tap j of the walk's i-th token at (i + j) % W
+    load_taps<W, E>(p.weight, c, w);
+    load_bias<E>(p.bias, c, bias);
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) widen8(win[r], v[r]);
-    const uint16_t *x = p.x + (int64_t)q.begin * p.xs + c;
-    uint16_t *y = p.y + (int64_t)q.begin * p.D + c;
-    u32x4 next[kAhead];
+    for (int r = 0; r < W - 1; ++r) widen<E>(win[r], v[r]);
+    // rows by an address that all lanes share and the lane's own offset in bytes
+    Scalar<const uint16_t> x(p.x + (int64_t)(q.begin + t0) * p.xs);
+    Scalar<uint16_t> y(p.y + (int64_t)(q.begin + t0) * p.D);
+    const uint32_t lo = c * 2;
+    // (no branch ends a group early, and rows behind the piece are its last one: values that meet where branches
+    // join would be copied)
+    Raw<E> rows[R];
+    int ahead = t0;  // the row that is fetched next
+    auto fetch = [&](int i) {
+        rows[i] = x.at<Raw<E>>(lo);
+        x.ptr += ahead < t1 - 1 ? p.xs : 0;
+        ++ahead;
+    };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (t0 + i < t1) next[i] = row8(x, (int64_t)(t0 + i) * p.xs);
-    for (int t = t0; t < t1; t += kAhead) {
-        u32x4 rows[kAhead];
+    for (int i = 0; i < R; ++i) fetch(i);
+    for (int t = t0; t < t1; t += R) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) rows[i] = next[i];
+        for (int i = 0; i < R; ++i) {
+            widen<E>(rows[i], v[(i + W - 1) % W]);
+            fetch(i);
+            float o[E];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (t + kAhead + i < t1) next[i] = row8(x, (int64_t)(t + kAhead + i) * p.xs);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (t + i >= t1) break;
-            widen8(rows[i], v[W - 1]);
-            float o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < E; ++e) {
                 float a = bias[e];
 #pragma unroll
-                for (int j = 0; j < W; ++j) a = __builtin_fmaf(w[j][e], v[j][e], a);
+                for (int j = 0; j < W; ++j) a = __builtin_fmaf(w[j][e], v[(i + j) % W][e], a);
                 o[e] = p.silu ? a * sigmoid_f(a) : a;
             }
-            put8(y, (int64_t)(t + i) * p.D, narrow8(o));
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[j][e] = v[j + 1][e];
+            if (t + i < t1) y.put(lo, narrow<E>(o));
+            y.ptr += p.D;
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
@@ -140,27 +179,28 @@ __global__ __launch_bounds__(256) void conv_step(ConvParams p) {
     const int64_t slot = p.cache_idx[b];
     if (slot >= (int64_t)p.max_slots) return;  // padding
     const bool init = p.has_init != nullptr && p.has_init[b] != 0;
+    constexpr int E = 8;
     uint16_t *state = p.state_out + slot * (W - 1) * p.D + c;
-    u32x4 win[W];
-    win[W - 1] = row8(p.x, b * p.xs + c);
+    Raw<E> win[W];
+    win[W - 1] = row_of<E>(p.x, b * p.xs + c);
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) win[r] = init ? row8(state, (int64_t)r * p.D) : u32x4{0, 0, 0, 0};
-    float w[W][8], a[8] = {};
-    load_taps<W>(p.weight, c, w);
-    if (p.bias != nullptr) load_state8<false>(p.bias, c, a);
+    for (int r = 0; r < W - 1; ++r) win[r] = init ? row_of<E>(state, (int64_t)r * p.D) : Raw<E>(0);
+    float w[W][E], a[E];
+    load_taps<W, E>(p.weight, c, w);
+    load_bias<E>(p.bias, c, a);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        float v[8];
-        widen8(win[j], v);
+        float v[E];
+        widen<E>(win[j], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = __builtin_fmaf(w[j][e], v[e], a[e]);
+        for (int e = 0; e < E; ++e) a[e] = __builtin_fmaf(w[j][e], v[e], a[e]);
     }
     if (p.silu)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= sigmoid_f(a[e]);
-    put8(p.y, b * p.D + c, narrow8(a));
+        for (int e = 0; e < E; ++e) a[e] *= sigmoid_f(a[e]);
+    put_row<E>(p.y, b * p.D + c, narrow<E>(a));
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) put8(state, (int64_t)r * p.D, win[r + 1]);
+    for (int r = 0; r < W - 1; ++r) put_row<E>(state, (int64_t)r * p.D, win[r + 1]);
 }
 
 // Backward.  With g_t = dy_t silu'(p_t) (0 behind the sequence's end),
@@ -169,17 +209,19 @@ __global__ __launch_bounds__(256) void conv_step(ConvParams p) {
 // token u + W - 1; a piece walks W - 1 tokens past its end, whose g's count
 // for the next piece's weights alone.  The four pieces of a block add their
 // weights' gradients before they store them.
+constexpr int kGradChannels = 4;  // of a lane
 template <int W>
 __global__ __launch_bounds__(256) void conv_grad(ConvParams p) {
-    __shared__ float sums[3][(W + 1) * 8][64];
+    constexpr int E = kGradChannels, R = kAhead<W>;
+    __shared__ float sums[3][(W + 1) * E][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    const int cblocks = (p.D + 511) / 512;
+    const int cblocks = (p.D + 64 * E - 1) / (64 * E);
     const int64_t quad = blockIdx.x / cblocks;
-    const int c = (int)(blockIdx.x % cblocks) * 512 + lane * 8;
+    const int c = (int)(blockIdx.x % cblocks) * 64 * E + lane * E;
     const bool in = c < p.D;
-    float dw[W][8], db[8];
+    float dw[W][E], db[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
         db[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
@@ -192,123 +234,128 @@ __global__ __launch_bounds__(256) void conv_grad(ConvParams p) {
         const uint16_t *state = p.state_in != nullptr ? p.state_in + at : nullptr;
         const int t0 = s * p.tile, t1 = min(q.len, t0 + p.tile);
         // tokens walked: W - 1 past the end of the piece (behind the sequence they hold nothing)
-        const int t2 = t1 + W - 1;
-        float w[W][8], bias[8] = {}, v[W][8], g[W][8];
-        load_taps<W>(p.weight, c, w);
-        if (p.bias != nullptr) load_state8<false>(p.bias, c, bias);
-        u32x4 win[W - 1];
-        load_window<W>(p, q, t0, state, c, win);
+        const int t2 = t1 + W - 1, live = min(q.len, t2);
+        float w[W][E], bias[E], v[W][E], g[W][E];  // v, g: of the walk's i-th token's window at (i + j) % W
+        load_taps<W, E>(p.weight, c, w);
+        load_bias<E>(p.bias, c, bias);
+        Raw<E> win[W - 1];
+        load_window<W, E>(p, q, t0, state, c, win);
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
-            widen8(win[r], v[r]);
+            widen<E>(win[r], v[r]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[r][e] = 0.f;
+            for (int e = 0; e < E; ++e) g[r][e] = 0.f;
         }
-        const uint16_t *x = p.x + (int64_t)q.begin * p.xs + c;
-        const uint16_t *dy = p.dy + (int64_t)q.begin * p.D + c;
-        uint16_t *dx = p.dx + (int64_t)q.begin * p.D + c;
-        const int live = min(q.len, t2);
-        u32x4 nx[kAhead], ng[kAhead];
+        Scalar<const uint16_t> x(p.x + (int64_t)(q.begin + t0) * p.xs), dy(p.dy + (int64_t)(q.begin + t0) * p.D);
+        Scalar<uint16_t> dx(p.dx + (int64_t)(q.begin + t0 - (W - 1)) * p.D);  // (row u of the walk)
+        const uint32_t lo = c * 2;
+        Raw<E> rx[R], rg[R];
+        int next = t0;  // the row that is fetched next
+        auto fetch = [&](int i) {
+            rx[i] = x.at<Raw<E>>(lo);
+            rg[i] = dy.at<Raw<E>>(lo);
+            x.ptr += next < live - 1 ? p.xs : 0;
+            dy.ptr += next < live - 1 ? p.D : 0;
+            ++next;
+        };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            nx[i] = ng[i] = u32x4{0, 0, 0, 0};
-            if (t0 + i < live) {
-                nx[i] = row8(x, (int64_t)(t0 + i) * p.xs);
-                ng[i] = row8(dy, (int64_t)(t0 + i) * p.D);
-            }
+        for (int i = 0; i < R; ++i) {
+            if (live > t0)
+                fetch(i);
+            else  // a sequence without tokens
+                rx[i] = rg[i] = Raw<E>(0);
         }
-        for (int t = t0; t < t2; t += kAhead) {
-            u32x4 rx[kAhead], rg[kAhead];
+        // WHOLE: all tokens of the group are the piece's own.  INNER: and the rows that they finish as well.
+        auto group = [&](int t, auto whole, auto inner) {
+            constexpr bool WHOLE = decltype(whole)::value, INNER = decltype(inner)::value;
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                rx[i] = nx[i];
-                rg[i] = ng[i];
-                nx[i] = ng[i] = u32x4{0, 0, 0, 0};
-                if (t + kAhead + i < live) {
-                    nx[i] = row8(x, (int64_t)(t + kAhead + i) * p.xs);
-                    ng[i] = row8(dy, (int64_t)(t + kAhead + i) * p.D);
-                }
-            }
+            for (int i = 0; i < R; ++i) {
+                float(&vn)[E] = v[(i + W - 1) % W], (&gn)[E] = g[(i + W - 1) % W];
+                widen<E>(rx[i], vn);
+                widen<E>(rg[i], gn);
+                if (live > t0) fetch(i);
+                if (p.silu)
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (t + i >= t2) break;
-                const int u = t + i - (W - 1);  // finished by this token
-                widen8(rx[i], v[W - 1]);
-                widen8(rg[i], g[W - 1]);
-                const bool count = t + i < t1;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (t + i >= q.len) {
-                        g[W - 1][e] = 0.f;  // also where 0 silu'(p) is NaN
-                    } else if (p.silu) {
+                    for (int e = 0; e < E; ++e) {
                         float a = bias[e];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) a = __builtin_fmaf(w[j][e], v[j][e], a);
+                        for (int j = 0; j < W; ++j) a = __builtin_fmaf(w[j][e], v[(i + j) % W][e], a);
                         const float o = sigmoid_f(a);
-                        g[W - 1][e] *= __builtin_fmaf(a * o, 1.f - o, o);
+                        gn[e] *= __builtin_fmaf(a * o, 1.f - o, o);
                     }
-                    if (count) {
-                        db[e] += g[W - 1][e];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][e] = __builtin_fmaf(g[W - 1][e], v[j][e], dw[j][e]);
+                for (int e = 0; e < E; ++e) {
+                    if (!WHOLE) gn[e] = t + i < q.len ? gn[e] : 0.f;
+                    const float own = WHOLE || t + i < t1 ? gn[e] : 0.f;
+                    db[e] += own;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        // (x behind the sequence is not there: 0 times it may be NaN)
+                        const float xv = WHOLE || t + i < t1 ? v[(i + j) % W][e] : 0.f;
+                        dw[j][e] = __builtin_fmaf(own, xv, dw[j][e]);
                     }
                 }
-                const bool ahead = u < 0;  // the state's rows, which the first piece finishes
-                if (ahead ? s == 0 && p.d_init != nullptr : u >= t0) {
-                    float o[8] = {};
+                const int u = t + i - (W - 1);       // finished by this token
+                const bool ahead = !INNER && u < 0;  // the state's rows, which the first piece finishes
+                if (INNER || (ahead ? s == 0 && p.d_init != nullptr : u >= t0 && u < t1)) {
+                    float o[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = 0.f;
                     const int r = u - (q.len - (W - 1));  // of the state that the sequence leaves
-                    if (p.d_final != nullptr && r >= 0)
-                        load_state8<true>(p.d_final, at + (int64_t)r * p.D + c, o);
+                    if (!WHOLE && p.d_final != nullptr && r >= 0)
+                        widen<E>(row_of<E>(p.d_final, at + (int64_t)r * p.D + c), o);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < E; ++e)
 #pragma unroll
-                        for (int k = 0; k < W; ++k) o[e] = __builtin_fmaf(w[W - 1 - k][e], g[k][e], o[e]);
+                        for (int k = 0; k < W; ++k)
+                            o[e] = __builtin_fmaf(w[W - 1 - k][e], g[(i + k) % W][e], o[e]);
                     if (ahead)
-                        put8(p.d_init, at + (int64_t)(u + W - 1) * p.D + c, narrow8(o));
+                        put_row<E>(p.d_init, at + (int64_t)(u + W - 1) * p.D + c, narrow<E>(o));
                     else
-                        put8(dx, (int64_t)u * p.D, narrow8(o));
+                        dx.put(lo, narrow<E>(o));
                 }
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[j][e] = v[j + 1][e];
-                        g[j][e] = g[j + 1][e];
-                    }
+                dx.ptr += p.D;
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        int t = t0;
+        if (t + R <= t1) {
+            group(t, std::true_type{}, std::false_type{});
+            for (t += R; t + R <= t1; t += R) group(t, std::true_type{}, std::true_type{});
         }
+        for (; t < t2; t += R) group(t, std::false_type{}, std::false_type{});
     }
     // the four pieces' sums, by the first wavefront
     if (wave > 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            sums[wave - 1][W * 8 + e][lane] = db[e];
+        for (int e = 0; e < E; ++e) {
+            sums[wave - 1][W * E + e][lane] = db[e];
 #pragma unroll
-            for (int j = 0; j < W; ++j) sums[wave - 1][j * 8 + e][lane] = dw[j][e];
+            for (int j = 0; j < W; ++j) sums[wave - 1][j * E + e][lane] = dw[j][e];
         }
     }
     __syncthreads();
     if (wave > 0 || !in) return;
     float *part = p.part + quad * (W + 1) * p.D;
-    // [channel][tap] as the weights lie, then the bias
+    float f[E * W];  // [channel][tap] as the weights lie
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
 #pragma unroll
         for (int n = 0; n < 3; ++n) {
-            db[e] += sums[n][W * 8 + e][lane];
+            db[e] += sums[n][W * E + e][lane];
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][e] += sums[n][j * 8 + e][lane];
+            for (int j = 0; j < W; ++j) dw[j][e] += sums[n][j * E + e][lane];
         }
-    }
-    float f[8 * W];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int j = 0; j < W; ++j) f[e * W + j] = dw[j][e];
+    }
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i)
+    for (int i = 0; i < E * W / 4; ++i)
         reinterpret_cast<f32x4 *>(part + (int64_t)c * W)[i] = f32x4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-    store_state8<false>(part, (int64_t)W * p.D + c, db);
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i)
+        reinterpret_cast<f32x4 *>(part + (int64_t)W * p.D + c)[i] =
+            f32x4{db[4 * i], db[4 * i + 1], db[4 * i + 2], db[4 * i + 3]};
 }
 
 template <typename F>
@@ -321,13 +368,22 @@ hipError_t by_width(int width, F f) {
 int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 }  // namespace
 
-void conv_shape(ConvParams &p, bool backward) {
+void conv_shape(ConvParams &p, int width, bool backward) {
     p.tile = 32;
     p.places = p.T / p.tile + p.batch;
-    (void)backward;
+    if (!backward) return;
+    // whole groups with the W - 1 tokens behind a piece, as many pieces as are resident (two wavefronts a SIMD) or
+    // groups to 16
+    const int rows = width == 3 ? kAhead<3> : kAhead<4>;
+    const int64_t cblocks = blocks_of(p.D, 64 * kGradChannels);
+    for (int groups = 2; groups <= 16; ++groups) {
+        p.tile = groups * rows - (width - 1);
+        p.places = p.T / p.tile + p.batch;
+        if (p.places * cblocks <= 2048) break;
+    }
 }
 int64_t conv_parts(const ConvParams &p) { return blocks_of(p.places, 4); }
-int64_t conv_threads(const ConvParams &p) { return blocks_of(p.places, 4) * 4 * blocks_of(p.D, 512) * 64; }
+int64_t conv_threads(const ConvParams &p) { return blocks_of(p.places, 4) * 4 * blocks_of(p.D, 64 * kGradChannels) * 64; }
 
 hipError_t launch_conv(const ConvParams &p, int width, hipStream_t s) {
     const dim3 grid((unsigned)blocks_of(p.places * blocks_of(p.D, 512), 4));
@@ -339,7 +395,7 @@ hipError_t launch_conv_step(const ConvParams &p, int width, hipStream_t s) {
 }
 hipError_t launch_conv_grad(const ConvParams &p, int width, hipStream_t s) {
     const int64_t quads = conv_parts(p);
-    const dim3 grid((unsigned)(quads * blocks_of(p.D, 512)));
+    const dim3 grid((unsigned)(quads * blocks_of(p.D, 64 * kGradChannels)));
     hipError_t e = by_width(width, [&](auto w) { conv_grad<decltype(w)::value><<<grid, 256, 0, s>>>(p); });
     if (e != hipSuccess) return e;
     const int64_t row = (int64_t)(width + 1) * p.D;

@@ -2,6 +2,8 @@
 // the short convolution and the selective scan.
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_common.hpp"
 
 namespace ssd {
@@ -38,16 +40,53 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
+// Adds to a pointer that is the same in all lanes.
+template <typename T>
+__device__ __forceinline__ T *moved(T *base, int64_t bytes) {
+    typedef std::conditional_t<std::is_const<T>::value, const char, char> Byte;
+    return reinterpret_cast<T *>(reinterpret_cast<Byte *>(base) + bytes);
+}
+// Such a pointer into global memory that stays in scalar registers: a loop that
+// adds to it and to a lane's offset would else be turned into one that adds to
+// 64 lanes' sums.
+template <typename T>
+struct Scalar {
+    __attribute__((address_space(1))) T *ptr;
+    __device__ explicit Scalar(T *p) : ptr((__attribute__((address_space(1))) T *)p) {}
+    template <typename V>
+    __device__ __forceinline__ V at(uint32_t bytes) {
+        typedef __attribute__((address_space(1))) const char *Bytes;
+        asm volatile("" : "+s"(ptr));
+        return *reinterpret_cast<const __attribute__((address_space(1))) V *>(reinterpret_cast<Bytes>(ptr) + bytes);
+    }
+    template <typename V>
+    __device__ __forceinline__ void put(uint32_t bytes, const V &v) {
+        typedef __attribute__((address_space(1))) char *Bytes;
+        asm volatile("" : "+s"(ptr));
+        *reinterpret_cast<__attribute__((address_space(1))) V *>(reinterpret_cast<Bytes>(ptr) + bytes) = v;
+    }
+};
+// ... and reads or writes at a lane's own offset from it, in bytes.
+template <typename V, typename T>
+__device__ __forceinline__ V at_offset(const T *base, uint32_t bytes) {
+    return *reinterpret_cast<const V *>(reinterpret_cast<const char *>(base) + bytes);
+}
+template <typename V, typename T>
+__device__ __forceinline__ void put_offset(T *base, uint32_t bytes, const V &v) {
+    *reinterpret_cast<V *>(reinterpret_cast<char *>(base) + bytes) = v;
+}
+
 // ---------------------------------------------------------------- ragged batches
 
-// Where a sequence lies: rows begin .. begin + len - 1.  Boundaries are clamped
+// Where a sequence lies, the same in all lanes: rows begin .. begin + len - 1.  Boundaries are clamped
 // to 0 .. T, so a wrong table never leads outside the tensors.
 struct Seq {
     int b, begin, len;
 };
 __device__ __forceinline__ int clamp_row(int v, int T) { return v < 0 ? 0 : v > T ? T : v; }
 __device__ __forceinline__ Seq seq_at(const int32_t *qsl, int b, int T) {
-    const int begin = clamp_row(qsl[b], T), end = clamp_row(qsl[b + 1], T);
+    const int begin = __builtin_amdgcn_readfirstlane(clamp_row(qsl[b], T));
+    const int end = __builtin_amdgcn_readfirstlane(clamp_row(qsl[b + 1], T));
     return Seq{b, begin, end > begin ? end - begin : 0};
 }
 
@@ -70,6 +109,7 @@ __device__ __forceinline__ bool find_piece(const int32_t *qsl, int batch, int T,
         lo += k * step;
         hi = hi < lo + step - 1 ? hi : lo + step - 1;
     }
+    lo = __builtin_amdgcn_readfirstlane(lo);
     seq = seq_at(qsl, lo, T);
     s = place - (seq.begin / piece + lo);
     return s >= 0 && (s == 0 || (int64_t)s * piece < seq.len);
@@ -173,7 +213,7 @@ struct ConvParams {
     int64_t places;  // of pieces
 };
 // Tokens of a piece and places, of either direction
-void conv_shape(ConvParams &p, bool backward);
+void conv_shape(ConvParams &p, int width, bool backward);
 int64_t conv_parts(const ConvParams &p);
 int64_t conv_threads(const ConvParams &p);
 hipError_t launch_conv(const ConvParams &p, int width, hipStream_t s);

@@ -77,7 +77,7 @@ ssd_status conv_forward(const ssd_conv_problem *p, void *y, const void *x, const
     if (!all_aligned(16, y, x, weight, bias, state_in, state_out) || !all_aligned(4, qsl, cache_idx))
         return SSD_ERR_MISALIGNED;
     ConvParams a = common(p);
-    conv_shape(a, false);
+    conv_shape(a, p->width, false);
     if (!fits(a)) return SSD_ERR_UNSUPPORTED;
     a.y = static_cast<uint16_t *>(y);
     a.x = static_cast<const uint16_t *>(x);
@@ -285,7 +285,7 @@ ssd_status ssd_causal_conv_workspace_size(const ssd_conv_problem *prob, size_t *
     const ssd_status st = check(prob);
     if (st != SSD_OK) return st;
     ConvParams a = common(prob);
-    conv_shape(a, true);
+    conv_shape(a, prob->width, true);
     if (!fits(a)) return SSD_ERR_UNSUPPORTED;
     *bytes = conv_workspace(a, prob->width);
     return SSD_OK;
@@ -304,7 +304,7 @@ ssd_status ssd_causal_conv_varlen_bwd(const ssd_conv_problem *prob, void *dx, fl
         !aligned(query_start_loc, 4))
         return SSD_ERR_MISALIGNED;
     ConvParams a = common(prob);
-    conv_shape(a, true);
+    conv_shape(a, prob->width, true);
     if (!fits(a)) return SSD_ERR_UNSUPPORTED;
     const ssd_status sw = check_workspace(conv_workspace(a, prob->width), workspace, workspace_bytes);
     if (sw != SSD_OK) return sw;

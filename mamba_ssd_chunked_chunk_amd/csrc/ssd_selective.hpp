@@ -97,6 +97,7 @@ __device__ __forceinline__ bool find_cut(const ScanParams &p, int place, Seq &q,
         lo += k * step;
         hi = hi < lo + step - 1 ? hi : lo + step - 1;
     }
+    lo = __builtin_amdgcn_readfirstlane(lo);
     q = seq_at(p.qsl, lo, p.T);
     s = place - (int)cut_place(p, q);
     return q.len > p.cut && s >= 0 && (int64_t)s * p.seg < q.len;

@@ -11,8 +11,6 @@
 // gradients, become one a lane in 6 steps, each of which adds what two lanes
 // hold of half the values.  They leave as fp32 for each 64 channels, and a last
 // kernel adds the blocks of a group, in their order.
-#include <type_traits>
-
 #include "ssd_selective.hpp"
 
 namespace ssd {
@@ -115,22 +113,6 @@ __device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, co
     }
     if (mine)
         *reinterpret_cast<f32x4 *>(p.adj + (cut_place(p, q) + s) * p.D * p.N + at) = f32x4{u[0], u[1], u[2], u[3]};
-}
-
-// Adds to a pointer that is the same in all lanes.
-template <typename T>
-__device__ __forceinline__ T *moved(T *base, int64_t bytes) {
-    typedef std::conditional_t<std::is_const<T>::value, const char, char> Byte;
-    return reinterpret_cast<T *>(reinterpret_cast<Byte *>(base) + bytes);
-}
-// ... and reads or writes at a lane's own offset from it, in bytes.
-template <typename V, typename T>
-__device__ __forceinline__ V at_offset(const T *base, uint32_t bytes) {
-    return *reinterpret_cast<const V *>(reinterpret_cast<const char *>(base) + bytes);
-}
-template <typename V, typename T>
-__device__ __forceinline__ void put_offset(T *base, uint32_t bytes, const V &v) {
-    *reinterpret_cast<V *>(reinterpret_cast<char *>(base) + bytes) = v;
 }
 
 // One segment of a sequence (or all of it) and 64 channels.
