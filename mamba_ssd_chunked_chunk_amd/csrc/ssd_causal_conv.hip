@@ -168,39 +168,54 @@ __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
     }
 }
 
-// One token a sequence.  A thread takes 8 channels.
-template <int W>
+// One token a sequence.  A thread takes 8 channels of several sequences, whose
+// rows are all on their way before the first is worked on.
+constexpr int kStepSeqs = 2;
+template <int W, int SEQS>
 __global__ __launch_bounds__(256) void conv_step(ConvParams p) {
+    constexpr int E = 8;
     const int cthreads = p.D / 8;
     const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t b = item / cthreads;
-    if (b >= p.batch) return;
+    const int64_t b0 = item / cthreads * SEQS;
     const int c = (int)(item % cthreads) * 8;
-    const int64_t slot = p.cache_idx[b];
-    if (slot >= (int64_t)p.max_slots) return;  // padding
-    const bool init = p.has_init != nullptr && p.has_init[b] != 0;
-    constexpr int E = 8;
-    uint16_t *state = p.state_out + slot * (W - 1) * p.D + c;
-    Raw<E> win[W];
-    win[W - 1] = row_of<E>(p.x, b * p.xs + c);
+    Raw<E> win[SEQS][W];
+    int64_t at[SEQS];
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) win[r] = init ? row_of<E>(state, (int64_t)r * p.D) : Raw<E>(0);
-    float w[W][E], a[E];
-    load_taps<W, E>(p.weight, c, w);
-    load_bias<E>(p.bias, c, a);
+    for (int k = 0; k < SEQS; ++k) {
+        const int64_t b = b0 + k;
+        const int64_t slot = b < p.batch ? (int64_t)p.cache_idx[b] : (int64_t)p.max_slots;
+        at[k] = slot < (int64_t)p.max_slots ? slot * (W - 1) * p.D + c : -1;  // none: padding
+        if (at[k] < 0) continue;
+        const bool init = p.has_init != nullptr && p.has_init[b] != 0;
+        win[k][W - 1] = row_of<E>(p.x, b * p.xs + c);
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        float v[E];
-        widen<E>(win[j], v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = __builtin_fmaf(w[j][e], v[e], a[e]);
+        for (int r = 0; r < W - 1; ++r)
+            win[k][r] = init ? row_of<E>(p.state_out, at[k] + (int64_t)r * p.D) : Raw<E>(0);
     }
-    if (p.silu)
+    if (b0 >= p.batch) return;
+    float w[W][E], bias[E];
+    load_taps<W, E>(p.weight, c, w);
+    load_bias<E>(p.bias, c, bias);
 #pragma unroll
-        for (int e = 0; e < E; ++e) a[e] *= sigmoid_f(a[e]);
-    put_row<E>(p.y, b * p.D + c, narrow<E>(a));
+    for (int k = 0; k < SEQS; ++k) {
+        if (at[k] < 0) continue;
+        float a[E];
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) put_row<E>(state, (int64_t)r * p.D, win[r + 1]);
+        for (int e = 0; e < E; ++e) a[e] = bias[e];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            float v[E];
+            widen<E>(win[k][j], v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] = __builtin_fmaf(w[j][e], v[e], a[e]);
+        }
+        if (p.silu)
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] *= sigmoid_f(a[e]);
+        put_row<E>(p.y, (b0 + k) * p.D + c, narrow<E>(a));
+#pragma unroll
+        for (int r = 0; r < W - 1; ++r) put_row<E>(p.state_out, at[k] + (int64_t)r * p.D, win[k][r + 1]);
+    }
 }
 
 // Backward.  With g_t = dy_t silu'(p_t) (0 behind the sequence's end),
@@ -390,8 +405,14 @@ hipError_t launch_conv(const ConvParams &p, int width, hipStream_t s) {
     return by_width(width, [&](auto w) { conv_fwd<decltype(w)::value><<<grid, 256, 0, s>>>(p); });
 }
 hipError_t launch_conv_step(const ConvParams &p, int width, hipStream_t s) {
-    const dim3 grid((unsigned)blocks_of((int64_t)p.batch * (p.D / 8), 256));
-    return by_width(width, [&](auto w) { conv_step<decltype(w)::value><<<grid, 256, 0, s>>>(p); });
+    return by_width(width, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        auto grid = [&](int seqs) { return dim3((unsigned)blocks_of(blocks_of(p.batch, seqs) * (p.D / 8), 256)); };
+        if (p.batch >= 16)
+            conv_step<W, kStepSeqs><<<grid(kStepSeqs), 256, 0, s>>>(p);
+        else
+            conv_step<W, 1><<<grid(1), 256, 0, s>>>(p);
+    });
 }
 hipError_t launch_conv_grad(const ConvParams &p, int width, hipStream_t s) {
     const int64_t quads = conv_parts(p);

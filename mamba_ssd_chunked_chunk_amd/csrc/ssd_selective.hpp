@@ -75,14 +75,56 @@ __device__ __forceinline__ int64_t cut_place(const ScanParams &p, const Seq &q) 
     return q.begin / p.seg + min(q.b, q.begin / (p.cut + 1));
 }
 
-__device__ __forceinline__ int segments_of(const ScanParams &p, const Seq &q) {
-    return q.len > p.cut ? (q.len + p.seg - 1) / p.seg : 1;
+// What a workgroup works on: segment s of nseg of a sequence, and the number
+// that no other segment of any sequence has.
+struct Piece {
+    Seq q;
+    int s, nseg, number;
+};
+__device__ __forceinline__ int segments_of(const ScanParams &p, int len) {
+    return len > p.cut ? (len + p.seg - 1) / p.seg : 1;
 }
-// The cut sequence and its segment at one of these places; false where none is.
-// (Places never meet, so the sequence is the last whose first place is not
-// behind it.)
-__device__ __forceinline__ bool find_cut(const ScanParams &p, int place, Seq &q, int &s) {
+
+// The piece at a place of the grid; false where there is none.  With CUT, of the
+// places of cut sequences alone.
+//
+// Up to 64 sequences are numbered one behind the other, a sequence a lane, those of
+// the longest pieces first (32 ragged prompts 988 -> 936 us): gaps between them
+// would leave whole rows of compute units without work, as they come in step with
+// the units that the workgroups are given to (states of 8 x 2048 tokens 430 -> 350
+// us).  More of them have the places of find_piece and cut_place, with gaps.
+template <bool CUT>
+__device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &w) {
     const int lane = threadIdx.x & 63;
+    if (p.batch <= 64) {
+        const int begin = lane < p.batch ? clamp_row(p.qsl[lane], p.T) : 0;
+        const int end = lane < p.batch ? clamp_row(p.qsl[lane + 1], p.T) : 0;
+        const int len = end > begin ? end - begin : 0;
+        const int n = lane < p.batch ? segments_of(p, len) : 0;
+        // the longest pieces first
+        const int key = lane < p.batch ? ((n > 1 ? p.seg : len) << 6 | (63 - lane)) : -1;
+        int rank = 0;
+        for (int j = 0; j < p.batch; ++j) rank += __builtin_amdgcn_readlane(key, j) > key ? 1 : 0;
+        if (lane >= p.batch) rank = lane;
+        const int order = __builtin_amdgcn_ds_permute(rank * 4, lane);  // the sequence of this rank
+        const int nr = __builtin_amdgcn_ds_bpermute(order * 4, n);
+        const int all = wave_incl_scan(nr), mine = CUT ? wave_incl_scan(nr > 1 ? nr : 0) : all;
+        const uint64_t m = __ballot(mine > place);
+        if (m == 0) return false;
+        const int at = __builtin_ctzll(m), b = __builtin_amdgcn_readlane(order, at);
+        w.q = Seq{b, __builtin_amdgcn_readlane(begin, b), __builtin_amdgcn_readlane(len, b)};
+        w.nseg = __builtin_amdgcn_readlane(n, b);
+        w.s = place - (__builtin_amdgcn_readlane(mine, at) - w.nseg);
+        w.number = __builtin_amdgcn_readlane(all, at) - w.nseg + w.s;
+        return true;
+    }
+    if (!CUT) {
+        const bool found = find_piece(p.qsl, p.batch, p.T, p.seg, place, w.q, w.s);
+        w.nseg = segments_of(p, w.q.len);
+        w.number = place;
+        return found && w.s < w.nseg;
+    }
+    // (places of cut sequences never meet, so the owner is the last sequence whose first place is not behind this one)
     int lo = 0, hi = p.batch - 1;
     while (hi > lo) {
         const int step = (hi - lo + 63) / 64;
@@ -98,9 +140,11 @@ __device__ __forceinline__ bool find_cut(const ScanParams &p, int place, Seq &q,
         hi = hi < lo + step - 1 ? hi : lo + step - 1;
     }
     lo = __builtin_amdgcn_readfirstlane(lo);
-    q = seq_at(p.qsl, lo, p.T);
-    s = place - (int)cut_place(p, q);
-    return q.len > p.cut && s >= 0 && (int64_t)s * p.seg < q.len;
+    w.q = seq_at(p.qsl, lo, p.T);
+    w.nseg = segments_of(p, w.q.len);
+    w.s = place - (int)cut_place(p, w.q);
+    w.number = w.q.begin / p.seg + w.q.b + w.s;
+    return w.nseg > 1 && w.s >= 0 && w.s < w.nseg;
 }
 
 // The state that enters segment s > 0 from the states that the segments ahead

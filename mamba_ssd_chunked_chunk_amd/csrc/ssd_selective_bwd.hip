@@ -117,7 +117,9 @@ __device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, co
 
 // One segment of a sequence (or all of it) and 64 channels.
 template <int NW>
-__device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const Seq &q, int s, int nseg, int block) {
+__device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const Piece &piece, int block) {
+    const Seq &q = piece.q;
+    const int s = piece.s, nseg = piece.nseg;
     constexpr int NT = NW * 64, K = kGradTile, kItems = (K * 32 + NT - 1) / NT, kStep = NT / 32;
     constexpr int kTeams = NT < 256 ? kStep : 8;  // threads that finish the same channels
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
@@ -360,7 +362,7 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
         dtp = moved(dtp, -(int64_t)K * ys);
         if (gate) dzp = moved(dzp, -(int64_t)K * ys);
     }
-    const int64_t place = q.begin / p.seg + q.b + s;
+    const int64_t place = piece.number;
     if (mine) {
         const f32x4 v = {u[0], u[1], u[2], u[3]};
         *reinterpret_cast<f32x4 *>(p.dA_part + place * p.D * p.N + at) = f32x4{dA[0], dA[1], dA[2], dA[3]};
@@ -397,33 +399,27 @@ template <int NW>
 __global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_first(ScanParams p) {
     __shared__ Shared<NW> lds;
     const int place = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
-    Seq q;
-    int s;
-    const bool found = find_piece(p.qsl, p.batch, p.T, p.seg, place, q, s);
-    const int nseg = found ? segments_of(p, q) : 0;
-    if (!found || s >= nseg) {  // an empty place adds nothing
-        const Span w = span_of(p, block);
+    Piece w;
+    if (!piece_at<false>(p, place, w)) {  // an empty place adds nothing
+        const Span c = span_of(p, block);
         const int lane = threadIdx.x & 63, n0 = threadIdx.x / 64 * 4;
-        if (lane < w.nch && n0 < p.N)
-            *reinterpret_cast<f32x4 *>(p.dA_part + ((int64_t)place * p.D + w.ch0 + lane) * p.N + n0) =
+        if (lane < c.nch && n0 < p.N)
+            *reinterpret_cast<f32x4 *>(p.dA_part + ((int64_t)place * p.D + c.ch0 + lane) * p.N + n0) =
                 f32x4{0.f, 0.f, 0.f, 0.f};
-        float *dD = p.dD_part + (int64_t)place * 2 * p.D + w.ch0;
-        if (threadIdx.x < w.nch) dD[threadIdx.x] = dD[p.D + threadIdx.x] = 0.f;
+        float *dD = p.dD_part + (int64_t)place * 2 * p.D + c.ch0;
+        if (threadIdx.x < c.nch) dD[threadIdx.x] = dD[p.D + threadIdx.x] = 0.f;
         return;
     }
-    if (s == nseg - 1)
-        grad<NW>(p, lds, q, s, nseg, block);
-    else if (s > 0)
-        adjoint<NW>(p, lds, q, s, span_of(p, block));
+    if (w.s == w.nseg - 1)
+        grad<NW>(p, lds, w, block);
+    else if (w.s > 0)
+        adjoint<NW>(p, lds, w.q, w.s, span_of(p, block));
 }
 template <int NW>
 __global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_rest(ScanParams p) {
     __shared__ Shared<NW> lds;
-    Seq q;
-    int s;
-    if (!find_cut(p, blockIdx.x / p.blocks, q, s)) return;
-    const int nseg = segments_of(p, q);
-    if (s < nseg - 1) grad<NW>(p, lds, q, s, nseg, blockIdx.x % p.blocks);
+    Piece w;
+    if (piece_at<true>(p, blockIdx.x / p.blocks, w) && w.s < w.nseg - 1) grad<NW>(p, lds, w, blockIdx.x % p.blocks);
 }
 
 // The sums over blocks and places: dB and dC, the blocks of a group added in

@@ -232,25 +232,21 @@ __device__ __forceinline__ bool padding(const ScanParams &p, int b) {
 template <int NW, Walk WALK>
 __global__ __launch_bounds__(NW * 64) void scan_first(ScanParams p) {
     __shared__ Shared<NW> lds;
-    Seq q;
-    int s;
-    if (!find_piece(p.qsl, p.batch, p.T, p.seg, blockIdx.x / p.blocks, q, s)) return;
-    const int nseg = segments_of(p, q);
-    if (padding(p, q.b) || (s > 0 && s >= nseg - 1)) return;
-    const Span w = span_of(p, blockIdx.x % p.blocks);
-    if (s == 0)
-        walk<NW, WALK>(p, lds, q, s, nseg, w);
-    else
-        walk<NW, kStates>(p, lds, q, s, nseg, w);
+    Piece w;
+    if (!piece_at<false>(p, blockIdx.x / p.blocks, w) || padding(p, w.q.b)) return;
+    const Span c = span_of(p, blockIdx.x % p.blocks);
+    if (w.s == 0)
+        walk<NW, WALK>(p, lds, w.q, w.s, w.nseg, c);
+    else if (w.s < w.nseg - 1)
+        walk<NW, kStates>(p, lds, w.q, w.s, w.nseg, c);
 }
 
 template <int NW, Walk WALK>
 __global__ __launch_bounds__(NW * 64) void scan_rest(ScanParams p) {
     __shared__ Shared<NW> lds;
-    Seq q;
-    int s;
-    if (!find_cut(p, blockIdx.x / p.blocks, q, s) || s == 0 || padding(p, q.b)) return;
-    walk<NW, WALK>(p, lds, q, s, segments_of(p, q), span_of(p, blockIdx.x % p.blocks));
+    Piece w;
+    if (!piece_at<true>(p, blockIdx.x / p.blocks, w) || w.s == 0 || padding(p, w.q.b)) return;
+    walk<NW, WALK>(p, lds, w.q, w.s, w.nseg, span_of(p, blockIdx.x % p.blocks));
 }
 
 template <Walk WALK>
@@ -268,11 +264,18 @@ hipError_t launch_walk(const ScanParams &p, hipStream_t s) {
 void scan_shape(ScanParams &p, bool backward) {
     p.Dg = p.D / p.G;
     p.blocks = p.G * ((p.Dg + 63) / 64);
-    // SEGMENT_RULE
-    const int64_t waves = (int64_t)p.blocks * waves_of(p.N), fill = backward ? 2048 : 4096;
+    // Segments: long enough that a workgroup's chaining of those ahead of it stays below its walk (the root of T: one
+    // sequence of 4096 tokens and 2048 channels 178, 88, 83, 104 us with 32, 64, 128, 256 tokens), and that there are
+    // no more of them than balance the card: 16 workgroups of 4 wavefronts a unit (65536 tokens 849, 872, 1026 us with
+    // 512, 768, 2048), in the backward pass, which would repeat more work, the two wavefronts a SIMD that are resident
+    // (8 x 2048 tokens, 4096 channels 1.25 ms uncut, 1.58 in segments of 512).  Where the sequences alone fill
+    // the card only those that stand out are cut (32 ragged prompts 936, 860, 890 us at 686, 1024, 1376 tokens; 40 of
+    // 300 tokens 160 us in segments of 112, 110 uncut).
+    const int64_t waves = (int64_t)p.blocks * waves_of(p.N);
     int64_t seg = std::max<int64_t>(backward ? 32 : 64, (int64_t)sqrt((double)p.T));
     seg = std::max(seg, (int64_t)p.T * waves / (backward ? 2048 : 16384));
-    if (p.batch * waves >= fill) seg = std::max<int64_t>(seg, p.T / p.batch / (backward ? 1 : 2));
+    if (p.batch * waves >= (backward ? 2048 : 4096))
+        seg = std::max<int64_t>(seg, (int64_t)(p.T / p.batch) * (backward ? 4 : 3) / 4);
     seg = (seg + kTile - 1) / kTile * kTile;
     p.seg = (int)seg;
     p.cut = (int)std::min<int64_t>(2 * seg, INT32_MAX);

@@ -20,64 +20,63 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// 4 bf16 from a 4-byte boundary on
-__device__ __forceinline__ void load_quad(const uint16_t *ptr, float (&o)[4]) {
-    const uint32_t *s = reinterpret_cast<const uint32_t *>(ptr);
-    widen4(u32x2{s[0], s[1]}, o);
-}
-
 template <int LANES, int SEQS, bool SB>
 __global__ __launch_bounds__(kThreads) void scan_step(ScanParams p, int cblocks) {
     const int cb = blockIdx.x % cblocks, b0 = blockIdx.x / cblocks * SEQS;
     const int ch = cb * (kThreads / LANES) + threadIdx.x / LANES, n0 = threadIdx.x % LANES * 4;
     const bool in = ch < p.D && n0 < p.N;
     const int64_t at = (int64_t)ch * p.N + n0;
-    float h[SEQS][4];
-    int64_t slot[SEQS];
-#pragma unroll
-    for (int k = 0; k < SEQS; ++k) {
-        const int b = b0 + k;
-        slot[k] = b < p.batch ? (int64_t)p.cache_idx[b] : (int64_t)p.max_slots;  // max_slots or more: nothing
-        const bool init = b < p.batch && p.has_init != nullptr && p.has_init[b] != 0;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (in && init && slot[k] < (int64_t)p.max_slots)
-            v = load_state4<SB>(p.state_in, slot[k] * p.D * p.N + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[k][i] = v[i];
-    }
-    float A[4] = {};
-    if (in) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(p.A + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) A[i] = v[i] * kLog2e;
-    }
     const int g = ch / p.Dg;
+    f32x4 h[SEQS];
+    int64_t slot[SEQS];
+    uint32_t bw[SEQS][2], cw[SEQS][2], x[SEQS], dt[SEQS], z[SEQS];
+    // all that is read, ahead of all that is computed
 #pragma unroll
     for (int k = 0; k < SEQS; ++k) {
         const int64_t b = b0 + k;
-        if (slot[k] >= (int64_t)p.max_slots) continue;
-        float B[4] = {}, C[4] = {}, y = 0.f, x = 0.f;
-        if (in) {
-            load_quad(p.B + b * p.bs + g * p.N + n0, B);
-            load_quad(p.C + b * p.cs + g * p.N + n0, C);
-            x = bf16_bits_to_float(p.x[b * p.xs + ch]);
-            const float step = time_step(p, bf16_bits_to_float(p.dt[b * p.dts + ch]) + (p.bias != nullptr ? p.bias[ch] : 0.f));
-            const float u = step * x;
+        slot[k] = b < p.batch ? (int64_t)p.cache_idx[b] : (int64_t)p.max_slots;  // max_slots or more: nothing
+        const bool init = b < p.batch && p.has_init != nullptr && p.has_init[b] != 0;
+        h[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        x[k] = dt[k] = z[k] = bw[k][0] = bw[k][1] = cw[k][0] = cw[k][1] = 0;
+        if (!in || slot[k] >= (int64_t)p.max_slots) continue;
+        if (init) h[k] = load_state4<SB>(p.state_in, slot[k] * p.D * p.N + at);
+        const uint32_t *B = reinterpret_cast<const uint32_t *>(p.B + b * p.bs + g * p.N + n0);
+        const uint32_t *C = reinterpret_cast<const uint32_t *>(p.C + b * p.cs + g * p.N + n0);
+        bw[k][0] = B[0];
+        bw[k][1] = B[1];
+        cw[k][0] = C[0];
+        cw[k][1] = C[1];
+        x[k] = p.x[b * p.xs + ch];
+        dt[k] = p.dt[b * p.dts + ch];
+        if (p.z != nullptr) z[k] = p.z[b * p.zs + ch];
+    }
+    f32x4 A = {0.f, 0.f, 0.f, 0.f};
+    float bias = 0.f, skip = 0.f;
+    if (in) {
+        A = *reinterpret_cast<const f32x4 *>(p.A + at) * kLog2e;
+        if (p.bias != nullptr) bias = p.bias[ch];
+        if (p.Dskip != nullptr) skip = p.Dskip[ch];
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[k][i] = __builtin_fmaf(fast_exp2(step * A[i]), h[k][i], u * B[i]);
-                y = __builtin_fmaf(C[i], h[k][i], y);
-            }
-            store_state4<SB>(p.state_out, slot[k] * p.D * p.N + at, f32x4{h[k][0], h[k][1], h[k][2], h[k][3]});
+    for (int k = 0; k < SEQS; ++k) {
+        if (slot[k] >= (int64_t)p.max_slots) continue;
+        float y = 0.f;
+        const float xv = bf16_bits_to_float(x[k]), step = time_step(p, bf16_bits_to_float(dt[k]) + bias);
+        const Quad B = quad_of(bw[k][0], bw[k][1]), C = quad_of(cw[k][0], cw[k][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[k][i] = __builtin_fmaf(fast_exp2(step * A[i]), h[k][i], step * xv * B.v[i]);
+            y = __builtin_fmaf(C.v[i], h[k][i], y);
         }
+        if (in) store_state4<SB>(p.state_out, slot[k] * p.D * p.N + at, h[k]);
         y = lanes_sum<LANES>(y);
         if (!in || n0 != 0) continue;
-        if (p.Dskip != nullptr) y = __builtin_fmaf(p.Dskip[ch], x, y);
+        y = __builtin_fmaf(skip, xv, y);
         if (p.z != nullptr) {
-            const float z = bf16_bits_to_float(p.z[b * p.zs + ch]);
-            y *= z * sigmoid_f(z);
+            const float zv = bf16_bits_to_float(z[k]);
+            y *= zv * sigmoid_f(zv);
         }
-        p.y[b * p.D + ch] = float_to_bf16_bits(y);
+        p.y[(b0 + k) * (int64_t)p.D + ch] = float_to_bf16_bits(y);
     }
 }
 
@@ -94,7 +93,7 @@ hipError_t launch_as(const ScanParams &p, hipStream_t s) {
 }
 template <int LANES>
 hipError_t launch_lanes(const ScanParams &p, hipStream_t s) {
-    return p.batch >= 16 ? launch_as<LANES, 4>(p, s) : launch_as<LANES, 1>(p, s);
+    return p.batch >= 16 ? launch_as<LANES, 2>(p, s) : launch_as<LANES, 1>(p, s);
 }
 }  // namespace
 
