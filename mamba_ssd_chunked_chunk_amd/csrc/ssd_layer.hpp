@@ -162,27 +162,47 @@ struct Sum {
 struct Sums {
     Sum s[3];
 };
-constexpr int kSumThreads = 256, kSumColumns = 64;
+constexpr int kSumThreads = 256;
+// Blocks of COLS columns each
+template <int COLS>
 inline __host__ __device__ int64_t sum_blocks(const Sum &s) {
-    return s.out == nullptr ? 0 : (s.width + kSumColumns - 1) / kSumColumns;
+    return s.out == nullptr ? 0 : (s.width + COLS - 1) / COLS;
 }
-// The block-th block of the sums: 16 threads of 4 columns each, 16 parts at a
-// time, in their order.
-__device__ __forceinline__ void add_parts(const Sums &all, int64_t block, f32x4 (&buf)[16][16]) {
+template <int COLS>
+inline __host__ int64_t sum_blocks(const Sums &a) {
+    return sum_blocks<COLS>(a.s[0]) + sum_blocks<COLS>(a.s[1]) + sum_blocks<COLS>(a.s[2]);
+}
+// The block-th of them, a thread 4 columns of every kSumThreads 4 / COLS-th part.
+// (Many parts of few columns want narrow blocks, 1024 of 2560 columns 6.4 us with
+// 32, 8.4 with 64; few of many do not, beside the sums of the scan's backward
+// pass 39 us and 33.)
+template <int COLS>
+__device__ __forceinline__ void add_parts(const Sums &all, int64_t block) {
+    constexpr int kRows = kSumThreads * 4 / COLS, kAtOnce = 8;
+    __shared__ f32x4 buf[kRows][COLS / 4];
     int k = 0;
-    while (k < 2 && block >= sum_blocks(all.s[k])) block -= sum_blocks(all.s[k++]);
+    while (k < 2 && block >= sum_blocks<COLS>(all.s[k])) block -= sum_blocks<COLS>(all.s[k++]);
     const Sum &a = all.s[k];
-    const int col = threadIdx.x % 16, first = threadIdx.x / 16;
-    const int64_t j = block * kSumColumns + col * 4;
+    const int col = threadIdx.x % (COLS / 4), first = threadIdx.x / (COLS / 4);
+    const int64_t j = block * COLS + col * 4;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (j < a.width)
-#pragma unroll 4
-        for (int i = first; i < a.n; i += 16) s += *reinterpret_cast<const f32x4 *>(a.part + i * a.stride + j);
+        for (int i = first; i < a.n; i += kAtOnce * kRows) {
+            f32x4 v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (i + u * kRows < a.n)
+                    v[u] = *reinterpret_cast<const f32x4 *>(a.part + (i + u * kRows) * a.stride + j);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) s += v[u];
+        }
     buf[first][col] = s;
     __syncthreads();
     if (first == 0 && j < a.width) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += buf[i][col];
+        for (int i = 1; i < kRows; ++i) s += buf[i][col];
         *reinterpret_cast<f32x4 *>(a.out + j) = s;
     }
 }

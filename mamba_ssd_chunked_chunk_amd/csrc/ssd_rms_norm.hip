@@ -228,8 +228,7 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
 }
 
 __global__ __launch_bounds__(kSumThreads) void sum_parts(Sums sums) {
-    __shared__ f32x4 buf[16][16];
-    add_parts(sums, blockIdx.x, buf);
+    add_parts<32>(sums, blockIdx.x);
 }
 
 template <int TPR, int VPT>
@@ -282,8 +281,7 @@ hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s) {
 }
 
 hipError_t launch_sums(const Sums &sums, hipStream_t s) {
-    const int64_t blocks = sum_blocks(sums.s[0]) + sum_blocks(sums.s[1]) + sum_blocks(sums.s[2]);
-    sum_parts<<<dim3((unsigned)blocks), kSumThreads, 0, s>>>(sums);
+    sum_parts<<<dim3((unsigned)sum_blocks<32>(sums)), kSumThreads, 0, s>>>(sums);
     return hipGetLastError();
 }
 

@@ -425,8 +425,7 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_rest(ScanP
 // The sums over blocks and places: dB and dC, the blocks of a group added in
 // their order, by the first bc_blocks workgroups, and dA, dD, dbias.
 __global__ __launch_bounds__(kSumThreads) void scan_sums(ScanParams p, int64_t bc_blocks, Sums sums) {
-    __shared__ f32x4 buf[16][16];
-    if (blockIdx.x >= bc_blocks) return add_parts(sums, blockIdx.x - bc_blocks, buf);
+    if (blockIdx.x >= bc_blocks) return add_parts<64>(sums, blockIdx.x - bc_blocks);
     const int quads = p.N / 4;
     int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
     const int j = (int)(i % quads);
@@ -462,8 +461,7 @@ hipError_t launch_scan_grad(const ScanParams &p, hipStream_t s) {
     const int n = (int)p.places;
     const Sums sums = {{{p.dA_part, n, DN, DN, p.dA}, {p.dD_part, n, 2 * p.D, p.D, p.dD},
                         {p.dD_part + p.D, n, 2 * p.D, p.D, p.dbias}}};
-    const int64_t blocks = bc_blocks + sum_blocks(sums.s[0]) + sum_blocks(sums.s[1]) + sum_blocks(sums.s[2]);
-    scan_sums<<<dim3((unsigned)blocks), kSumThreads, 0, s>>>(p, bc_blocks, sums);
+    scan_sums<<<dim3((unsigned)(bc_blocks + sum_blocks<64>(sums))), kSumThreads, 0, s>>>(p, bc_blocks, sums);
     return hipGetLastError();
 }
 

@@ -286,7 +286,7 @@ void scan_shape(ScanParams &p, bool backward) {
 
 int64_t scan_threads(const ScanParams &p, bool backward) {
     const int64_t walk = p.places * p.blocks * 64 * waves_of(p.N);
-    const int64_t sums = backward ? (int64_t)p.T * p.G * (p.N / 2) + 4 * ((int64_t)p.D * (p.N + 2)) + 1024 : 0;
+    const int64_t sums = backward ? (int64_t)p.T * p.G * (p.N / 2) + 8 * ((int64_t)p.D * (p.N + 2)) + 1024 : 0;
     return walk > sums ? walk : sums;
 }
 
