@@ -142,6 +142,7 @@ __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
     Raw<E> rows[R];
     int ahead = t0;  // the row that is fetched next
     auto fetch = [&](int i) {
+        x.hold();
         rows[i] = x.at<Raw<E>>(lo);
         x.ptr += ahead < t1 - 1 ? p.xs : 0;
         ++ahead;
@@ -161,6 +162,7 @@ __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
                 for (int j = 0; j < W; ++j) a = __builtin_fmaf(w[j][e], v[(i + j) % W][e], a);
                 o[e] = p.silu ? a * sigmoid_f(a) : a;
             }
+            y.hold();
             if (t + i < t1) y.put(lo, narrow<E>(o));
             y.ptr += p.D;
             __builtin_amdgcn_sched_barrier(0);
@@ -267,6 +269,8 @@ __global__ __launch_bounds__(256) void conv_grad(ConvParams p) {
         Raw<E> rx[R], rg[R];
         int next = t0;  // the row that is fetched next
         auto fetch = [&](int i) {
+            x.hold();
+            dy.hold();
             rx[i] = x.at<Raw<E>>(lo);
             rg[i] = dy.at<Raw<E>>(lo);
             x.ptr += next < live - 1 ? p.xs : 0;
@@ -310,6 +314,7 @@ __global__ __launch_bounds__(256) void conv_grad(ConvParams p) {
                         dw[j][e] = __builtin_fmaf(own, xv, dw[j][e]);
                     }
                 }
+                dx.hold();
                 const int u = t + i - (W - 1);       // finished by this token
                 const bool ahead = !INNER && u < 0;  // the state's rows, which the first piece finishes
                 if (INNER || (ahead ? s == 0 && p.d_init != nullptr : u >= t0 && u < t1)) {

@@ -48,21 +48,20 @@ __device__ __forceinline__ T *moved(T *base, int64_t bytes) {
 }
 // Such a pointer into global memory that stays in scalar registers: a loop that
 // adds to it and to a lane's offset would else be turned into one that adds to
-// 64 lanes' sums.
+// 64 lanes' sums.  (hold() where all lanes are, at() and put() anywhere.)
 template <typename T>
 struct Scalar {
     __attribute__((address_space(1))) T *ptr;
     __device__ explicit Scalar(T *p) : ptr((__attribute__((address_space(1))) T *)p) {}
+    __device__ __forceinline__ void hold() { asm volatile("" : "+s"(ptr)); }
     template <typename V>
-    __device__ __forceinline__ V at(uint32_t bytes) {
+    __device__ __forceinline__ V at(uint32_t bytes) const {
         typedef __attribute__((address_space(1))) const char *Bytes;
-        asm volatile("" : "+s"(ptr));
         return *reinterpret_cast<const __attribute__((address_space(1))) V *>(reinterpret_cast<Bytes>(ptr) + bytes);
     }
     template <typename V>
-    __device__ __forceinline__ void put(uint32_t bytes, const V &v) {
+    __device__ __forceinline__ void put(uint32_t bytes, const V &v) const {
         typedef __attribute__((address_space(1))) char *Bytes;
-        asm volatile("" : "+s"(ptr));
         *reinterpret_cast<__attribute__((address_space(1))) V *>(reinterpret_cast<Bytes>(ptr) + bytes) = v;
     }
 };

@@ -80,30 +80,47 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
         if (in && p.bias != nullptr) bias[e] = p.bias[w.ch0 + c + e];
         if (OUT && in && p.Dskip != nullptr) skip[e] = p.Dskip[w.ch0 + c + e];
     }
-    const int64_t row0 = q.begin + t0 + r0;
-    const uint16_t *xp = p.x + row0 * p.xs + w.ch0 + c, *dp = p.dt + row0 * p.dts + w.ch0 + c;
+    // rows by an address that all lanes share and the lane's own offset in bytes; rows and channels that are not there
+    // are read as the last and the first there are, and go no further than LDS
+    const int64_t row0 = q.begin + t0;
     const bool gate = OUT && p.z != nullptr;
-    const uint16_t *zp = gate ? p.z + row0 * p.zs + w.ch0 + c : nullptr;
-    uint16_t *yp = OUT ? p.y + row0 * p.D + w.ch0 + c : nullptr;
-    const uint16_t *Bp = p.B + (int64_t)(q.begin + t0) * p.bs + w.g * p.N + n0;
-    const uint16_t *Cp = p.C + (int64_t)(q.begin + t0) * p.cs + w.g * p.N + n0;
-    u32x2 nx[kItems], nd[kItems], nz[kItems];
-    auto fetch = [&](int t) {
+    Scalar<const uint16_t> xp(p.x + row0 * p.xs + w.ch0), dp(p.dt + row0 * p.dts + w.ch0);
+    Scalar<const uint16_t> zp(gate ? p.z + row0 * p.zs + w.ch0 : p.x);
+    Scalar<uint16_t> yp(OUT ? p.y + row0 * p.D + w.ch0 : nullptr);
+    const uint16_t *Bp = p.B + row0 * p.bs + w.g * p.N + n0, *Cp = p.C + row0 * p.cs + w.g * p.N + n0;
+    const uint32_t xs = (uint32_t)p.xs * 2, ds = (uint32_t)p.dts * 2, zs = (uint32_t)p.zs * 2, ys = (uint32_t)p.D * 2;
+    uint32_t xo[kItems], od[kItems], zo[kItems];
+    auto offsets = [&](int n) {  // of a tile of n tokens
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            nx[k] = nd[k] = nz[k] = u32x2{0, 0};
-            const int r = r0 + k * (NT / 16);
-            if (r >= kTile || t + r >= t1 || !in) continue;
-            nx[k] = *reinterpret_cast<const u32x2 *>(xp + k * (NT / 16) * p.xs);
-            nd[k] = *reinterpret_cast<const u32x2 *>(dp + k * (NT / 16) * p.dts);
-            if (gate) nz[k] = *reinterpret_cast<const u32x2 *>(zp + k * (NT / 16) * p.zs);
+            const uint32_t r = min(r0 + k * (NT / 16), n - 1), cc = in ? c * 2 : 0;
+            xo[k] = r * xs + cc;
+            od[k] = r * ds + cc;
+            zo[k] = r * zs + cc;
         }
-        xp += kTile * p.xs;
-        dp += kTile * p.dts;
-        if (gate) zp += kTile * p.zs;
+    };
+    u32x2 nx[kItems], nd[kItems], nz[kItems];
+    auto fetch = [&](int t) {
+        if (t + kTile > t1) offsets(t1 - t);
+        xp.hold();
+        dp.hold();
+        zp.hold();
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            nx[k] = xp.at<u32x2>(xo[k]);
+            nd[k] = dp.at<u32x2>(od[k]);
+            nz[k] = u32x2{0, 0};
+            if (gate) nz[k] = zp.at<u32x2>(zo[k]);
+        }
+        xp.ptr += kTile * p.xs;
+        dp.ptr += kTile * p.dts;
+        if (gate) zp.ptr += kTile * p.zs;
     };
     float steps = 0.f;  // sum of this lane's channel's time steps
-    fetch(t0);
+    if (t0 < t1) {
+        offsets(kTile);
+        fetch(t0);
+    }
     // (loads that have to be here before the loop: a wait inside it would be for the last tile's stores too)
 #pragma unroll
     for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(bias[e]), "+v"(skip[e]), "+v"(A[e]), "+v"(h[e]));
@@ -135,7 +152,9 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
                 float y = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    h[j] = __builtin_fmaf(fast_exp2(e.x * A[j]), h[j], e.y * B.v[j]);
+                    // (a product of two vector registers and a fused add with a scalar one: three vector operands
+                    // would take longer)
+                    h[j] = __builtin_fmaf(e.y, B.v[j], fast_exp2(e.x * A[j]) * h[j]);
                     if (OUT) y = j == 0 ? C.v[j] * h[j] : __builtin_fmaf(C.v[j], h[j], y);
                 }
                 if (STATES) steps += e.x;
@@ -201,15 +220,16 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
                 }
                 out[k] = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
             }
+            yp.hold();
             // the next tile's rows are waited for here, ahead of the stores
 #pragma unroll
             for (int k = 0; k < kItems; ++k) asm volatile("" : "+v"(nx[k]), "+v"(nd[k]), "+v"(nz[k]));
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
                 const int r = r0 + k * (NT / 16);
-                if (r < kTile && t + r < t1 && in) *reinterpret_cast<u32x2 *>(yp + k * (NT / 16) * p.D) = out[k];
+                if (r < kTile && t + r < t1 && in) yp.put((uint32_t)r * ys + c * 2, out[k]);
             }
-            yp += (int64_t)kTile * p.D;
+            yp.ptr += (int64_t)kTile * p.D;
         }
     }
     if (!mine) return;
