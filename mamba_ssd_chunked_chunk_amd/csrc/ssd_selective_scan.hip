@@ -35,7 +35,10 @@ enum Walk { kOutputs, kMarks, kStates };
 template <int NW>
 struct Shared {
     float2 step[kTile][64];  // time step, and times x
-    float y[NW][kTile][64];  // a wavefront's share of C.h
+    union {
+        float y[NW][kTile][64];  // a wavefront's share of C.h
+        f32x4 B[kTile][NW];      // (walks without outputs)
+    };
 };
 
 // One segment of a sequence (or all of it) and 64 channels.
@@ -99,6 +102,11 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
             zo[k] = r * zs + cc;
         }
     };
+    // Walks without outputs take B through LDS, two elements of a token by each of the first threads: few wavefronts a
+    // unit do not hide what scalar loads wait for (8 x 2048 tokens of 4096 channels 350 -> 245 us).
+    const int bt = threadIdx.x / (p.N / 2), bj = threadIdx.x % (p.N / 2) * 2;
+    const uint16_t *wp = OUT ? nullptr : p.B + (row0 + bt) * p.bs + w.g * p.N + bj;
+    uint32_t nb = 0;
     u32x2 nx[kItems], nd[kItems], nz[kItems];
     auto fetch = [&](int t) {
         if (t + kTile > t1) offsets(t1 - t);
@@ -112,6 +120,8 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
             nz[k] = u32x2{0, 0};
             if (gate) nz[k] = zp.at<u32x2>(zo[k]);
         }
+        if (!OUT && bt < kTile && t + bt < t1) nb = *reinterpret_cast<const uint32_t *>(wp);
+        if (!OUT) wp += kTile * p.bs;
         xp.ptr += kTile * p.xs;
         dp.ptr += kTile * p.dts;
         if (gate) zp.ptr += kTile * p.zs;
@@ -141,19 +151,19 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
                 lds.step[r][c + e] = make_float2(step, step * x[e]);
             }
         }
+        if (!OUT && bt < kTile)
+            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(&lds.B[bt][0]) + bj) =
+                make_float2(bf16x2_lo(nb), bf16x2_hi(nb));
         if (t + kTile < t1) fetch(t + kTile);
         __syncthreads();
         if (n0 < p.N) {
             const int n = min(kTile, t1 - t);
-            auto token = [&](int i, const float2 &e, const Words &m) {
+            auto token = [&](int i, const float2 &e, const Quad &B, const Quad &C) {
                 if (WALK == kMarks && i % kGradTile == 0 && mine)
                     *reinterpret_cast<f32x4 *>(mark_at(p, q, t + i, n0, ch)) = f32x4{h[0], h[1], h[2], h[3]};
-                const Quad B = quad_of(m.b[0], m.b[1]), C = quad_of(m.c[0], m.c[1]);
                 float y = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    // (a product of two vector registers and a fused add with a scalar one: three vector operands
-                    // would take longer)
                     h[j] = __builtin_fmaf(e.y, B.v[j], fast_exp2(e.x * A[j]) * h[j]);
                     if (OUT) y = j == 0 ? C.v[j] * h[j] : __builtin_fmaf(C.v[j], h[j], y);
                 }
@@ -163,14 +173,17 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
             if (n == kTile) {
                 Words next[kGroup], now[kGroup];
                 float2 en[kGroup], ee[kGroup];
+                f32x4 bn[kGroup], bb[kGroup];
                 auto ahead = [&](int g) {
 #pragma unroll
                     for (int i = 0; i < kGroup; ++i) {
-                        words_at(Bp, next[i].b);
-                        Bp += p.bs;
-                        if (OUT) {
+                        if constexpr (OUT) {
+                            words_at(Bp, next[i].b);
+                            Bp += p.bs;
                             words_at(Cp, next[i].c);
                             Cp += p.cs;
+                        } else {
+                            bn[i] = lds.B[g + i][wave];
                         }
                         en[i] = lds.step[g + i][lane];
                     }
@@ -180,22 +193,32 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
                 for (int g = 0; g < kTile; g += kGroup) {
 #pragma unroll
                     for (int i = 0; i < kGroup; ++i) {
-                        now[i] = next[i];
+                        if constexpr (OUT)
+                            now[i] = next[i];
+                        else
+                            bb[i] = bn[i];
                         ee[i] = en[i];
                     }
                     if (g + kGroup < kTile) ahead(g + kGroup);
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int i = 0; i < kGroup; ++i) token(g + i, ee[i], now[i]);
+                    for (int i = 0; i < kGroup; ++i) {
+                        if constexpr (OUT)
+                            token(g + i, ee[i], quad_of(now[i].b[0], now[i].b[1]), quad_of(now[i].c[0], now[i].c[1]));
+                        else
+                            token(g + i, ee[i], Quad{{bb[i][0], bb[i][1], bb[i][2], bb[i][3]}}, Quad{});
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
-                    Words m;
-                    words_at(Bp + (int64_t)i * p.bs, m.b);
-                    words_at(Cp + (int64_t)i * p.cs, m.c);
-                    token(i, lds.step[i][lane], m);
+                    if constexpr (OUT) {
+                        token(i, lds.step[i][lane], quad_at(Bp + (int64_t)i * p.bs), quad_at(Cp + (int64_t)i * p.cs));
+                    } else {
+                        const f32x4 B = lds.B[i][wave];
+                        token(i, lds.step[i][lane], Quad{{B[0], B[1], B[2], B[3]}}, Quad{});
+                    }
                 }
             }
         }
