@@ -44,28 +44,12 @@ __device__ __forceinline__ float time_step(const ScanParams &p, float raw) {
     return p.softplus ? softplus_fast(raw) : raw;
 }
 
-// 4 bf16 at an address that is the same in all lanes: a scalar load (the
-// constant address space says that nothing writes there during the kernel) and
-// the scalar unit's shifts.
+// 4 bf16 in two dwords
 struct Quad {
     float v[4];
 };
-struct Words {
-    uint32_t b[2], c[2];  // 4 of B and of C
-};
-__device__ __forceinline__ void words_at(const uint16_t *ptr, uint32_t (&w)[2]) {
-    typedef const __attribute__((address_space(4))) uint32_t *Scalar;
-    const Scalar s = (Scalar)(uintptr_t)ptr;
-    w[0] = s[0];
-    w[1] = s[1];
-}
 __device__ __forceinline__ Quad quad_of(uint32_t a, uint32_t b) {
     return Quad{{bf16x2_lo(a), bf16x2_hi(a), bf16x2_lo(b), bf16x2_hi(b)}};
-}
-__device__ __forceinline__ Quad quad_at(const uint16_t *ptr) {
-    uint32_t w[2];
-    words_at(ptr, w);
-    return quad_of(w[0], w[1]);
 }
 
 // First place of a cut sequence's segments among those of all cut sequences: at
@@ -102,7 +86,7 @@ __device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &
         const int len = end > begin ? end - begin : 0;
         const int n = lane < p.batch ? segments_of(p, len) : 0;
         // the longest pieces first
-        const int key = lane < p.batch ? ((n > 1 ? p.seg : len) << 6 | (63 - lane)) : -1;
+        const int key = lane < p.batch ? (min(n > 1 ? p.seg : len, 1 << 24) << 6 | (63 - lane)) : -1;
         int rank = 0;
         for (int j = 0; j < p.batch; ++j) rank += __builtin_amdgcn_readlane(key, j) > key ? 1 : 0;
         if (lane >= p.batch) rank = lane;

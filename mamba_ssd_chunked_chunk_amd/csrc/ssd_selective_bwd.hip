@@ -63,7 +63,10 @@ union Shared {
         float y[NW][kGradTile][64];    // a wavefront's shares of C.h
         float2 uq[NW][kGradTile][64];  // and of U.B and q.A
     };
-    float2 adjoint[kTile][64];  // time step and e
+    struct {
+        float2 step[kTile][64];  // time step and e
+        f32x4 adjC[kTile][NW];
+    };
 };
 
 // What a segment between the first and the last passes on to those ahead of it,
@@ -80,9 +83,15 @@ __device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, co
     if (mine)
 #pragma unroll
         for (int i = 0; i < 4; ++i) A[i] = p.A[at + i] * kLog2e;
-    const uint16_t *Cp = p.C + (int64_t)q.begin * p.cs + w.g * p.N + n0;
+    const int half = p.N / 2, wt = threadIdx.x / half, we = threadIdx.x % half * 2;  // two elements of C, by a thread
     for (int t = t0 + p.seg - kTile; t >= t0; t -= kTile) {  // (a whole number of tiles)
         __syncthreads();
+        if (wt < kTile) {
+            const uint32_t v =
+                *reinterpret_cast<const uint32_t *>(p.C + (int64_t)(q.begin + t + wt) * p.cs + w.g * p.N + we);
+            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(&lds.adjC[wt][0]) + we) =
+                make_float2(bf16x2_lo(v), bf16x2_hi(v));
+        }
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int i = threadIdx.x + k * NT, r = i / 16, c = (i % 16) * 4;
@@ -98,17 +107,17 @@ __device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, co
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                lds.adjoint[r][c + j] = make_float2(
+                lds.step[r][c + j] = make_float2(
                     time_step(p, d[j] + (p.bias != nullptr ? p.bias[w.ch0 + c + j] : 0.f)), e[j]);
         }
         __syncthreads();
         if (n0 >= p.N) continue;
-#pragma unroll 4
-        for (int i = kTile - 1; i >= 0; --i) {
-            const float2 e = lds.adjoint[i][lane];
-            const Quad C = quad_at(Cp + (int64_t)(t + i) * p.cs);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = __builtin_fmaf(C.v[j], e.y, u[j]) * fast_exp2(e.x * A[j]);
+        for (int i = kTile - 1; i >= 0; --i) {
+            const float2 e = lds.step[i][lane];
+            const f32x4 C = lds.adjC[i][wave];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = __builtin_fmaf(C[j], e.y, u[j]) * fast_exp2(e.x * A[j]);
         }
     }
     if (mine)

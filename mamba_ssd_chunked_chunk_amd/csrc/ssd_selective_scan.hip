@@ -4,10 +4,13 @@
 // products and two fused adds, and this, not memory, is what bounds it.
 //
 // A workgroup takes 64 channels of a sequence (or of one of its segments) and a
-// wavefront 4 states of them, a channel a lane: B and C are then the same for
-// all lanes and come through scalar registers, and what belongs to a token and
+// wavefront 4 states of them, a channel a lane.  What belongs to a token and
 // channel alone (softplus, gate, input and output) is done once, by all threads
-// together, for a tile of 16 tokens at a time, and handed over through LDS.
+// together, for a tile of 16 tokens at a time, and handed over through LDS, as
+// are B and C, which all lanes of a wavefront read alike.  (Scalar loads, which
+// return in any order, would have to be waited for all at once: 8 x 2048 tokens
+// of 4096 channels 441 us in place of 302, though a scalar operand costs the
+// adds less.)
 //
 // Sequences longer than a share of the card are cut into segments, in two
 // launches: the first walks whole sequences and first segments, which leave
@@ -26,8 +29,6 @@ namespace ssd {
 namespace layer {
 namespace {
 
-constexpr int kGroup = 4;  // tokens whose B, C and steps are on their way while as many are worked on
-
 // kOutputs: the scan itself.  kMarks: the state ahead of every kGradTile tokens,
 // for the backward pass.  kStates: the state a segment leaves from zero.
 enum Walk { kOutputs, kMarks, kStates };
@@ -35,10 +36,8 @@ enum Walk { kOutputs, kMarks, kStates };
 template <int NW>
 struct Shared {
     float2 step[kTile][64];  // time step, and times x
-    union {
-        float y[NW][kTile][64];  // a wavefront's share of C.h
-        f32x4 B[kTile][NW];      // (walks without outputs)
-    };
+    f32x4 B[kTile][NW], C[kTile][NW];
+    float y[NW][kTile][64];  // a wavefront's share of C.h
 };
 
 // One segment of a sequence (or all of it) and 64 channels.
@@ -90,7 +89,6 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
     Scalar<const uint16_t> xp(p.x + row0 * p.xs + w.ch0), dp(p.dt + row0 * p.dts + w.ch0);
     Scalar<const uint16_t> zp(gate ? p.z + row0 * p.zs + w.ch0 : p.x);
     Scalar<uint16_t> yp(OUT ? p.y + row0 * p.D + w.ch0 : nullptr);
-    const uint16_t *Bp = p.B + row0 * p.bs + w.g * p.N + n0, *Cp = p.C + row0 * p.cs + w.g * p.N + n0;
     const uint32_t xs = (uint32_t)p.xs * 2, ds = (uint32_t)p.dts * 2, zs = (uint32_t)p.zs * 2, ys = (uint32_t)p.D * 2;
     uint32_t xo[kItems], od[kItems], zo[kItems];
     auto offsets = [&](int n) {  // of a tile of n tokens
@@ -102,11 +100,24 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
             zo[k] = r * zs + cc;
         }
     };
-    // Walks without outputs take B through LDS, two elements of a token by each of the first threads: few wavefronts a
-    // unit do not hide what scalar loads wait for (8 x 2048 tokens of 4096 channels 350 -> 245 us).
-    const int bt = threadIdx.x / (p.N / 2), bj = threadIdx.x % (p.N / 2) * 2;
-    const uint16_t *wp = OUT ? nullptr : p.B + (row0 + bt) * p.bs + w.g * p.N + bj;
-    uint32_t nb = 0;
+    // two elements of B or of C of a token, by a thread (twice where there are outputs)
+    constexpr int kWords = OUT ? 2 : 1;
+    const int half = p.N / 2, each = OUT ? p.N : half;
+    uint32_t nw[kWords] = {};
+    const uint16_t *wp[kWords];
+    float *wl[kWords];
+    int64_t ws[kWords];
+    int wt[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+        const int i = threadIdx.x + k * NT, t = i / each, j = i % each;
+        const bool ofC = OUT && j >= half;
+        const int e = (ofC ? j - half : j) * 2;
+        wt[k] = t < kTile ? t : INT32_MAX;
+        ws[k] = ofC ? p.cs : p.bs;
+        wp[k] = (ofC ? p.C : p.B) + (row0 + t) * ws[k] + w.g * p.N + e;
+        wl[k] = t < kTile ? reinterpret_cast<float *>(ofC ? &lds.C[t][0] : &lds.B[t][0]) + e : nullptr;
+    }
     u32x2 nx[kItems], nd[kItems], nz[kItems];
     auto fetch = [&](int t) {
         if (t + kTile > t1) offsets(t1 - t);
@@ -120,8 +131,11 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
             nz[k] = u32x2{0, 0};
             if (gate) nz[k] = zp.at<u32x2>(zo[k]);
         }
-        if (!OUT && bt < kTile && t + bt < t1) nb = *reinterpret_cast<const uint32_t *>(wp);
-        if (!OUT) wp += kTile * p.bs;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if (wt[k] < t1 - t) nw[k] = *reinterpret_cast<const uint32_t *>(wp[k]);
+            wp[k] += kTile * ws[k];
+        }
         xp.ptr += kTile * p.xs;
         dp.ptr += kTile * p.dts;
         if (gate) zp.ptr += kTile * p.zs;
@@ -151,75 +165,47 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
                 lds.step[r][c + e] = make_float2(step, step * x[e]);
             }
         }
-        if (!OUT && bt < kTile)
-            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(&lds.B[bt][0]) + bj) =
-                make_float2(bf16x2_lo(nb), bf16x2_hi(nb));
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+            if (wl[k] != nullptr) *reinterpret_cast<float2 *>(wl[k]) = make_float2(bf16x2_lo(nw[k]), bf16x2_hi(nw[k]));
         if (t + kTile < t1) fetch(t + kTile);
         __syncthreads();
         if (n0 < p.N) {
             const int n = min(kTile, t1 - t);
-            auto token = [&](int i, const float2 &e, const Quad &B, const Quad &C) {
+            struct Token {
+                float2 e;
+                f32x4 B, C;
+            };
+            auto read = [&](int i) {
+                return Token{lds.step[i][lane], lds.B[i][wave], OUT ? lds.C[i][wave] : f32x4{0.f, 0.f, 0.f, 0.f}};
+            };
+            auto token = [&](int i, const Token &m) {
                 if (WALK == kMarks && i % kGradTile == 0 && mine)
                     *reinterpret_cast<f32x4 *>(mark_at(p, q, t + i, n0, ch)) = f32x4{h[0], h[1], h[2], h[3]};
                 float y = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    h[j] = __builtin_fmaf(e.y, B.v[j], fast_exp2(e.x * A[j]) * h[j]);
-                    if (OUT) y = j == 0 ? C.v[j] * h[j] : __builtin_fmaf(C.v[j], h[j], y);
+                    h[j] = __builtin_fmaf(m.e.y, m.B[j], fast_exp2(m.e.x * A[j]) * h[j]);
+                    if (OUT) y = j == 0 ? m.C[j] * h[j] : __builtin_fmaf(m.C[j], h[j], y);
                 }
-                if (STATES) steps += e.x;
+                if (STATES) steps += m.e.x;
                 if (OUT) lds.y[wave][i][lane] = y;
             };
             if (n == kTile) {
-                Words next[kGroup], now[kGroup];
-                float2 en[kGroup], ee[kGroup];
-                f32x4 bn[kGroup], bb[kGroup];
-                auto ahead = [&](int g) {
+                // a token is read while the one ahead of it is worked on (the compiler would not move it past the
+                // stores between)
+                Token next = read(0);
 #pragma unroll
-                    for (int i = 0; i < kGroup; ++i) {
-                        if constexpr (OUT) {
-                            words_at(Bp, next[i].b);
-                            Bp += p.bs;
-                            words_at(Cp, next[i].c);
-                            Cp += p.cs;
-                        } else {
-                            bn[i] = lds.B[g + i][wave];
-                        }
-                        en[i] = lds.step[g + i][lane];
-                    }
-                };
-                ahead(0);
-#pragma unroll
-                for (int g = 0; g < kTile; g += kGroup) {
-#pragma unroll
-                    for (int i = 0; i < kGroup; ++i) {
-                        if constexpr (OUT)
-                            now[i] = next[i];
-                        else
-                            bb[i] = bn[i];
-                        ee[i] = en[i];
-                    }
-                    if (g + kGroup < kTile) ahead(g + kGroup);
+                for (int i = 0; i < kTile; ++i) {
+                    const Token m = next;
+                    if (i + 1 < kTile) next = read(i + 1);
                     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int i = 0; i < kGroup; ++i) {
-                        if constexpr (OUT)
-                            token(g + i, ee[i], quad_of(now[i].b[0], now[i].b[1]), quad_of(now[i].c[0], now[i].c[1]));
-                        else
-                            token(g + i, ee[i], Quad{{bb[i][0], bb[i][1], bb[i][2], bb[i][3]}}, Quad{});
-                    }
+                    token(i, m);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
 #pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    if constexpr (OUT) {
-                        token(i, lds.step[i][lane], quad_at(Bp + (int64_t)i * p.bs), quad_at(Cp + (int64_t)i * p.cs));
-                    } else {
-                        const f32x4 B = lds.B[i][wave];
-                        token(i, lds.step[i][lane], Quad{{B[0], B[1], B[2], B[3]}}, Quad{});
-                    }
-                }
+                for (int i = 0; i < n; ++i) token(i, read(i));
             }
         }
         __syncthreads();
@@ -304,24 +290,26 @@ hipError_t launch_walk(const ScanParams &p, hipStream_t s) {
 }
 }  // namespace
 
+// (total_len stays below 2^30)
+constexpr int64_t kSegLimit = 1 << 29;
 void scan_shape(ScanParams &p, bool backward) {
     p.Dg = p.D / p.G;
     p.blocks = p.G * ((p.Dg + 63) / 64);
-    // Segments: long enough that a workgroup's chaining of those ahead of it stays below its walk (the root of T: one
-    // sequence of 4096 tokens and 2048 channels 178, 88, 83, 104 us with 32, 64, 128, 256 tokens), and that there are
-    // no more of them than balance the card: 16 workgroups of 4 wavefronts a unit (65536 tokens 849, 872, 1026 us with
-    // 512, 768, 2048), in the backward pass, which would repeat more work, the two wavefronts a SIMD that are resident
-    // (8 x 2048 tokens, 4096 channels 1.25 ms uncut, 1.58 in segments of 512).  Where the sequences alone fill
-    // the card only those that stand out are cut (32 ragged prompts 936, 860, 890 us at 686, 1024, 1376 tokens; 40 of
-    // 300 tokens 160 us in segments of 112, 110 uncut).
-    const int64_t waves = (int64_t)p.blocks * waves_of(p.N);
-    int64_t seg = std::max<int64_t>(backward ? 32 : 64, (int64_t)sqrt((double)p.T));
-    seg = std::max(seg, (int64_t)p.T * waves / (backward ? 2048 : 16384));
-    if (p.batch * waves >= (backward ? 2048 : 4096))
-        seg = std::max<int64_t>(seg, (int64_t)(p.T / p.batch) * (backward ? 4 : 3) / 4);
+    // Segments: long enough that a workgroup's chaining of those ahead of it stays below its walk (one sequence of 4096
+    // tokens and 2048 channels 88, 75, 80 us with 64, 128, 256 tokens), and that there are no more of them than
+    // balance the card: 8 wavefronts a SIMD (65536 tokens of 4096 channels 820, 787, 848 us with 512, 1024, 2048), in
+    // the backward pass, which would repeat more work, 2 (one of 4096 tokens 282, 261, 280, 426 us with 64, 128, 256,
+    // 512).  Where the sequences alone fill the card only those that stand out are cut (8 x 2048 tokens 300 us uncut,
+    // 372 in segments of 512, their backward pass 1084 and 1445; 32 ragged prompts of 1372 tokens on average 891, 791,
+    // 795, 875 us with 512, 1024, 2048, 4096).
+    const int64_t waves = (int64_t)p.blocks * waves_of(p.N), resident = 2048;
+    int64_t seg = std::max<int64_t>(backward ? 32 : 64, (int64_t)((backward ? 1.0 : 1.5) * sqrt((double)p.T)));
+    seg = std::max(seg, (int64_t)p.T * waves / (backward ? resident : 4 * resident));
+    if (p.batch * waves >= resident) seg = std::max<int64_t>(seg, p.T / p.batch);
     seg = (seg + kTile - 1) / kTile * kTile;
+    if (seg > kSegLimit) seg = kSegLimit;
     p.seg = (int)seg;
-    p.cut = (int)std::min<int64_t>(2 * seg, INT32_MAX);
+    p.cut = 2 * p.seg;
     p.places = p.T / seg + p.batch;
     p.cuts = std::min<int64_t>(p.T / ((int64_t)p.cut + 1), p.batch);
     p.cut_places = p.cuts > 0 ? p.T / seg + p.cuts : 0;
