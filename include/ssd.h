@@ -563,7 +563,7 @@ ssd_status ssd_rms_norm_bwd(const ssd_norm_problem *prob, void *dx, void *d_resi
  * entries as for linear attention.  Sums are fp32.                         */
 #define SSD_CONV_MAX_WIDTH 4
 typedef struct ssd_conv_problem {
-    int64_t total_len;  /* rows of x and y; >= 0, fits int32                  */
+    int64_t total_len;  /* rows of x and y; 0 .. 2^30 - 1                     */
     int32_t batch;      /* number of sequences; >= 1                          */
     int32_t channels;   /* multiple of 8                                      */
     int32_t width;      /* taps: 2 .. SSD_CONV_MAX_WIDTH                      */
@@ -624,7 +624,7 @@ ssd_status ssd_causal_conv_step_inplace(
  * fp32 over a whole sequence.  Results are deterministic (bitwise run to run). */
 #define SSD_SELECTIVE_MAX_DSTATE 64
 typedef struct ssd_selective_problem {
-    int64_t total_len;   /* rows of x, dt, z, B, C, y; >= 0, fits int32        */
+    int64_t total_len;   /* rows of x, dt, z, B, C, y; 0 .. 2^30 - 1           */
     int32_t batch;       /* number of sequences; >= 1                         */
     int32_t channels;    /* multiple of 8 ngroups                             */
     int32_t ngroups;     /* G                                                 */

@@ -16,7 +16,8 @@ using ssd::layer::NormParams;
 using ssd::layer::ScanParams;
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxRow = 1 << 22;  // elements from one row to the next
+constexpr int64_t kMaxRow = 1 << 22;        // elements from one row to the next
+constexpr int64_t kMaxTokens = (1 << 30) - 1;  // so that a token's number and a tile or a segment fit 32 bits
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void *ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 template <typename... P>
@@ -51,7 +52,7 @@ ssd_status check(const ssd_conv_problem *p) {
         !stride_ok(p->x_stride, p->channels, 8))
         return SSD_ERR_BAD_SHAPE;
     if (p->width < 2 || p->width > SSD_CONV_MAX_WIDTH || p->channels % 8 != 0) return SSD_ERR_UNSUPPORTED;
-    if (std::max<int64_t>(p->x_stride, p->channels) > kMaxRow) return SSD_ERR_UNSUPPORTED;
+    if (p->total_len > kMaxTokens || std::max<int64_t>(p->x_stride, p->channels) > kMaxRow) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 ConvParams common(const ssd_conv_problem *p) {
@@ -111,6 +112,7 @@ ssd_status check(const ssd_selective_problem *p) {
     if (p->dstate > SSD_SELECTIVE_MAX_DSTATE || p->dstate % 4 != 0 || p->channels / p->ngroups % 8 != 0)
         return SSD_ERR_UNSUPPORTED;
     if (p->state_dtype != SSD_STATE_F32 && p->state_dtype != SSD_STATE_BF16) return SSD_ERR_UNSUPPORTED;
+    if (p->total_len > kMaxTokens) return SSD_ERR_UNSUPPORTED;
     const int64_t rows[] = {p->x_stride, p->dt_stride, p->z_stride, p->b_stride, p->c_stride, p->channels, bc};
     for (const int64_t r : rows)
         if (r > kMaxRow) return SSD_ERR_UNSUPPORTED;

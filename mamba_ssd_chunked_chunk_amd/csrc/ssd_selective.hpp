@@ -100,7 +100,7 @@ __device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &
         w.nseg = __builtin_amdgcn_readlane(n, b);
         w.s = place - (__builtin_amdgcn_readlane(mine, at) - w.nseg);
         w.number = __builtin_amdgcn_readlane(all, at) - w.nseg + w.s;
-        return true;
+        return w.number < p.places;  // (more there are where a wrong table lets sequences overlap)
     }
     if (!CUT) {
         const bool found = find_piece(p.qsl, p.batch, p.T, p.seg, place, w.q, w.s);

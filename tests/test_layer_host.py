@@ -67,7 +67,7 @@ BAD = [(norm, dict(rows=-1), SHAPE), (norm, dict(width=0), SHAPE), (norm, dict(w
        (conv, dict(channels=0), SHAPE), (conv, dict(max_slots=0), SHAPE), (conv, dict(channels=12), UNSUPPORTED),
        (conv, dict(width=1), UNSUPPORTED), (conv, dict(width=5), UNSUPPORTED), (conv, dict(x_stride=504), SHAPE),
        (conv, dict(x_stride=516), SHAPE), (conv, dict(x_stride=-512), SHAPE),
-       (conv, dict(channels=1 << 23), UNSUPPORTED),
+       (conv, dict(channels=1 << 23), UNSUPPORTED), (conv, dict(total_len=1 << 30), UNSUPPORTED),
        (scan, dict(total_len=-1), SHAPE), (scan, dict(total_len=1 << 31), SHAPE), (scan, dict(batch=0), SHAPE),
        (scan, dict(channels=0), SHAPE), (scan, dict(ngroups=0), SHAPE), (scan, dict(ngroups=3), SHAPE),
        (scan, dict(dstate=0), SHAPE), (scan, dict(max_slots=0), SHAPE), (scan, dict(dstate=6), UNSUPPORTED),
@@ -75,7 +75,8 @@ BAD = [(norm, dict(rows=-1), SHAPE), (norm, dict(width=0), SHAPE), (norm, dict(w
        (scan, dict(state_dtype=2), UNSUPPORTED), (scan, dict(x_stride=504), SHAPE), (scan, dict(dt_stride=516), SHAPE),
        (scan, dict(z_stride=-1024), SHAPE), (scan, dict(b_stride=31), SHAPE), (scan, dict(c_stride=33), SHAPE),
        (scan, dict(b_stride=1 << 23), UNSUPPORTED), (scan, dict(channels=1 << 23), UNSUPPORTED),
-       (scan, dict(total_len=(1 << 31) - 1, batch=1 << 30), UNSUPPORTED)]
+       (scan, dict(total_len=(1 << 31) - 1, batch=1 << 30), UNSUPPORTED),
+       (scan, dict(total_len=1 << 30), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kind,kw,status", BAD)

@@ -389,6 +389,21 @@ def test_backward_many_sequences():
     check_backward(lens, 8, 1, 4, 1400, tail=3)
 
 
+def test_backward_of_wrong_tables_stays_inside():
+    """... and sequences that a wrong table lets overlap have no more workspace than there is."""
+    for table in ([0, 600, 0, 600, 0, 600], [600, 0, 600, 0, 600, 0], [-7, 1000000, 3, 400, 20, 599]):
+        d = L.scan_inputs([120] * 5, 64, 1, 16, 1406)
+        c = cuda(d)
+        c["query_start_loc"] = torch.tensor(table, dtype=torch.int32, device="cuda")
+        bytes_ = binding.ssd_selective_scan_workspace_size(
+            binding.ssd_selective_problem(total_len=600, batch=5, channels=64, ngroups=1, dstate=16, max_slots=5,
+                                          dt_softplus=1, state_dtype=binding.STATE_F32), backward=True)
+        guard = torch.full((bytes_ + 4096,), 7, dtype=torch.uint8, device="cuda")
+        gradients(c, None, None, workspace=guard[:bytes_])
+        torch.cuda.synchronize()
+        assert bool((guard[bytes_:] == 7).all())
+
+
 def test_backward_of_padding_that_is_not_finite():
     """Rows behind the last sequence are not read: NaN there stays out of the sums over tokens."""
     lens = [13, 30]
