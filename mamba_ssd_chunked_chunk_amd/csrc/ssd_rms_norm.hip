@@ -220,10 +220,29 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
             }
         }
     }
+    // the teams of a block are one part, added by the first (5001 rows of 512: 24.6 -> 14.5 us with the sums behind)
+    constexpr int kOthers = Team<TPR>::kRows - 1;
+    if constexpr (kOthers > 0) {
+        __shared__ float others[kOthers][VPT * 8][TPR];
+        const int i = threadIdx.x / TPR - 1;
+        if (i >= 0)
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) others[i][v * 8 + e][t] = dw[v][e];
+        __syncthreads();
+        if (i >= 0) return;
+#pragma unroll
+        for (int k = 0; k < kOthers; ++k)
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dw[v][e] += others[k][v * 8 + e][t];
+    }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int c = (t + v * TPR) * 8;
-        if (c < p.width) store_state8<false>(p.part, (int64_t)team * p.width + c, dw[v]);
+        if (c < p.width) store_state8<false>(p.part, (int64_t)blockIdx.x * p.width + c, dw[v]);
     }
 }
 
@@ -239,7 +258,7 @@ hipError_t norm_as(const NormParams &p, hipStream_t s) {
 }
 template <int TPR, int VPT>
 hipError_t norm_grad_as(const NormGradParams &p, hipStream_t s) {
-    rms_norm_grad<TPR, VPT><<<dim3((unsigned)(p.parts / Team<TPR>::kRows)), Team<TPR>::kThreads, 0, s>>>(p);
+    rms_norm_grad<TPR, VPT><<<dim3((unsigned)p.parts), Team<TPR>::kThreads, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -264,7 +283,7 @@ hipError_t launch_norm(const NormParams &p, hipStream_t s) {
 int norm_grad_parts(int64_t rows, int width) {
     const int per_block = width <= 1024 ? 4 : 1;
     const int64_t blocks = (rows + per_block - 1) / per_block;
-    return (int)(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024) * per_block;
+    return (int)(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024);
 }
 
 hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s) {
