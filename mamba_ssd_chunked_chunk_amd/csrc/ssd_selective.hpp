@@ -155,19 +155,19 @@ __device__ __forceinline__ float *mark_at(const ScanParams &p, const Seq &q, int
 }
 
 // wavefronts that hold N states, 4 each
-inline int waves_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 12 ? 3 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+inline int waves_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 template <typename F>
 void by_waves(int n, F f) {
     switch (n) {
     case 1: return f(std::integral_constant<int, 1>{});
     case 2: return f(std::integral_constant<int, 2>{});
-    case 3: return f(std::integral_constant<int, 3>{});
     case 4: return f(std::integral_constant<int, 4>{});
     case 8: return f(std::integral_constant<int, 8>{});
     default: return f(std::integral_constant<int, 16>{});
     }
 }
 
+int grad_waves_of(int N);  // and in the backward pass
 hipError_t launch_scan_marks(const ScanParams &p, hipStream_t s);
 
 }  // namespace layer

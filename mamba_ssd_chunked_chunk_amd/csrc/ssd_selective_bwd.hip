@@ -5,12 +5,20 @@
 // first leaves the state ahead of each tile of 8 tokens, and the backward walk
 // goes from tile to tile, makes its 8 states again (and keeps them and their
 // decays in registers) and then turns round.  As in the forward pass a
-// workgroup takes 64 channels, a wavefront 4 states of them, a channel a lane;
-// sums over states go through LDS.  Sums over channels (dB and dC) are formed
-// by exchanging halves: 64 values a lane, of 8 tokens, 4 states and the two
-// gradients, become one a lane in 6 steps, each of which adds what two lanes
-// hold of half the values.  They leave as fp32 for each 64 channels, and a last
-// kernel adds the blocks of a group, in their order.
+// workgroup takes 64 channels and a wavefront 4 states of them (or two groups of
+// 4 in turn), a channel a lane; sums over states go through LDS.  Sums over
+// channels (dB and dC) are formed by exchanging halves: 64 values a lane, of 8
+// tokens, 4 states and the two gradients, become one a lane in 6 steps, each of
+// which adds what two lanes hold of half the values.  They leave as fp32 for each
+// 64 channels, and a last kernel adds the blocks of a group, in their order.
+//
+// 8 x 2048 tokens of 4096 channels and 16 states: states 230 us (of which the
+// 537 MB that they write 103), gradients 815, sums 33.  The vector units are busy
+// 89% of the gradients' time: a token and state costs its decay (an exponential
+// and a product), 4 products and 5 fused adds and 3.5 exchanges of 64 lanes.
+// Tiles of 16 tokens would halve the states (213 us) but hold 64 more registers
+// a lane, and spill (gradients 944 us); three wavefronts a SIMD in 168 registers
+// leave the last workgroups alone on their units (989 us).
 #include "ssd_selective.hpp"
 
 namespace ssd {
@@ -54,35 +62,38 @@ __device__ __forceinline__ f32x4 final_grad(const ScanParams &p, int64_t at) {
     return p.state_bf16 ? load_state4<true>(p.d_final, at) : load_state4<false>(p.d_final, at);
 }
 
-template <int NW>
+// G: groups of 4 states that a wavefront takes one after the other
+template <int NW, int G>
 union Shared {
     struct {
         float2 sx[kGradTile][64];      // time step, and times x
-        f32x4 B[kGradTile][NW], C[kGradTile][NW];
+        f32x4 B[kGradTile][NW * G], C[kGradTile][NW * G];
         float e[kGradTile][64];
         float y[NW][kGradTile][64];    // a wavefront's shares of C.h
         float2 uq[NW][kGradTile][64];  // and of U.B and q.A
     };
     struct {
         float2 step[kTile][64];  // time step and e
-        f32x4 adjC[kTile][NW];
+        f32x4 adjC[kTile][NW * G];
     };
 };
 
 // What a segment between the first and the last passes on to those ahead of it,
 // from zero: U_t = (U_{t+1} + C_t e_t) a_t down to its first token.
-template <int NW>
-__device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, const Seq &q, int s, const Span &w) {
+template <int NW, int G>
+__device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW, G> &lds, const Seq &q, int s, const Span &w) {
     constexpr int NT = NW * 64, kItems = (kTile * 16 + NT - 1) / NT;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
-    const int t0 = s * p.seg, n0 = wave * 4;
-    const bool mine = lane < w.nch && n0 < p.N;
+    const int t0 = s * p.seg;
     const int ch = w.ch0 + (lane < w.nch ? lane : 0);
-    const int64_t at = (int64_t)ch * p.N + n0;
-    float A[4] = {}, u[4] = {};
-    if (mine)
+    float A[G][4] = {}, u[G][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) A[i] = p.A[at + i] * kLog2e;
+    for (int g = 0; g < G; ++g) {
+        const int n0 = (g * NW + wave) * 4;
+        if (lane < w.nch && n0 < p.N)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) A[g][i] = p.A[(int64_t)ch * p.N + n0 + i] * kLog2e;
+    }
     const int half = p.N / 2, wt = threadIdx.x / half, we = threadIdx.x % half * 2;  // two elements of C, by a thread
     for (int t = t0 + p.seg - kTile; t >= t0; t -= kTile) {  // (a whole number of tiles)
         __syncthreads();
@@ -111,48 +122,59 @@ __device__ __forceinline__ void adjoint(const ScanParams &p, Shared<NW> &lds, co
                     time_step(p, d[j] + (p.bias != nullptr ? p.bias[w.ch0 + c + j] : 0.f)), e[j]);
         }
         __syncthreads();
-        if (n0 >= p.N) continue;
 #pragma unroll
-        for (int i = kTile - 1; i >= 0; --i) {
-            const float2 e = lds.step[i][lane];
-            const f32x4 C = lds.adjC[i][wave];
+        for (int g = 0; g < G; ++g) {
+            if ((g * NW + wave) * 4 >= p.N) continue;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = __builtin_fmaf(C[j], e.y, u[j]) * fast_exp2(e.x * A[j]);
+            for (int i = kTile - 1; i >= 0; --i) {
+                const float2 e = lds.step[i][lane];
+                const f32x4 C = lds.adjC[i][g * NW + wave];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[g][j] = __builtin_fmaf(C[j], e.y, u[g][j]) * fast_exp2(e.x * A[g][j]);
+            }
         }
     }
-    if (mine)
-        *reinterpret_cast<f32x4 *>(p.adj + (cut_place(p, q) + s) * p.D * p.N + at) = f32x4{u[0], u[1], u[2], u[3]};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int n0 = (g * NW + wave) * 4;
+        if (lane < w.nch && n0 < p.N)
+            *reinterpret_cast<f32x4 *>(p.adj + ((cut_place(p, q) + s) * p.D + ch) * p.N + n0) =
+                f32x4{u[g][0], u[g][1], u[g][2], u[g][3]};
+    }
 }
 
 // One segment of a sequence (or all of it) and 64 channels.
-template <int NW>
-__device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const Piece &piece, int block) {
+template <int NW, int G>
+__device__ __forceinline__ void grad(const ScanParams &p, Shared<NW, G> &lds, const Piece &piece, int block) {
     const Seq &q = piece.q;
     const int s = piece.s, nseg = piece.nseg;
     constexpr int NT = NW * 64, K = kGradTile, kItems = (K * 32 + NT - 1) / NT, kStep = NT / 32;
     constexpr int kTeams = NT < 256 ? kStep : 8;  // threads that finish the same channels
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
     const Span w = span_of(p, block);
-    const int n0 = wave * 4;
-    const bool mine = lane < w.nch && n0 < p.N;
     const int ch = w.ch0 + (lane < w.nch ? lane : 0);
-    const int64_t at = (int64_t)ch * p.N + n0;
+    const int64_t at = (int64_t)ch * p.N;
     const int t0 = s * p.seg, t1 = nseg > 1 ? min(q.len, t0 + p.seg) : q.len;
     const int64_t state = (int64_t)q.b * p.D * p.N + at;
 
-    float A[4] = {}, u[4] = {}, dA[4] = {};  // u: the gradient of the state behind the walk
-    if (mine) {
+    bool mine[G];
+    float A[G][4] = {}, u[G][4] = {}, dA[G][4] = {};  // u: the gradient of the state behind the walk
 #pragma unroll
-        for (int i = 0; i < 4; ++i) A[i] = p.A[at + i] * kLog2e;
+    for (int g = 0; g < G; ++g) {
+        const int n0 = (g * NW + wave) * 4;
+        mine[g] = lane < w.nch && n0 < p.N;
+        if (!mine[g]) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A[g][i] = p.A[at + n0 + i] * kLog2e;
         if (s == nseg - 1) {
-            const f32x4 v = final_grad(p, state);
+            const f32x4 v = final_grad(p, state + n0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = v[i];
+            for (int i = 0; i < 4; ++i) u[g][i] = v[i];
         } else {
-            chain_back(p, cut_place(p, q), s, nseg, at, ch, A, u);
+            chain_back(p, cut_place(p, q), s, nseg, at + n0, ch, A[g], u[g]);
         }
     }
-    if (n0 >= p.N) {  // no states, no share
+    if (wave * 4 >= p.N) {  // no states, no share
         for (int i = 0; i < K; ++i) {
             lds.y[wave][i][lane] = 0.f;
             lds.uq[wave][i][lane] = make_float2(0.f, 0.f);
@@ -186,14 +208,14 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
     float *Wl = reinterpret_cast<float *>(ofC ? &lds.C[bt < K ? bt : 0][0] : &lds.B[bt < K ? bt : 0][0]) +
                 (ofC ? bj - p.N : bj);
     uint32_t nw = 0;
-    const float *mp = p.marks + ((q.begin / K + q.b + t0 / K + (int64_t)(tiles - 1)) * (p.N / 4) + wave) * p.D * 4;
+    const float *mp = p.marks + ((q.begin / K + q.b + t0 / K + (int64_t)(tiles - 1)) * (p.N / 4) + wave) * p.D * 4;  // (of group 0)
     // value (gradient, token, state) of a lane's bits (5), (4, 3, 2), (1, 0)
-    float *bcp = p.bc + ((int64_t)block * p.T + row) * 2 * p.N + n0;
+    float *bcp = p.bc + ((int64_t)block * p.T + row) * 2 * p.N;
     const int bi = (lane >> 2) & 7;
-    const uint32_t bo = ((bi * 2 + (lane >> 5)) * p.N + (lane & 3)) * 4;
+    const uint32_t bo = ((bi * 2 + (lane >> 5)) * p.N + wave * 4 + (lane & 3)) * 4;
 
     uint32_t nx[kItems], nd[kItems], nz[kItems], ny[kItems];
-    f32x4 mark = {0.f, 0.f, 0.f, 0.f};
+    f32x4 mark[G] = {};
     auto fetch = [&](int n) {  // n: tokens of the tile
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
@@ -204,7 +226,9 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
             ny[k] = at_offset<uint32_t>(yp, yo + k * kStep * ys);
             if (gate) nz[k] = at_offset<uint32_t>(zp, zo + k * kStep * zs);
         }
-        if (mine) mark = at_offset<f32x4>(mp, (uint32_t)ch * 16);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            if (mine[g]) mark[g] = at_offset<f32x4>(mp + (int64_t)g * NW * p.D * 4, (uint32_t)ch * 16);
         nw = bt < n ? *reinterpret_cast<const uint32_t *>(Wp) : 0;
         Wp -= K * bcs;
         xp = moved(xp, -(int64_t)K * xs);
@@ -219,7 +243,9 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
 #pragma unroll
     for (int e = 0; e < 2; ++e) asm volatile("" : "+v"(bias[e]), "+v"(skip[e]));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(A[e]), "+v"(u[e]));
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(A[g][e]), "+v"(u[g][e]));
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int n = min(K, t1 - t0 - tile * K);
         if (bt < K) *reinterpret_cast<float2 *>(Wl) = make_float2(bf16x2_lo(nw), bf16x2_hi(nw));
@@ -254,19 +280,30 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
                 lds.e[r][c + i] = e[k][i];
             }
         }
-        const f32x4 h0 = mark;
+        f32x4 first[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) first[g] = mark[g];
         if (tile > 0) fetch(K);
         __syncthreads();
-        if (n0 < p.N) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if ((g * NW + wave) * 4 >= p.N) continue;
+            if (g > 0) asm volatile("" ::: "memory");  // (what both groups read is read again, not kept)
+            const f32x4 h0 = first[g];
             // a token's numbers are read while the one ahead of it is worked on (the compiler, which takes the stores
             // between for a hindrance, would read and wait)
             struct Token {
                 float2 v;
                 float e;
                 f32x4 B, C;
+                float2 share;  // of the groups ahead
             };
             auto read = [&](int i, bool back) {
-                return Token{lds.sx[i][lane], back ? lds.e[i][lane] : 0.f, lds.B[i][wave], lds.C[i][wave]};
+                const int b = g * NW + wave;
+                Token m{lds.sx[i][lane], back ? lds.e[i][lane] : 0.f, lds.B[i][b], lds.C[i][b], make_float2(0.f, 0.f)};
+                if (g > 0 && back) m.share = lds.uq[wave][i][lane];
+                if (g > 0 && !back && gate) m.share.x = lds.y[wave][i][lane];
+                return m;
             };
             float h[K][4], a[K][4];
             Token next = read(0, false);
@@ -278,11 +315,11 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
                 float y = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    a[i][j] = fast_exp2(m.v.x * A[j]);
+                    a[i][j] = fast_exp2(m.v.x * A[g][j]);
                     h[i][j] = __builtin_fmaf(a[i][j], i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j], m.v.y * m.B[j]);
                     y = j == 0 ? m.C[j] * h[i][j] : __builtin_fmaf(m.C[j], h[i][j], y);
                 }
-                if (gate) lds.y[wave][i][lane] = y;
+                if (gate) lds.y[wave][i][lane] = g > 0 ? y + m.share.x : y;
                 __builtin_amdgcn_sched_barrier(0);
             }
             float dAt[4] = {}, f[K][4];
@@ -294,13 +331,13 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
                 float uB = 0.f, qA = 0.f, forB[4], forC[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    u[j] = __builtin_fmaf(m.C[j], m.e, u[j]);
+                    u[g][j] = __builtin_fmaf(m.C[j], m.e, u[g][j]);
                     forC[j] = m.e * h[i][j];
-                    forB[j] = u[j] * m.v.y;
-                    uB = j == 0 ? u[j] * m.B[j] : __builtin_fmaf(u[j], m.B[j], uB);
-                    u[j] *= a[i][j];
-                    const float qq = u[j] * (i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j]);
-                    qA = j == 0 ? qq * A[j] : __builtin_fmaf(qq, A[j], qA);
+                    forB[j] = u[g][j] * m.v.y;
+                    uB = j == 0 ? u[g][j] * m.B[j] : __builtin_fmaf(u[g][j], m.B[j], uB);
+                    u[g][j] *= a[i][j];
+                    const float qq = u[g][j] * (i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j]);
+                    qA = j == 0 ? qq * A[g][j] : __builtin_fmaf(qq, A[g][j], qA);
                     dAt[j] = i == K - 1 ? qq * m.v.x : __builtin_fmaf(qq, m.v.x, dAt[j]);
                 }
 #pragma unroll
@@ -310,17 +347,21 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
                     if (i < 4) f[i][j] = fold16(f[i][j], f[i + 4][j]);
                     if (i < 2) f[i][j] = fold_dpp<0x128>(f[i][j], f[i + 2][j], lane & 8);  // row_ror:8
                 }
+                if (g > 0) {
+                    uB += m.share.x;
+                    qA += m.share.y;
+                }
                 lds.uq[wave][i][lane] = make_float2(uB, qA);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dA[j] += dAt[j];
+            for (int j = 0; j < 4; ++j) dA[g][j] += dAt[j];
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[0][j] = fold_dpp<0x141>(f[0][j], f[1][j], lane & 4);  // row_half_mirror
             f[0][0] = fold_dpp<0x4E>(f[0][0], f[0][2], lane & 2);  // quad_perm [2,3,0,1]
             f[0][1] = fold_dpp<0x4E>(f[0][1], f[0][3], lane & 2);
             f[0][0] = fold_dpp<0xB1>(f[0][0], f[0][1], lane & 1);  // quad_perm [1,0,3,2]
-            if (bi < n) put_offset(bcp, bo, f[0][0]);
+            if (bi < n) put_offset(bcp, bo + g * NW * 16, f[0][0]);
         }
         bcp -= (int64_t)K * 2 * p.N;
         __syncthreads();
@@ -358,7 +399,9 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
         // the next tile's rows are waited for here, ahead of the stores
 #pragma unroll
         for (int k = 0; k < kItems; ++k) asm volatile("" : "+v"(nx[k]), "+v"(nd[k]), "+v"(ny[k]), "+v"(nz[k]));
-        asm volatile("" : "+v"(mark), "+v"(nw));
+#pragma unroll
+        for (int g = 0; g < G; ++g) asm volatile("" : "+v"(mark[g]));
+        asm volatile("" : "+v"(nw));
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             if (r0 + k * kStep >= n || !in) continue;
@@ -372,16 +415,20 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
         if (gate) dzp = moved(dzp, -(int64_t)K * ys);
     }
     const int64_t place = piece.number;
-    if (mine) {
-        const f32x4 v = {u[0], u[1], u[2], u[3]};
-        *reinterpret_cast<f32x4 *>(p.dA_part + place * p.D * p.N + at) = f32x4{dA[0], dA[1], dA[2], dA[3]};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        if (!mine[g]) continue;
+        const int n0 = (g * NW + wave) * 4;
+        const f32x4 v = {u[g][0], u[g][1], u[g][2], u[g][3]};
+        *reinterpret_cast<f32x4 *>(p.dA_part + place * p.D * p.N + at + n0) =
+            f32x4{dA[g][0], dA[g][1], dA[g][2], dA[g][3]};
         if (s > 0) {
-            if (s == nseg - 1) *reinterpret_cast<f32x4 *>(p.adj + (cut_place(p, q) + s) * p.D * p.N + at) = v;
+            if (s == nseg - 1) *reinterpret_cast<f32x4 *>(p.adj + (cut_place(p, q) + s) * p.D * p.N + at + n0) = v;
         } else if (p.d_init != nullptr) {
             if (p.state_bf16)
-                store_state4<true>(p.d_init, state, v);
+                store_state4<true>(p.d_init, state + n0, v);
             else
-                store_state4<false>(p.d_init, state, v);
+                store_state4<false>(p.d_init, state + n0, v);
         }
     }
     // sums over tokens of what belongs to channels
@@ -404,15 +451,15 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW> &lds, const
 }
 
 // Whole sequences and last segments; what the segments between pass on.
-template <int NW>
-__global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_first(ScanParams p) {
-    __shared__ Shared<NW> lds;
+template <int NW, int G>
+__global__ __launch_bounds__(NW * 64, 2) void scan_grad_first(ScanParams p) {
+    __shared__ Shared<NW, G> lds;
     const int place = blockIdx.x / p.blocks, block = blockIdx.x % p.blocks;
     Piece w;
     if (!piece_at<false>(p, place, w)) {  // an empty place adds nothing
         const Span c = span_of(p, block);
-        const int lane = threadIdx.x & 63, n0 = threadIdx.x / 64 * 4;
-        if (lane < c.nch && n0 < p.N)
+        const int lane = threadIdx.x & 63;
+        for (int n0 = threadIdx.x / 64 * 4; lane < c.nch && n0 < p.N; n0 += NW * 4)
             *reinterpret_cast<f32x4 *>(p.dA_part + ((int64_t)place * p.D + c.ch0 + lane) * p.N + n0) =
                 f32x4{0.f, 0.f, 0.f, 0.f};
         float *dD = p.dD_part + (int64_t)place * 2 * p.D + c.ch0;
@@ -420,15 +467,15 @@ __global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_first(Scan
         return;
     }
     if (w.s == w.nseg - 1)
-        grad<NW>(p, lds, w, block);
+        grad<NW, G>(p, lds, w, block);
     else if (w.s > 0)
-        adjoint<NW>(p, lds, w.q, w.s, span_of(p, block));
+        adjoint<NW, G>(p, lds, w.q, w.s, span_of(p, block));
 }
-template <int NW>
-__global__ __launch_bounds__(NW * 64, NW == 4 ? 2 : 1) void scan_grad_rest(ScanParams p) {
-    __shared__ Shared<NW> lds;
+template <int NW, int G>
+__global__ __launch_bounds__(NW * 64, 2) void scan_grad_rest(ScanParams p) {
+    __shared__ Shared<NW, G> lds;
     Piece w;
-    if (piece_at<true>(p, blockIdx.x / p.blocks, w) && w.s < w.nseg - 1) grad<NW>(p, lds, w, blockIdx.x % p.blocks);
+    if (piece_at<true>(p, blockIdx.x / p.blocks, w) && w.s < w.nseg - 1) grad<NW, G>(p, lds, w, blockIdx.x % p.blocks);
 }
 
 // The sums over blocks and places: dB and dC, the blocks of a group added in
@@ -453,16 +500,44 @@ __global__ __launch_bounds__(kSumThreads) void scan_sums(ScanParams p, int64_t b
     *reinterpret_cast<u32x2 *>(to) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
+// The wavefronts that hold N states, and the groups of 4 that each of them takes: one to 16 states, two above, which
+// share a tile's preparation and let two wavefronts a SIMD keep their registers (8 x 1024 tokens of 4096 channels with
+// one and two groups: 20 states 988 and 849 us, 32 states 1041 and 967; 64 states in 16 wavefronts, which had to spill,
+// 3976, in 8 1866).  A third of 4 wavefronts is left idle where 3 would do (12 states 610 -> 549 us: the rows of a tile
+// come out even), not two of 4 (8 states 611 us in 2, 535 in 4, but with 16 sequences 669 and 941).
+template <typename F>
+void by_groups(int N, F f) {
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    switch ((N + 3) / 4) {
+    case 1: return f(std::integral_constant<int, 1>{}, one);
+    case 2: return f(std::integral_constant<int, 2>{}, one);
+    case 3:
+    case 4: return f(std::integral_constant<int, 4>{}, one);
+    case 5:
+    case 6:
+    case 7:
+    case 8: return f(std::integral_constant<int, 4>{}, two);
+    default: return f(std::integral_constant<int, 8>{}, two);
+    }
+}
+
 }  // namespace
+
+int grad_waves_of(int N) {
+    int waves = 0;
+    by_groups(N, [&](auto n, auto) { waves = decltype(n)::value; });
+    return waves;
+}
 
 hipError_t launch_scan_grad(const ScanParams &p, hipStream_t s) {
     hipError_t e = launch_scan_marks(p, s);
     if (e != hipSuccess) return e;
-    by_waves(waves_of(p.N), [&](auto n) {
-        constexpr int NW = decltype(n)::value;
-        scan_grad_first<NW><<<dim3((unsigned)(p.places * p.blocks)), NW * 64, 0, s>>>(p);
+    by_groups(p.N, [&](auto n, auto groups) {
+        constexpr int NW = decltype(n)::value, G = decltype(groups)::value;
+        scan_grad_first<NW, G><<<dim3((unsigned)(p.places * p.blocks)), NW * 64, 0, s>>>(p);
         if (p.cut_places > 0)
-            scan_grad_rest<NW><<<dim3((unsigned)(p.cut_places * p.blocks)), NW * 64, 0, s>>>(p);
+            scan_grad_rest<NW, G><<<dim3((unsigned)(p.cut_places * p.blocks)), NW * 64, 0, s>>>(p);
     });
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t bc_blocks = ((int64_t)p.T * p.G * (p.N / 2) + kSumThreads - 1) / kSumThreads;

@@ -297,15 +297,17 @@ void scan_shape(ScanParams &p, bool backward) {
     p.blocks = p.G * ((p.Dg + 63) / 64);
     // Segments: long enough that a workgroup's chaining of those ahead of it stays below its walk (one sequence of 4096
     // tokens and 2048 channels 88, 75, 80 us with 64, 128, 256 tokens), and that there are no more of them than
-    // balance the card: 8 wavefronts a SIMD (65536 tokens of 4096 channels 820, 787, 848 us with 512, 1024, 2048), in
-    // the backward pass, which would repeat more work, 2 (one of 4096 tokens 282, 261, 280, 426 us with 64, 128, 256,
-    // 512).  Where the sequences alone fill the card only those that stand out are cut (8 x 2048 tokens 300 us uncut,
-    // 372 in segments of 512, their backward pass 1084 and 1445; 32 ragged prompts of 1372 tokens on average 891, 791,
-    // 795, 875 us with 512, 1024, 2048, 4096).
-    const int64_t waves = (int64_t)p.blocks * waves_of(p.N), resident = 2048;
+    // balance the card: 8 wavefronts a SIMD (65536 tokens 820, 787, 848 us with 512, 1024, 2048), in the backward
+    // pass, which would repeat more work, 2 (one of 4096 tokens 282, 261, 280, 426 us with 64, 128, 256, 512).  Where
+    // the sequences alone come near 2 wavefronts a SIMD only those that stand out are cut (8 x 2048 tokens of 4096
+    // channels 300 us uncut, 372 in segments of 512, their backward pass 1084 and 1445; 32 ragged prompts of 1372 on
+    // average 891, 791, 795, 875 us with 512, 1024, 2048, 4096; with half as many wavefronts 16 x 1024 tokens of 4
+    // states 178 us uncut and 200 in segments of 256, 4 x 1024 tokens of 16 states 121 and 113 in segments of 128).
+    const int64_t waves = (int64_t)p.blocks * (backward ? grad_waves_of(p.N) : waves_of(p.N));
+    const int64_t resident = 2048;
     int64_t seg = std::max<int64_t>(backward ? 32 : 64, (int64_t)((backward ? 1.0 : 1.5) * sqrt((double)p.T)));
     seg = std::max(seg, (int64_t)p.T * waves / (backward ? resident : 4 * resident));
-    if (p.batch * waves >= resident) seg = std::max<int64_t>(seg, p.T / p.batch);
+    if (p.batch * waves >= resident * 3 / 4) seg = std::max<int64_t>(seg, p.T / p.batch);
     seg = (seg + kTile - 1) / kTile * kTile;
     if (seg > kSegLimit) seg = kSegLimit;
     p.seg = (int)seg;

@@ -258,7 +258,7 @@ def test_tokens_behind_2_31_elements():
 
 # ------------------------------------------------------------------ single tokens
 
-@pytest.mark.parametrize("N", [4, 8, 12, 16, 20, 32, 48, 64])
+@pytest.mark.parametrize("N", [4, 8, 12, 16, 20, 24, 28, 32, 36, 48, 64])
 @pytest.mark.parametrize("B", [1, 3, 16, 37])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_step(N, B, dtype):
@@ -347,7 +347,7 @@ def check_backward(lens, D, G, N, seed, dtype=F32, initial=True, final=True, tai
         assert not rows or bool((t[T:] == 7.0).all()), n
 
 
-@pytest.mark.parametrize("N", [4, 8, 12, 16, 20, 32, 48, 64])
+@pytest.mark.parametrize("N", [4, 8, 12, 16, 20, 24, 28, 32, 36, 48, 64])
 @pytest.mark.parametrize("D,G", [(8, 1), (200, 1), (144, 2)])
 def test_backward_sizes(D, G, N):
     check_backward([35, 1, 0, 50], D, G, N, 900 + D + N)
