@@ -392,18 +392,25 @@ void conv_shape(ConvParams &p, int width, bool backward) {
     p.tile = 32;
     p.places = p.T / p.tile + p.batch;
     if (!backward) return;
-    // whole groups with the W - 1 tokens behind a piece, as many pieces as are resident (two wavefronts a SIMD) or
-    // groups to 16
+    // whole groups with the W - 1 tokens behind a piece: as many pieces as are resident (two wavefronts a SIMD) where
+    // they fit with 16 groups or fewer (32 x 1024 tokens, 1536 channels: 14 groups 71 us, 8 76, 4 80), or 8 groups,
+    // which even out (40 ragged prompts of 80 on average, 10240 channels 73 us, with 16 groups 99; 64 x 512 tokens,
+    // 4096 channels 190 and 201)
     const int rows = width == 3 ? kAhead<3> : kAhead<4>;
     const int64_t cblocks = blocks_of(p.D, 64 * kGradChannels);
-    for (int groups = 2; groups <= 16; ++groups) {
+    auto pieces = [&](int groups) {
         p.tile = groups * rows - (width - 1);
         p.places = p.T / p.tile + p.batch;
-        if (p.places * cblocks <= 2048) break;
-    }
+        return p.places * cblocks;
+    };
+    int groups = 2;
+    while (groups <= 16 && pieces(groups) > 2048) ++groups;
+    if (groups > 16) pieces(8);
 }
 int64_t conv_parts(const ConvParams &p) { return blocks_of(p.places, 4); }
-int64_t conv_threads(const ConvParams &p) { return blocks_of(p.places, 4) * 4 * blocks_of(p.D, 64 * kGradChannels) * 64; }
+int64_t conv_threads(const ConvParams &p) {
+    return blocks_of(p.places, 4) * 4 * blocks_of(p.D, 64 * kGradChannels) * 64;
+}
 
 hipError_t launch_conv(const ConvParams &p, int width, hipStream_t s) {
     const dim3 grid((unsigned)blocks_of(p.places * blocks_of(p.D, 512), 4));

@@ -15,7 +15,7 @@
 // 8 x 2048 tokens of 4096 channels and 16 states: states 230 us (of which the
 // 537 MB that they write 103), gradients 815, sums 33.  The vector units are busy
 // 89% of the gradients' time: a token and state costs its decay (an exponential
-// and a product), 4 products and 5 fused adds and 3.5 exchanges of 64 lanes.
+// and a product), 5 products, 6 fused adds and two exchanges between lanes.
 // Tiles of 16 tokens would halve the states (213 us) but hold 64 more registers
 // a lane, and spill (gradients 944 us); three wavefronts a SIMD in 168 registers
 // leave the last workgroups alone on their units (989 us).
@@ -208,7 +208,8 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW, G> &lds, co
     float *Wl = reinterpret_cast<float *>(ofC ? &lds.C[bt < K ? bt : 0][0] : &lds.B[bt < K ? bt : 0][0]) +
                 (ofC ? bj - p.N : bj);
     uint32_t nw = 0;
-    const float *mp = p.marks + ((q.begin / K + q.b + t0 / K + (int64_t)(tiles - 1)) * (p.N / 4) + wave) * p.D * 4;  // (of group 0)
+    const int64_t mark0 = q.begin / K + q.b + t0 / K + (int64_t)(tiles - 1);
+    const float *mp = p.marks + (mark0 * (p.N / 4) + wave) * p.D * 4;  // (of group 0)
     // value (gradient, token, state) of a lane's bits (5), (4, 3, 2), (1, 0)
     float *bcp = p.bc + ((int64_t)block * p.T + row) * 2 * p.N;
     const int bi = (lane >> 2) & 7;
