@@ -1,6 +1,11 @@
 // Root-mean-square norm with the residual's addition, its 8-bit outputs and
-// its backward pass.  A row lies in the registers of 64, 256 or 1024 threads, 8
-// consecutive elements each, so it is read once; the sums over it are fp32.
+// its backward pass.  A row lies in the registers of 64 to 1024 threads, 8
+// consecutive elements each and up to 4 times, so it is read once; the sums over
+// it are fp32.  Memory bounds both directions: 16384 rows of 2560 with an fp32
+// residual, 806 MB, 147 us (5.5 TB/s); the backward pass of 5001 such rows in
+// bf16, 102 MB, 21 us, and 6 us for the sum over the blocks' shares.
+#include <algorithm>
+
 #include "ssd.h"
 #include "ssd_layer.hpp"
 #include "ssd_state_cache.hpp"
@@ -163,13 +168,21 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
     const int t = threadIdx.x % TPR;
     const int team = blockIdx.x * Team<TPR>::kRows + threadIdx.x / TPR;
     const int teams = gridDim.x * Team<TPR>::kRows;
+    // rows of 4 vectors a thread leave no registers for the weights, which they read again from L2 (3000 rows of 24576:
+    // 251 -> 187 us)
+    constexpr bool kKeep = VPT < 4 || TPR < 1024;
     float w[VPT][8], dw[VPT][8];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
+    auto weight = [&](int v) {
         const int c = (t + v * TPR) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[v][e] = dw[v][e] = 0.f;
+        for (int e = 0; e < 8; ++e) w[v][e] = 0.f;
         if (c < p.width) load_state8<false>(p.weight, c, w[v]);
+    };
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[v][e] = 0.f;
+        if (kKeep) weight(v);
     }
     const float share = 1.f / (float)p.width;
     // every team of a block takes as many turns (they share barriers)
@@ -190,12 +203,14 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
             }
         }
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int v = 0; v < VPT; ++v) {
+            if (!kKeep) weight(v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 sum.x = __builtin_fmaf(r[v][e], r[v][e], sum.x);
                 sum.y = __builtin_fmaf(u[v][e] * w[v][e], r[v][e], sum.y);
             }
+        }
         sum = row_sum<TPR>(sum, sums[n & 1]);
         const float s = 1.f / sqrtf(sum.x * share + p.eps);
         const float k = s * s * s * (sum.y * share);
@@ -206,6 +221,7 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
             const int64_t at = row * p.width + c;
             float d[8] = {};
             if (p.d_r != nullptr) load8(p.d_r, at, p.res_bf16, d);
+            if (!kKeep) weight(v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 dw[v][e] = __builtin_fmaf(s * r[v][e], u[v][e], dw[v][e]);
@@ -267,32 +283,35 @@ constexpr int kWide = 2048;  // above this width a row has 256 threads
 
 int64_t norm_threads(int64_t rows, int width) {
     if (rows > UINT32_MAX) return rows;
-    return rows * (width <= kWide ? 64 : width <= 16384 ? 256 : 1024) + 255;
+    return rows * (width <= kWide ? 64 : width <= 4096 ? 256 : width <= 8192 ? 512 : 1024) + 255;
 }
 
+// Rows of more than 8192 elements in 1024 threads, 2 vectors each (12000 rows of 16384: 342 us in 256 threads, 297 in
+// 512, 268 in 1024), of more than 4096 in 512 (20000 of 5120: 153 us in 256, 147 in 512, 159 in 1024).
 hipError_t launch_norm(const NormParams &p, hipStream_t s) {
     if (p.width <= 512) return norm_as<64, 1>(p, s);
     if (p.width <= 1024) return norm_as<64, 2>(p, s);
     if (p.width <= kWide) return norm_as<64, 4>(p, s);
     if (p.width <= 4096) return norm_as<256, 2>(p, s);
-    if (p.width <= 8192) return norm_as<256, 4>(p, s);
-    if (p.width <= 16384) return norm_as<256, 8>(p, s);
+    if (p.width <= 8192) return norm_as<512, 2>(p, s);
+    if (p.width <= 16384) return norm_as<1024, 2>(p, s);
     return norm_as<1024, 4>(p, s);
 }
 
 int norm_grad_parts(int64_t rows, int width) {
     const int per_block = width <= 1024 ? 4 : 1;
-    const int64_t blocks = (rows + per_block - 1) / per_block;
-    return (int)(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024);
+    const int64_t most = width <= 4096 ? 1024 : 256;  // blocks that are resident (of 1024 threads one a unit)
+    return (int)std::clamp<int64_t>((rows + per_block - 1) / per_block, 1, most);
 }
 
+// (12000 rows of 8192: 226 us in 1024 blocks of 256 threads, 166 in 256 of 1024)
 hipError_t launch_norm_grad(const NormGradParams &p, hipStream_t s) {
     hipError_t e;
     if (p.width <= 512) e = norm_grad_as<64, 1>(p, s);
     else if (p.width <= 1024) e = norm_grad_as<64, 2>(p, s);
     else if (p.width <= 2048) e = norm_grad_as<256, 1>(p, s);
     else if (p.width <= 4096) e = norm_grad_as<256, 2>(p, s);
-    else if (p.width <= 8192) e = norm_grad_as<256, 4>(p, s);
+    else if (p.width <= 8192) e = norm_grad_as<1024, 1>(p, s);
     else if (p.width <= 16384) e = norm_grad_as<1024, 2>(p, s);
     else e = norm_grad_as<1024, 4>(p, s);
     if (e != hipSuccess) return e;
