@@ -5,6 +5,12 @@
 // so a row is read once but for the few ahead of a piece.  Only the first piece of
 // a sequence, which alone reads its state, writes the one that it leaves, so the
 // pool needs no second launch.
+//
+// Memory bounds it: 43898 tokens of 10240 channels, 1.80 GB, 362 us (5.0 TB/s); the
+// backward pass of 4 x 4096 tokens of 1536 channels, 151 MB, 35 us (its arithmetic,
+// 30 operations an element with the silu's slope, takes about half of that), and 5
+// for the sum of the blocks' shares; a step of 512 sequences of 10240 channels, 84
+// MB, 16 us.
 #include "ssd_layer.hpp"
 
 namespace ssd {
