@@ -1,10 +1,12 @@
 // Selective scan over ragged batches: h = exp(dts A) h + dts x B, y = C.h + D x,
 // gated by silu(z).  Every channel and state decays on its own, so there is no
 // matrix product in it: a token costs each (channel, state) an exponential, two
-// products and two fused adds, and this, not memory, is what bounds it: the vector
-// units are busy 95% of the time.  65536 tokens of 2048 channels and 16 states, cut
-// into 64 segments (which all but doubles the work), 790 us; 8 x 2048 tokens of 4096
-// channels, uncut, 300 us.
+// products and two fused adds, and this, not memory, is what bounds it: 11 ns for
+// the 64 channels of a wavefront on one SIMD, at which 8 x 2048 tokens of 4096
+// channels and 16 states take 180 us, while all a wavefront does is 33 instructions
+// a token, 20 of them for its states.  They take 300 us (1.1 vector instructions a
+// cycle and compute unit); 65536 tokens of 2048 channels, cut into 64 segments, which
+// all but doubles the work, 790 us.
 //
 // A workgroup takes 64 channels of a sequence (or of one of its segments) and a
 // wavefront 4 states of them, a channel a lane.  What belongs to a token and
