@@ -259,6 +259,7 @@ struct ScanParams {
     uint32_t max_slots;
     // sequences of more than `cut` tokens are cut into segments of `seg`
     int seg, cut;
+    int listed;      // sequences are numbered without gaps
     int64_t places;  // of segments
     int64_t cut_places, cuts;  // of segments of cut sequences; most of those sequences
     float *parts;    // [cut_places][D][N]: the states that segments leave, from zero but the first

@@ -72,35 +72,77 @@ __device__ __forceinline__ int segments_of(const ScanParams &p, int len) {
 // The piece at a place of the grid; false where there is none.  With CUT, of the
 // places of cut sequences alone.
 //
-// Up to 64 sequences are numbered one behind the other, a sequence a lane, those of
-// the longest pieces first (32 ragged prompts 988 -> 936 us): gaps between them
-// would leave whole rows of compute units without work, as they come in step with
-// the units that the workgroups are given to (states of 8 x 2048 tokens 430 -> 350
-// us).  More of them have the places of find_piece and cut_place, with gaps.
+// Sequences are numbered one behind the other, 64 of them at a time, a sequence a
+// lane: whole ones in classes of their length, the longest first, and the segments
+// of cut ones in the middle, where their length belongs.  Gaps between them would
+// leave whole rows of compute units without work, as they come in step with the
+// units that the workgroups are given to (states of 8 x 2048 tokens 430 -> 350 us),
+// and a long one at the end all but one (backward pass of 65 ragged prompts of 186
+// tokens on average 632 -> 436 us).  Where that is not worth the search (`listed`)
+// they have the places of find_piece and cut_place, with gaps.
+constexpr int kClasses = 30;
 template <bool CUT>
 __device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &w) {
     const int lane = threadIdx.x & 63;
-    if (p.batch <= 64) {
-        const int begin = lane < p.batch ? clamp_row(p.qsl[lane], p.T) : 0;
-        const int end = lane < p.batch ? clamp_row(p.qsl[lane + 1], p.T) : 0;
-        const int len = end > begin ? end - begin : 0;
-        const int n = lane < p.batch ? segments_of(p, len) : 0;
-        // the longest pieces first
-        const int key = lane < p.batch ? (min(n > 1 ? p.seg : len, 1 << 24) << 6 | (63 - lane)) : -1;
-        int rank = 0;
-        for (int j = 0; j < p.batch; ++j) rank += __builtin_amdgcn_readlane(key, j) > key ? 1 : 0;
-        if (lane >= p.batch) rank = lane;
-        const int order = __builtin_amdgcn_ds_permute(rank * 4, lane);  // the sequence of this rank
-        const int nr = __builtin_amdgcn_ds_bpermute(order * 4, n);
-        const int all = wave_incl_scan(nr), mine = CUT ? wave_incl_scan(nr > 1 ? nr : 0) : all;
-        const uint64_t m = __ballot(mine > place);
-        if (m == 0) return false;
-        const int at = __builtin_ctzll(m), b = __builtin_amdgcn_readlane(order, at);
-        w.q = Seq{b, __builtin_amdgcn_readlane(begin, b), __builtin_amdgcn_readlane(len, b)};
-        w.nseg = __builtin_amdgcn_readlane(n, b);
-        w.s = place - (__builtin_amdgcn_readlane(mine, at) - w.nseg);
-        w.number = __builtin_amdgcn_readlane(all, at) - w.nseg + w.s;
-        return w.number < p.places;  // (more there are where a wrong table lets sequences overlap)
+    if (p.listed) {
+        struct Lane {
+            int begin, len, n, cls;  // n: pieces, 0 behind the last sequence; cls: of a whole one, else -1
+        };
+        const float per_class = (float)kClasses / ((float)p.cut + 1.f);
+        auto lane_of = [&](int j) {
+            Lane v{0, 0, 0, -1};
+            const int b = j * 64 + lane;
+            if (b >= p.batch) return v;
+            v.begin = clamp_row(p.qsl[b], p.T);
+            const int end = clamp_row(p.qsl[b + 1], p.T);
+            v.len = end > v.begin ? end - v.begin : 0;
+            v.n = segments_of(p, v.len);
+            if (v.n == 1) v.cls = min((int)((float)(p.cut - v.len) * per_class), kClasses - 1);
+            return v;
+        };
+        constexpr int kLong = kClasses / 2;  // classes of more than a segment's length
+        const int chunks = (p.batch + 63) / 64;
+        Lane v;
+        int cut = 0, longer = 0, whole[kClasses] = {};  // segments, long sequences, sequences of each class
+        for (int j = 0; j < chunks; ++j) {
+            v = lane_of(j);
+            if (__ballot(v.n > 1) != 0) cut += __builtin_amdgcn_readlane(wave_incl_scan(v.n > 1 ? v.n : 0), 63);
+            longer += __builtin_popcountll(__ballot(v.cls >= 0 && v.cls < kLong));
+            if (!CUT)
+#pragma unroll
+                for (int c = 0; c < kClasses; ++c) whole[c] += __builtin_popcountll(__ballot(v.cls == c));
+        }
+        w.number = CUT ? place + longer : place;
+        if (w.number >= p.places) return false;  // (where a wrong table lets sequences overlap)
+        const bool among_cut = w.number >= longer && w.number < longer + cut;
+        if (CUT && !among_cut) return false;
+        int rest = w.number, cls = -1;
+        if (among_cut) {
+            rest -= longer;
+        } else {
+            rest -= rest < longer ? 0 : cut;
+#pragma unroll
+            for (int c = 0; c < kClasses; ++c) {
+                if (cls < 0 && rest < whole[c]) cls = c;
+                if (cls < 0) rest -= whole[c];
+            }
+            if (cls < 0) return false;
+        }
+        for (int j = 0; j < chunks; ++j) {
+            if (chunks > 1) v = lane_of(j);
+            // pieces of this chunk's lanes up to each
+            const int mine = among_cut ? (v.n > 1 ? v.n : 0) : v.cls == cls ? 1 : 0;
+            const int upto = wave_incl_scan(mine), all = __builtin_amdgcn_readlane(upto, 63);
+            if (rest < all) {
+                const int at = __builtin_ctzll(__ballot(upto > rest));
+                w.q = Seq{j * 64 + at, __builtin_amdgcn_readlane(v.begin, at), __builtin_amdgcn_readlane(v.len, at)};
+                w.nseg = __builtin_amdgcn_readlane(v.n, at);
+                w.s = rest - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+                return true;
+            }
+            rest -= all;
+        }
+        return false;
     }
     if (!CUT) {
         const bool found = find_piece(p.qsl, p.batch, p.T, p.seg, place, w.q, w.s);

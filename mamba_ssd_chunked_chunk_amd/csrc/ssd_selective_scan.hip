@@ -317,6 +317,8 @@ void scan_shape(ScanParams &p, bool backward) {
     if (seg > kSegLimit) seg = kSegLimit;
     p.seg = (int)seg;
     p.cut = 2 * p.seg;
+    // (256 x 30 tokens 80 us with gaps, 107 without; 200 ragged prompts of 155 on average 305 and 245)
+    p.listed = p.batch <= 64 || (p.batch <= 256 && p.T / p.batch >= 128);
     p.places = p.T / seg + p.batch;
     p.cuts = std::min<int64_t>(p.T / ((int64_t)p.cut + 1), p.batch);
     p.cut_places = p.cuts > 0 ? p.T / seg + p.cuts : 0;

@@ -94,6 +94,21 @@ def test_prompt_long(lens, dtype):
     check_prompt(lens, 16, 2, 8, 601 + sum(lens), dtype=dtype, init="half", decay=0.01)
 
 
+def lens_of_many(n, seed):
+    """Ragged prompts of 128 tokens and more on average, whole and cut ones of every class of length, some empty."""
+    lens = [int(x) for x in torch.randint(0, 260, (n,), generator=torch.Generator().manual_seed(seed))]
+    for i, long in enumerate((1500, 700, 391, 385, 384, 383, 0, 0, 1, 1100)):
+        lens[i * (n // 10) + (3 if i % 2 else 0)] = long
+    return lens
+
+
+@pytest.mark.parametrize("n", [64, 65, 130, 256])
+def test_prompt_many_long_sequences(n):
+    lens = lens_of_many(n, 60 + n)
+    assert sum(lens) // n >= 128
+    check_prompt(lens, 8, 1, 8, 560 + n)
+
+
 def test_prompt_cut_among_many():
     lens = [int(x) for x in torch.randint(0, 30, (200,), generator=torch.Generator().manual_seed(3))]
     lens[0], lens[100], lens[199] = 700, 1100, 513
@@ -387,6 +402,13 @@ def test_backward_many_sequences():
     lens = [int(x) for x in torch.randint(0, 12, (300,), generator=torch.Generator().manual_seed(6))]
     lens[150] = 400
     check_backward(lens, 8, 1, 4, 1400, tail=3)
+
+
+@pytest.mark.parametrize("n", [64, 130, 256])
+def test_backward_many_long_sequences(n):
+    lens = lens_of_many(n, 80 + n)
+    assert sum(lens) // n >= 128
+    check_backward(lens, 8, 1, 4, 1420 + n, tail=3)
 
 
 def test_backward_of_wrong_tables_stays_inside():
