@@ -304,7 +304,7 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW, G> &lds, co
                 const int b = g * NW + wave;
                 Token m{lds.sx[i][lane], back ? lds.e[i][lane] : 0.f, lds.B[i][b], lds.C[i][b], make_float2(0.f, 0.f)};
                 if (g > 0 && back) m.share = lds.uq[wave][i][lane];
-                if (g > 0 && !back && gate) m.share.x = lds.y[wave][i][lane];
+                if (g > 0 && !back) m.share.x = lds.y[wave][i][lane];
                 return m;
             };
             float h[K][4], a[K][4];
@@ -313,7 +313,6 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW, G> &lds, co
             for (int i = 0; i < K; ++i) {
                 const Token m = next;
                 next = i < K - 1 ? read(i + 1, false) : read(K - 1, true);
-                __builtin_amdgcn_sched_barrier(0);
                 float y = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -321,15 +320,13 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW, G> &lds, co
                     h[i][j] = __builtin_fmaf(a[i][j], i > 0 ? h[i > 0 ? i - 1 : 0][j] : h0[j], m.v.y * m.B[j]);
                     y = j == 0 ? m.C[j] * h[i][j] : __builtin_fmaf(m.C[j], h[i][j], y);
                 }
-                if (gate) lds.y[wave][i][lane] = g > 0 ? y + m.share.x : y;
-                __builtin_amdgcn_sched_barrier(0);
+                lds.y[wave][i][lane] = g > 0 ? y + m.share.x : y;
             }
             float dAt[4] = {}, f[K][4];
 #pragma unroll
             for (int i = K - 1; i >= 0; --i) {
                 const Token m = next;
                 if (i > 0) next = read(i - 1, true);
-                __builtin_amdgcn_sched_barrier(0);
                 float uB = 0.f, qA = 0.f, forB[4], forC[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -354,7 +351,6 @@ __device__ __forceinline__ void grad(const ScanParams &p, Shared<NW, G> &lds, co
                     qA += m.share.y;
                 }
                 lds.uq[wave][i][lane] = make_float2(uB, qA);
-                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) dA[g][j] += dAt[j];
@@ -505,14 +501,15 @@ __global__ __launch_bounds__(kSumThreads) void scan_sums(ScanParams p, int64_t b
 // The wavefronts that hold N states, and the groups of 4 that each of them takes: one to 16 states, two above, which
 // share a tile's preparation and let two wavefronts a SIMD keep their registers (8 x 1024 tokens of 4096 channels with
 // one and two groups: 20 states 988 and 849 us, 32 states 1041 and 967; 64 states in 16 wavefronts, which had to spill,
-// 3976, in 8 1866).  A third of 4 wavefronts is left idle where 3 would do (12 states 610 -> 549 us: the rows of a tile
-// come out even), not two of 4 (8 states 611 us in 2, 535 in 4, but with 16 sequences 669 and 941).
+// 3976, in 8 1866).  One of 4 wavefronts is left idle where 3 would do (12 states 610 -> 549 us: the rows of a tile
+// come out even), not two of 4 (8 states 611 us in 2, 535 in 4, but with 16 sequences 669 and 941); one of 2 is, as a
+// wavefront alone would spill (4 states 505 us in 1, 508 in 2, with 16 sequences 825 and 627, with 32 1023 and 1140).
 template <typename F>
 void by_groups(int N, F f) {
     const std::integral_constant<int, 1> one;
     const std::integral_constant<int, 2> two;
     switch ((N + 3) / 4) {
-    case 1: return f(std::integral_constant<int, 1>{}, one);
+    case 1:
     case 2: return f(std::integral_constant<int, 2>{}, one);
     case 3:
     case 4: return f(std::integral_constant<int, 4>{}, one);

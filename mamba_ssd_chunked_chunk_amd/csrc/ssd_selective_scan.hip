@@ -206,7 +206,6 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
                     if (i + 1 < kTile) next = read(i + 1);
                     __builtin_amdgcn_sched_barrier(0);
                     token(i, m);
-                    __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
 #pragma unroll 1
