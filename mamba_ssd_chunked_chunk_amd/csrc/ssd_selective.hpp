@@ -80,10 +80,16 @@ __device__ __forceinline__ int segments_of(const ScanParams &p, int len) {
 // and a long one at the end all but one (backward pass of 65 ragged prompts of 186
 // tokens on average 632 -> 436 us).  Where that is not worth the search (`listed`)
 // they have the places of find_piece and cut_place, with gaps.
-constexpr int kClasses = 30;
+constexpr int kClasses = 14;
 template <bool CUT>
 __device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &w) {
     const int lane = threadIdx.x & 63;
+    if (p.batch == 1) {  // (300 tokens 27.4 -> 25.0 us)
+        w.q = seq_at(p.qsl, 0, p.T);
+        w.nseg = segments_of(p, w.q.len);
+        w.s = w.number = place;
+        return place < w.nseg && !(CUT && w.nseg == 1);
+    }
     if (p.listed) {
         struct Lane {
             int begin, len, n, cls;  // n: pieces, 0 behind the last sequence; cls: of a whole one, else -1
@@ -130,14 +136,23 @@ __device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &
         }
         for (int j = 0; j < chunks; ++j) {
             if (chunks > 1) v = lane_of(j);
-            // pieces of this chunk's lanes up to each
-            const int mine = among_cut ? (v.n > 1 ? v.n : 0) : v.cls == cls ? 1 : 0;
-            const int upto = wave_incl_scan(mine), all = __builtin_amdgcn_readlane(upto, 63);
+            // pieces of this chunk's lanes, and those ahead of each
+            int all, ahead;
+            const bool some = among_cut ? v.n > 1 : v.cls == cls;
+            if (among_cut) {
+                const int upto = wave_incl_scan(some ? v.n : 0);
+                all = __builtin_amdgcn_readlane(upto, 63);
+                ahead = upto - v.n;
+            } else {
+                const uint64_t m = __ballot(some);
+                all = __builtin_popcountll(m);
+                ahead = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+            }
             if (rest < all) {
-                const int at = __builtin_ctzll(__ballot(upto > rest));
+                const int at = __builtin_ctzll(__ballot(some && ahead <= rest && rest < ahead + v.n));
                 w.q = Seq{j * 64 + at, __builtin_amdgcn_readlane(v.begin, at), __builtin_amdgcn_readlane(v.len, at)};
                 w.nseg = __builtin_amdgcn_readlane(v.n, at);
-                w.s = rest - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+                w.s = rest - __builtin_amdgcn_readlane(ahead, at);
                 return true;
             }
             rest -= all;
