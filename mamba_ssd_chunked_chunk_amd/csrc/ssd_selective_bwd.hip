@@ -12,14 +12,14 @@
 // which adds what two lanes hold of half the values.  They leave as fp32 for each
 // 64 channels, and a last kernel adds the blocks of a group, in their order.
 //
-// 8 x 2048 tokens of 4096 channels and 16 states: states 230 us (of which the
-// 537 MB that they write 103), gradients 815, sums 33.  Arithmetic bounds the
-// gradients (0.87 vector instructions a cycle and compute unit): a token and state
+// 8 x 2048 tokens of 4096 channels and 16 states: states 212 us (of which the
+// 537 MB that they write 103), gradients 785, sums 33.  Arithmetic bounds the
+// gradients (0.88 vector instructions a cycle and compute unit): a token and state
 // costs its decay (an exponential and a product), 5 products, 6 fused adds and two
 // exchanges between lanes.
-// Tiles of 16 tokens would halve the states (213 us) but hold 64 more registers
-// a lane, and spill (gradients 944 us); three wavefronts a SIMD in 168 registers
-// leave the last workgroups alone on their units (989 us).
+// Tiles of 16 tokens would halve the states (226 -> 213 us) but hold 64 more
+// registers a lane, and spill (gradients 857 -> 944 us); three wavefronts a SIMD in
+// 168 registers leave the last workgroups alone on their units (857 -> 989 us).
 #include "ssd_selective.hpp"
 
 namespace ssd {
