@@ -44,14 +44,6 @@ __device__ __forceinline__ float time_step(const ScanParams &p, float raw) {
     return p.softplus ? softplus_fast(raw) : raw;
 }
 
-// 4 bf16 in two dwords
-struct Quad {
-    float v[4];
-};
-__device__ __forceinline__ Quad quad_of(uint32_t a, uint32_t b) {
-    return Quad{{bf16x2_lo(a), bf16x2_hi(a), bf16x2_lo(b), bf16x2_hi(b)}};
-}
-
 // First place of a cut sequence's segments among those of all cut sequences: at
 // most begin / (cut + 1) of them lie ahead of it, each with at most one partial
 // segment.
