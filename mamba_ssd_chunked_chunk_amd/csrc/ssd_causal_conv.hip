@@ -6,7 +6,7 @@
 // a sequence, which alone reads its state, writes the one that it leaves, so the
 // pool needs no second launch.
 //
-// Memory bounds it: 43898 tokens of 10240 channels, 1.80 GB, 362 us (5.0 TB/s); the
+// Memory bounds it: 43898 tokens of 10240 channels, 1.80 GB, 353 us (5.1 TB/s); the
 // backward pass of 4 x 4096 tokens of 1536 channels, 151 MB, 35 us (its arithmetic,
 // 30 operations an element with the silu's slope, takes about half of that), and 5
 // for the sum of the blocks' shares; a step of 512 sequences of 10240 channels, 84
@@ -94,7 +94,8 @@ __device__ __forceinline__ void load_window(const ConvParams &p, const Seq &q, i
     }
 }
 
-template <int W>
+// PAST: the outputs pass by the caches.
+template <int W, bool PAST>
 __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
     const int cblocks = (p.D + 511) / 512;
@@ -169,7 +170,12 @@ __global__ __launch_bounds__(256) void conv_fwd(ConvParams p) {
                 o[e] = p.silu ? a * sigmoid_f(a) : a;
             }
             y.hold();
-            if (t + i < t1) y.put(lo, narrow<E>(o));
+            if (t + i < t1) {
+                if constexpr (PAST)
+                    y.put_past(lo, narrow<E>(o));
+                else
+                    y.put(lo, narrow<E>(o));
+            }
             y.ptr += p.D;
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -420,7 +426,15 @@ int64_t conv_threads(const ConvParams &p) {
 
 hipError_t launch_conv(const ConvParams &p, int width, hipStream_t s) {
     const dim3 grid((unsigned)blocks_of(p.places * blocks_of(p.D, 512), 4));
-    return by_width(width, [&](auto w) { conv_fwd<decltype(w)::value><<<grid, 256, 0, s>>>(p); });
+    // outputs that the 256 MB cache would not hold for the next kernel pass by it (0.9 GB 364 -> 353 us)
+    const bool past = (int64_t)p.T * p.D * 2 > (int64_t)256 << 20;
+    return by_width(width, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        if (past)
+            conv_fwd<W, true><<<grid, 256, 0, s>>>(p);
+        else
+            conv_fwd<W, false><<<grid, 256, 0, s>>>(p);
+    });
 }
 hipError_t launch_conv_step(const ConvParams &p, int width, hipStream_t s) {
     return by_width(width, [&](auto w) {

@@ -64,6 +64,13 @@ struct Scalar {
         typedef __attribute__((address_space(1))) char *Bytes;
         *reinterpret_cast<__attribute__((address_space(1))) V *>(reinterpret_cast<Bytes>(ptr) + bytes) = v;
     }
+    // the same past the caches
+    template <typename V>
+    __device__ __forceinline__ void put_past(uint32_t bytes, const V &v) const {
+        typedef __attribute__((address_space(1))) char *Bytes;
+        __builtin_nontemporal_store(
+            v, reinterpret_cast<__attribute__((address_space(1))) V *>(reinterpret_cast<Bytes>(ptr) + bytes));
+    }
 };
 // ... and reads or writes at a lane's own offset from it, in bytes.
 template <typename V, typename T>
