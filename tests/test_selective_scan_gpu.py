@@ -311,6 +311,26 @@ def test_step_forms_and_padding(use, softplus):
     assert torch.equal(pool.cpu()[slots[4]], d["pool"][slots[4]])
 
 
+@pytest.mark.parametrize("N", [12, 16, 64])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step_of_slices(N, dtype):
+    """Rows of B and C at odd dwords, of x, dt and z inside wider ones: bit for bit the results of dense ones."""
+    B, D = 19, 72
+    d = L.scan_inputs([1] * B, D, 1, N, 835 + N, slots=B)
+    c = cuda(d)
+    xdz = torch.cat([c["x"], c["dt"], c["z"]], 1)
+    bc = torch.cat([torch.zeros(B, 10, dtype=BF16, device="cuda"), c["B"].view(B, N), c["C"].view(B, N)], 1)
+    sliced = dict(c, x=xdz[:, :D], dt=xdz[:, D:2 * D], z=xdz[:, 2 * D:], B=bc[:, 10:10 + N].unflatten(1, (1, N)),
+                  C=bc[:, 10 + N:].unflatten(1, (1, N)))
+    assert sliced["B"].data_ptr() % 8 == 4 and bc.stride(0) % 4 == 2
+    flags, outs = torch.ones(B, dtype=torch.uint8, device="cuda"), []
+    for s in (c, sliced):
+        pool, y = c["pool"].to(dtype, copy=True), torch.empty_like(c["x"])
+        binding.ssd_selective_scan_step_inplace(y, *inputs(s), pool, flags, c["cache_indices"])
+        outs.append((y, pool))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def test_steps_continue_a_prompt():
     D, N = 72, 16
     d = L.scan_inputs([40], D, 1, N, 840, slots=1)
