@@ -248,7 +248,9 @@ __device__ __forceinline__ void walk(const ScanParams &p, Shared<NW> &lds, const
     if (!mine) return;
     const f32x4 v = {h[0], h[1], h[2], h[3]};
     if (s < nseg - 1) {
-        *reinterpret_cast<f32x4 *>(p.parts + (first + s) * p.D * p.N + at) = v;
+        // What chain_states reads: the first segment's state, which holds what entered it, and the others' from zero.
+        // The later walk of those, from what entered them, leaves nothing: other workgroups of its launch read them.
+        if (STATES || s == 0) *reinterpret_cast<f32x4 *>(p.parts + (first + s) * p.D * p.N + at) = v;
         if (STATES && wave == 0) p.steps[(first + s) * p.D + ch] = steps;
     } else if (OUT) {
         if (p.state_bf16)
