@@ -326,7 +326,9 @@ void scan_shape(ScanParams &p, bool backward) {
 }
 
 int64_t scan_threads(const ScanParams &p, bool backward) {
-    const int64_t walk = p.places * p.blocks * 64 * waves_of(p.N);
+    // (the gradients' workgroups are the larger ones with 4 states, the walks' above 16)
+    const int waves = backward ? std::max(waves_of(p.N), grad_waves_of(p.N)) : waves_of(p.N);
+    const int64_t walk = p.places * p.blocks * 64 * waves;
     const int64_t sums = backward ? (int64_t)p.T * p.G * (p.N / 2) + 8 * ((int64_t)p.D * (p.N + 2)) + 1024 : 0;
     return walk > sums ? walk : sums;
 }
