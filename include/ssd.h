@@ -560,7 +560,10 @@ ssd_status ssd_rms_norm_bwd(const ssd_norm_problem *prob, void *dx, void *d_resi
  * The state of a sequence is its last width - 1 inputs, oldest first:
  * [width - 1, channels] in bf16, bit for bit the inputs.  query_start_loc,
  * has_initial_state, cache_indices, rows behind the last sequence and padding
- * entries as for linear attention.  Sums are fp32.                         */
+ * entries as for linear attention.  Sums are fp32.  No output may overlap an
+ * input, but where a state is said to be updated or to share a buffer; the
+ * prompt forms and the backward pass refuse y or dx among the rows of x, and
+ * dx in d_y (SSD_ERR_UNSUPPORTED).                                         */
 #define SSD_CONV_MAX_WIDTH 4
 typedef struct ssd_conv_problem {
     int64_t total_len;  /* rows of x and y; 0 .. 2^30 - 1                     */

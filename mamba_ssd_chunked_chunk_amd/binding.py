@@ -889,7 +889,7 @@ def ssd_causal_conv_varlen_fwd_inplace(y, x, weight, bias, pool, query_start_loc
     tokens that is a multiple of 8); weight fp32 [channels,width], width 2 to 4;
     bias fp32 [channels] or None; pool bf16 [S,width-1,channels];
     query_start_loc, has_initial_state and cache_indices as for
-    ssd_linear_attn_varlen_fwd_inplace.
+    ssd_linear_attn_varlen_fwd_inplace.  y may not overlap x.
     """
     batch, slots = query_start_loc.numel() - 1, pool.shape[0]
     prob, _, dev, state, inputs = _causal_conv(x, weight, bias, batch, slots, silu, False)

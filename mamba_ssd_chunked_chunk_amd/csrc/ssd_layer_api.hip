@@ -66,6 +66,12 @@ ConvParams common(const ssd_conv_problem *p) {
     a.max_slots = (uint32_t)p->batch;
     return a;
 }
+// Whether the dense rows [rows][width] at `a` share memory with as many of that width at `b`, `stride` elements apart
+bool rows_meet(const void *a, const void *b, int64_t rows, int64_t width, int64_t stride) {
+    const int64_t row = width * 2, step = stride * 2, begin = (int64_t)(uintptr_t)a - (int64_t)(uintptr_t)b;
+    const int64_t r = begin < row ? 0 : (begin - row) / step + 1;  // the first at b that ends behind a's begin
+    return r < rows && r * step < begin + rows * row;
+}
 bool fits(const ConvParams &a) { return a.places <= INT32_MAX && conv_threads(a) <= UINT32_MAX; }
 
 ssd_status conv_forward(const ssd_conv_problem *p, void *y, const void *x, const float *weight, const float *bias,
@@ -80,6 +86,8 @@ ssd_status conv_forward(const ssd_conv_problem *p, void *y, const void *x, const
     ConvParams a = common(p);
     conv_shape(a, p->width, false);
     if (!fits(a)) return SSD_ERR_UNSUPPORTED;
+    // a piece reads the rows ahead of it, which another workgroup writes in y
+    if (rows_meet(y, x, a.T, a.D, a.xs)) return SSD_ERR_UNSUPPORTED;
     a.y = static_cast<uint16_t *>(y);
     a.x = static_cast<const uint16_t *>(x);
     a.weight = weight;
@@ -310,6 +318,7 @@ ssd_status ssd_causal_conv_varlen_bwd(const ssd_conv_problem *prob, void *dx, fl
     if (!fits(a)) return SSD_ERR_UNSUPPORTED;
     const ssd_status sw = check_workspace(conv_workspace(a, prob->width), workspace, workspace_bytes);
     if (sw != SSD_OK) return sw;
+    if (rows_meet(dx, x, a.T, a.D, a.xs) || rows_meet(dx, d_y, a.T, a.D, a.D)) return SSD_ERR_UNSUPPORTED;
     a.x = static_cast<const uint16_t *>(x);
     a.weight = weight;
     a.bias = bias;
