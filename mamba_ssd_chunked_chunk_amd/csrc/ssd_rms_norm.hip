@@ -160,8 +160,10 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm(NormParams p) {
     if (live && t == 0) p.scales[row] = scale;
 }
 
-// Gradient: with u = w dy, d = s u - s^3 r mean(u r) + d_r.  Each row's team walks
-// over rows and keeps its share of sum s r dy in registers.
+// Gradient: with u = w dy, d = s u - s^3 r mean(u r) + d_r, formed as
+// s (u - (s r) (s mean(u r))), whose factors stay near u and 1 (s^3 alone leaves the
+// range of fp32 where r is above 2^43 or below 2^-43).  Each row's team walks over
+// rows and keeps its share of sum s r dy in registers.
 template <int TPR, int VPT>
 __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradParams p) {
     __shared__ float2 sums[2][16];
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
         }
         sum = row_sum<TPR>(sum, sums[n & 1]);
         const float s = 1.f / sqrtf(sum.x * share + p.eps);
-        const float k = s * s * s * (sum.y * share);
+        const float k = s * (sum.y * share);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int c = (t + v * TPR) * 8;
@@ -224,8 +226,9 @@ __global__ __launch_bounds__(Team<TPR>::kThreads) void rms_norm_grad(NormGradPar
             if (!kKeep) weight(v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dw[v][e] = __builtin_fmaf(s * r[v][e], u[v][e], dw[v][e]);
-                d[e] += s * (u[v][e] * w[v][e]) - k * r[v][e];
+                const float n = s * r[v][e];
+                dw[v][e] = __builtin_fmaf(n, u[v][e], dw[v][e]);
+                d[e] = __builtin_fmaf(s, __builtin_fmaf(-k, n, u[v][e] * w[v][e]), d[e]);
             }
             *reinterpret_cast<u32x4 *>(p.dx + at) = narrow8(d);
             if (p.d_res != nullptr) {
