@@ -1,5 +1,6 @@
-"""The norm's backward pass on the GPU for rows of extreme magnitude, against the
-definition in 64 bits within layer_testlib's bounds."""
+"""The norm's backward pass on the GPU for rows of extreme magnitude and for more
+wide rows than there are blocks, against the definition in 64 bits within
+layer_testlib's bounds."""
 
 import pytest
 
@@ -40,3 +41,12 @@ def test_rows_of_every_size(width, kind, given, power, eps):
     r, w, dy, dr = draw(5, width, kind, given, 100 + width)
     # the stream's own gradient of the order of the norm's, which goes with 1 / r
     check((r.float() * 2.0 ** power).to(kind), w, dy, None if dr is None else dr * 2.0 ** -power, eps)
+
+
+@pytest.mark.parametrize("width", [4104, 8200, 16392, 32768])
+@pytest.mark.parametrize("rows", [257, 513, 600])
+@pytest.mark.parametrize("kind,given", [(F32, False), (F32, True), (BF16, False), (BF16, True)])
+def test_wide_rows_in_several_turns(width, rows, kind, given):
+    """Above 4096 elements 256 blocks walk over the rows, one at a time: two and three turns, the last not whole."""
+    r, w, dy, dr = draw(rows, width, kind, given, 200 + width + rows)
+    check(r, w, dy, dr, 1e-5)
