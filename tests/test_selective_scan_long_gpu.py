@@ -197,3 +197,22 @@ def test_two_long_sequences_at_once():
         torch.cuda.synchronize()
         for a, b in zip(*outs):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("N", [4, 8, 12, 20, 32, 36, 64])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_cut_sequences_of_every_state_size(N, dtype):
+    """... whose workgroups have 1 to 16 wavefronts, and one or two groups of states a wavefront backwards."""
+    lens, D = [35, 900, 0, 450, 1, 500], 136
+    c = draw(lens, D, N, 170 + N, 2e-3, dtype)
+    check_forward(c, lens)
+    check_backward(c, lens)
+
+
+@pytest.mark.parametrize("N", [4, 12, 20, 32, 36, 64])
+@pytest.mark.parametrize("softplus", [True, False])
+def test_cut_sequences_of_groups(N, softplus):
+    """The same of two groups, random signs and decays that forget, against the recurrence token by token."""
+    from test_selective_scan_gpu import check_backward, check_prompt
+    check_prompt([300, 35, 0, 420], 144, 2, N, 180 + N, softplus=softplus)
+    check_backward([150, 35, 0, 200], 144, 2, N, 190 + N, softplus=softplus, tail=3)
