@@ -513,7 +513,8 @@ ssd_status ssd_state_dequantize(const ssd_state_cache_problem *prob, void *pool,
  * (r = x without a residual).  y is bf16, or 8 bits with one fp32 scale a row
  * by the rule of the parked states above (SSD_CODE_I8, SSD_CODE_E4M3), a row
  * of y in place of a row of a state.  Sums are fp32; r is rounded once, to the
- * residual's type, and y is the norm of what is stored.                    */
+ * residual's type, and y is the norm of what is stored.  No output may overlap
+ * an input, but where one buffer is said to do for both.                   */
 #define SSD_NORM_MAX_WIDTH 32768
 #define SSD_OUT_BF16 2  /* beside SSD_CODE_I8 and SSD_CODE_E4M3 */
 typedef struct ssd_norm_problem {
@@ -539,7 +540,8 @@ ssd_status ssd_rms_norm_fwd(const ssd_norm_problem *prob, void *y, float *scales
 ssd_status ssd_rms_norm_workspace_size(const ssd_norm_problem *prob, size_t *bytes);
 
 /* Backward pass, of y in bf16.  With r what the forward pass stored (x where
- * there was no residual), s = 1 / sqrt(mean(r^2) + eps), u = weight d_y:
+ * there was no residual), s = 1 / sqrt(mean(r^2) + eps), u = weight d_y (all
+ * tensors are dense: the problem's x_stride and out_format are not used):
  *     d = s u - s^3 r mean(u r) + d_r       dweight = sum over rows of s r d_y
  *   dx           OUT  bf16 [rows,width]: d
  *   d_residual   OUT  the residual's type [rows,width]: d, or NULL (dx serves
@@ -624,7 +626,8 @@ ssd_status ssd_causal_conv_step_inplace(
  * may have a stride between tokens (slices of projections); everything else is
  * dense.  Activations are bf16; A, D, dt_bias, the states and all sums are
  * fp32.  A is normally negative; powers of decays above 1 have to be finite in
- * fp32 over a whole sequence.  Results are deterministic (bitwise run to run). */
+ * fp32 over a whole sequence.  Results are deterministic (bitwise run to run).
+ * No output may overlap an input, but where states share a buffer.         */
 #define SSD_SELECTIVE_MAX_DSTATE 64
 typedef struct ssd_selective_problem {
     int64_t total_len;   /* rows of x, dt, z, B, C, y; 0 .. 2^30 - 1           */

@@ -7,10 +7,10 @@
 // pool needs no second launch.
 //
 // Memory bounds it: 43898 tokens of 10240 channels, 1.80 GB, 353 us (5.1 TB/s); the
-// backward pass of 4 x 4096 tokens of 1536 channels, 151 MB, 35 us (its arithmetic,
+// backward pass of 4 x 4096 tokens of 1536 channels, 151 MB, 36 us (its arithmetic,
 // 30 operations an element with the silu's slope, takes about half of that), and 5
 // for the sum of the blocks' shares; a step of 512 sequences of 10240 channels, 84
-// MB, 16 us.
+// MB, 17 us.
 #include "ssd_layer.hpp"
 
 namespace ssd {

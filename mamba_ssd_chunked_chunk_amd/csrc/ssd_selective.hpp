@@ -76,7 +76,7 @@ constexpr int kClasses = 14;
 template <bool CUT>
 __device__ __forceinline__ bool piece_at(const ScanParams &p, int place, Piece &w) {
     const int lane = threadIdx.x & 63;
-    if (p.batch == 1) {  // (300 tokens 27.4 -> 25.0 us)
+    if (p.batch == 1) {  // (300 tokens, with and without the search, 27.4 and 25.0 us)
         w.q = seq_at(p.qsl, 0, p.T);
         w.nseg = segments_of(p, w.q.len);
         w.s = w.number = place;

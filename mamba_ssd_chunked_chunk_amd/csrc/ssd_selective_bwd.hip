@@ -12,9 +12,9 @@
 // which adds what two lanes hold of half the values.  They leave as fp32 for each
 // 64 channels, and a last kernel adds the blocks of a group, in their order.
 //
-// 8 x 2048 tokens of 4096 channels and 16 states: states 212 us (of which the
-// 537 MB that they write 103), gradients 785, sums 33.  Arithmetic bounds the
-// gradients (0.88 vector instructions a cycle and compute unit): a token and state
+// 8 x 2048 tokens of 4096 channels and 16 states: states 215 us (of which the
+// 537 MB that they write 103), gradients 790, sums 34.  Arithmetic bounds the
+// gradients (0.89 vector instructions a cycle and compute unit): a token and state
 // costs its decay (an exponential and a product), 5 products, 6 fused adds and two
 // exchanges between lanes.
 // Tiles of 16 tokens would halve the states (226 -> 213 us) but hold 64 more

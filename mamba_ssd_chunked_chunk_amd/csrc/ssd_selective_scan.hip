@@ -1,12 +1,12 @@
 // Selective scan over ragged batches: h = exp(dts A) h + dts x B, y = C.h + D x,
 // gated by silu(z).  Every channel and state decays on its own, so there is no
 // matrix product in it: a token costs each (channel, state) an exponential, two
-// products and two fused adds, and this, not memory, is what bounds it: 11 ns for
-// the 64 channels of a wavefront on one SIMD, at which 8 x 2048 tokens of 4096
-// channels and 16 states take 180 us, while all a wavefront does is 33 instructions
-// a token, 20 of them for its states.  They take 300 us (1.1 vector instructions a
-// cycle and compute unit); 65536 tokens of 2048 channels, cut into 64 segments, which
-// all but doubles the work, 790 us.
+// products and two fused adds, and this, not memory, is what bounds it: 11 ns a
+// state and token for the 64 channels of a wavefront on one SIMD, at which 8 x 2048
+// tokens of 4096 channels and 16 states take 180 us, while all a wavefront does is 33
+// instructions a token, 20 of them for its states.  They take 293 us (1.1 vector
+// instructions a cycle and compute unit); 65536 tokens of 2048 channels, cut into 64
+// segments, which all but doubles the work, 804 us.
 //
 // A workgroup takes 64 channels of a sequence (or of one of its segments) and a
 // wavefront 4 states of them, a channel a lane.  What belongs to a token and
@@ -302,13 +302,13 @@ void scan_shape(ScanParams &p, bool backward) {
     p.Dg = p.D / p.G;
     p.blocks = p.G * ((p.Dg + 63) / 64);
     // Segments: long enough that a workgroup's chaining of those ahead of it stays below its walk (one sequence of 4096
-    // tokens and 2048 channels 88, 75, 80 us with 64, 128, 256 tokens), and that there are no more of them than
-    // balance the card: 8 wavefronts a SIMD (65536 tokens 820, 787, 848 us with 512, 1024, 2048), in the backward
-    // pass, which would repeat more work, 2 (one of 4096 tokens 282, 261, 280, 426 us with 64, 128, 256, 512).  Where
+    // tokens and 2048 channels 79, 68, 75 us with 64, 128, 256 tokens), and that there are no more of them than
+    // balance the card: 8 wavefronts a SIMD (65536 tokens 888, 855, 895 us with 512, 1024, 2048), in the backward
+    // pass, which would repeat more work, 2 (one of 4096 tokens 276, 250, 266, 407 us with 64, 128, 256, 512).  Where
     // the sequences alone come near 2 wavefronts a SIMD only those that stand out are cut (8 x 2048 tokens of 4096
-    // channels 300 us uncut, 372 in segments of 512, their backward pass 1084 and 1445; 32 ragged prompts of 1372 on
-    // average 891, 791, 795, 875 us with 512, 1024, 2048, 4096; with half as many wavefronts 16 x 1024 tokens of 4
-    // states 178 us uncut and 200 in segments of 256, 4 x 1024 tokens of 16 states 121 and 113 in segments of 128).
+    // channels 293 us uncut, 362 in segments of 512, their backward pass 1071 and 1433; 32 ragged prompts of 1372 on
+    // average 959, 865, 866, 939 us with 512, 1024, 2048, 4096; with half as many wavefronts 16 x 1024 tokens of 4
+    // states 172 us uncut and 187 in segments of 256, 4 x 1024 tokens of 16 states 125 and 113 in segments of 128).
     const int64_t waves = (int64_t)p.blocks * (backward ? grad_waves_of(p.N) : waves_of(p.N));
     const int64_t resident = 2048;
     int64_t seg = std::max<int64_t>(backward ? 32 : 64, (int64_t)((backward ? 1.0 : 1.5) * sqrt((double)p.T)));
